@@ -18,7 +18,8 @@ from ._build import LIB, build
 __all__ = ["load", "spec_verify", "spec_verify_noalloc", "spec_verify_workspace_bytes",
            "spec_truncated_probs", "NOALLOC_SCRATCH_BYTES",
            "spec_sample", "spec_philox_uniforms", "spec_lm_head_logits", "spec_verify_from_hidden",
-           "spec_verify_greedy_from_hidden", "sv_version", "Workspace", "SV_BF16", "SV_F32", "SpecVerifyError"]
+           "spec_verify_greedy_from_hidden", "spec_token_logprobs", "spec_token_logprobs_backward",
+           "TokenLogprobs", "sv_version", "Workspace", "SV_BF16", "SV_F32", "SpecVerifyError"]
 
 SV_BF16, SV_F32 = 0, 1
 _STATUS = {0: "ok", 1: "null pointer", 2: "shape", 3: "dtype", 4: "workspace", 5: "cuda",
@@ -67,6 +68,12 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.spec_verify_from_hidden.restype = i32
     lib.spec_verify_greedy_from_hidden.argtypes = [vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, vp, sz, vp]
     lib.spec_verify_greedy_from_hidden.restype = i32
+    i64, f32 = ctypes.c_longlong, ctypes.c_float
+    lib.spec_token_logprobs.argtypes = [vp, i32, i32, i32, i64, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.spec_token_logprobs.restype = i32
+    lib.spec_token_logprobs_backward.argtypes = [vp, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, i32, vp, vp,
+                                                 vp, i64, vp]
+    lib.spec_token_logprobs_backward.restype = i32
     lib.sv_status_string.argtypes = [i32]
     lib.sv_status_string.restype = ctypes.c_char_p
     lib.sv_version.argtypes = []
@@ -358,3 +365,6 @@ def spec_verify_greedy_from_hidden(hidden_target: torch.Tensor, weight: torch.Te
         workspace.buf.data_ptr(), workspace.nbytes, _stream(stream))
     _check(st, "spec_verify_greedy_from_hidden")
     return out_tokens, out_n, flag
+
+
+from .logprobs import TokenLogprobs, spec_token_logprobs, spec_token_logprobs_backward  # noqa: E402

@@ -1,0 +1,55 @@
+"""Where a call runs: its device and stream, and the pointers handed to the library."""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+
+def ptr(t: torch.Tensor, name: str, dtype, device) -> int:
+    """Device address of a contiguous tensor of this type on this device."""
+    from . import SpecVerifyError
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise SpecVerifyError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise SpecVerifyError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise SpecVerifyError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise SpecVerifyError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+class _Here:
+    """The device's current stream on the current device: nothing to set or restore."""
+
+    def __init__(self, handle):
+        self.handle = handle
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        return False
+
+
+@contextlib.contextmanager
+def _there(device, stream, tensors):
+    with torch.cuda.device(device):
+        s = torch.cuda.current_stream() if stream is None else stream
+        # Outputs made inside come from this stream's memory, and the caching
+        # allocator learns that the inputs are in use on it.
+        with torch.cuda.stream(s):
+            if stream is not None:
+                for t in tensors:
+                    if isinstance(t, torch.Tensor) and t.is_cuda:
+                        t.record_stream(s)
+            yield int(s.cuda_stream)
+
+
+def on_device(device, stream, *tensors):
+    """Context in which outputs are allocated and the call is made; gives the stream's
+    handle. The caller orders `stream` after the work that produces the tensors."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _Here(int(torch.cuda.current_stream().cuda_stream))
+    return _there(device, stream, tensors)
