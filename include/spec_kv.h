@@ -72,6 +72,37 @@ sv_status spec_kv_append(const void* k, long long k_stride, const void* v, long 
                          int max_pages, int num_pages, int page_size, int q_heads, int kv_heads, int head_dim,
                          void* k_codes, float* k_scale, void* v_codes, float* v_scale, int32_t* flag, void* stream);
 
+/* Bytes of device workspace that spec_kv_attention needs for these arguments on the
+ * current device; 0 for arguments outside the limits. The workspace need not be
+ * cleared and holds nothing between calls; calls that may run at the same time must
+ * not share one. */
+size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int kv_heads, int head_dim);
+
+/* Attention of the window's queries over the cache. With a = scale * q . k, query
+ * i of sequence b (position seq_len[b] + i) sees the keys at positions p with
+ * p <= seq_len[b] + i and, when window > 0, p > seq_len[b] + i - window, that lie on
+ * mapped pages:
+ *   lse = ln sum_p exp(a_p),  out = sum_p exp(a_p - lse) v_p
+ * A query that sees nothing gets out = 0 and lse = -inf. What the cache holds past
+ * a sequence's last new token is never looked at.
+ *   q      [N][q_heads][head_dim] bf16, token stride q_stride elements (heads
+ *          adjacent; rows 16-byte aligned)
+ *   out    [N][q_heads][head_dim] bf16, contiguous, 16-byte aligned (written)
+ *   lse    [N][q_heads] float (written) or NULL
+ *   scale  a finite factor, usually head_dim^-1/2; window >= 0 (0: no limit)
+ *   workspace: 16-byte aligned, spec_kv_attention_workspace_bytes() bytes
+ * Products are formed from queries and weights in fp16 (queries scaled by a power of
+ * two for each row, so their 8 significant bits are kept; weights to 11 bits) and
+ * codes as they are, all sums in fp32. Repeated calls give the same bits.
+ * Returns SV_ERR_NULL, SV_ERR_SHAPE, SV_ERR_ALIGN or SV_ERR_WORKSPACE before
+ * launching, SV_ERR_CUDA when a launch fails. */
+sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_codes, const float* k_scale,
+                            const void* v_codes, const float* v_scale, const int32_t* seq_len,
+                            const int32_t* cu_tokens, const int32_t* page_table, int B, int N, int max_tokens,
+                            int max_pages, int num_pages, int page_size, int q_heads, int kv_heads, int head_dim,
+                            float scale, int window, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

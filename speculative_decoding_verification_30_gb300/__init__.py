@@ -19,7 +19,8 @@ __all__ = ["load", "spec_verify", "spec_verify_noalloc", "spec_verify_workspace_
            "spec_truncated_probs", "NOALLOC_SCRATCH_BYTES",
            "spec_sample", "spec_philox_uniforms", "spec_lm_head_logits", "spec_verify_from_hidden",
            "spec_verify_greedy_from_hidden", "spec_token_logprobs", "spec_token_logprobs_backward",
-           "TokenLogprobs", "KVCache", "rope_tables", "spec_kv_append", "sv_version", "Workspace", "SV_BF16", "SV_F32", "SpecVerifyError"]
+           "TokenLogprobs", "KVCache", "rope_tables", "spec_kv_append",
+           "spec_kv_attention", "spec_kv_attention_workspace_bytes", "sv_version", "Workspace", "SV_BF16", "SV_F32", "SpecVerifyError"]
 
 SV_BF16, SV_F32 = 0, 1
 _STATUS = {0: "ok", 1: "null pointer", 2: "shape", 3: "dtype", 4: "workspace", 5: "cuda",
@@ -77,6 +78,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.spec_kv_append.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp,
                                    *[i32] * 9, vp, vp, vp, vp, vp, vp]
     lib.spec_kv_append.restype = i32
+    lib.spec_kv_attention_workspace_bytes.argtypes = [i32] * 5
+    lib.spec_kv_attention_workspace_bytes.restype = sz
+    lib.spec_kv_attention.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, *[i32] * 9, f32, i32, vp, vp, vp, sz, vp]
+    lib.spec_kv_attention.restype = i32
     lib.sv_status_string.argtypes = [i32]
     lib.sv_status_string.restype = ctypes.c_char_p
     lib.sv_version.argtypes = []
@@ -370,5 +375,6 @@ def spec_verify_greedy_from_hidden(hidden_target: torch.Tensor, weight: torch.Te
     return out_tokens, out_n, flag
 
 
-from .kv import KVCache, rope_tables, spec_kv_append  # noqa: E402
+from .kv import (KVCache, rope_tables, spec_kv_append, spec_kv_attention,  # noqa: E402
+                 spec_kv_attention_workspace_bytes)
 from .logprobs import TokenLogprobs, spec_token_logprobs, spec_token_logprobs_backward  # noqa: E402

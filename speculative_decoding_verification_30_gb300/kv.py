@@ -1,7 +1,8 @@
 """The target model's paged 8-bit key/value cache around the verify step: appending a
-window of tokens (include/spec_kv.h)."""
+window of tokens, and the attention of the window over it (include/spec_kv.h)."""
 from __future__ import annotations
 
+import math
 from typing import NamedTuple
 
 import torch
@@ -117,3 +118,48 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
                                    max_tokens, max_pages, pages, page, qh, heads, dim, *cache, fp, st)
     _check(rc, "spec_kv_append")
     return q_out
+
+
+def spec_kv_attention_workspace_bytes(B: int, max_tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace of spec_kv_attention on the current device."""
+    return int(load().spec_kv_attention_workspace_bytes(B, max_tokens, q_heads, kv_heads, head_dim))
+
+
+def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_tokens: torch.Tensor,
+                      page_table: torch.Tensor, max_tokens: int, scale: float | None = None, window: int = 0,
+                      out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """Attention of a window's queries q [N, q_heads, head_dim] (bf16) over the cache: query i
+    of sequence b, at position seq_len[b] + i, sees the keys up to its own position (the window
+    must have been appended) and, with window > 0, only the last `window` of them. Returns
+    (out [N, q_heads, head_dim] bf16, lse [N, q_heads] float32).
+
+    scale defaults to head_dim^-1/2. workspace: uint8, at least
+    spec_kv_attention_workspace_bytes(...) bytes, not shared by calls that may overlap."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise SpecVerifyError("q must be a CUDA tensor")
+    dev = q.device
+    cache, (pages, heads, page, dim) = _cache(kv, dev)
+    win, B, max_pages = _window(seq_len, cu_tokens, page_table, dev)
+    qp, qs, qh = _heads(q, "q", torch.bfloat16, dev, dim)
+    N = q.shape[0]
+    if scale is None:
+        scale = 1.0 / math.sqrt(dim)
+    with on_device(dev, stream, q, *kv, seq_len, cu_tokens, page_table, out, lse, workspace) as st:
+        need = spec_kv_attention_workspace_bytes(B, max_tokens, qh, heads, dim)
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        if out is None:
+            out = torch.empty(N, qh, dim, dtype=torch.bfloat16, device=dev)
+        elif out.shape != (N, qh, dim):
+            raise SpecVerifyError("out must be [N, q_heads, head_dim]")
+        if lse is None:
+            lse = torch.empty(N, qh, dtype=torch.float32, device=dev)
+        elif lse.shape != (N, qh):
+            raise SpecVerifyError("lse must be [N, q_heads]")
+        rc = load().spec_kv_attention(qp, qs, *cache, *win, B, N, max_tokens, max_pages, pages, page, qh, heads, dim,
+                                      float(scale), window, ptr(out, "out", torch.bfloat16, dev),
+                                      ptr(lse, "lse", torch.float32, dev),
+                                      ptr(workspace, "workspace", torch.uint8, dev), workspace.numel(), st)
+    _check(rc, "spec_kv_attention")
+    return out, lse

@@ -82,3 +82,25 @@ def test_binding_rejects_bad_tensors():
     i = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(sv.SpecVerifyError, match="CUDA tensor"):
         sv.spec_kv_append(k, k, cache, i, torch.zeros(2, dtype=torch.int32), i[None], 1)
+
+
+def attend(q=A, qs=512, kc=A, ks=A, vc=A, vs=A, sl=A, cu=A, pt=A, B=2, N=8, mt=4, maxp=4, np_=16, page=16, qh=4, kh=2, D=128,
+           scale=0.1, win=0, out=A, lse=None, ws=A, wsb=1 << 30):
+    return sv.load().spec_kv_attention(q, qs, kc, ks, vc, vs, sl, cu, pt, B, N, mt, maxp, np_, page, qh, kh, D, scale, win, out, lse,
+                                       ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), 1), (dict(kc=None), 1), (dict(vs=None), 1), (dict(out=None), 1), (dict(ws=None), 1), (dict(cu=None), 1),
+    (dict(B=0), 2), (dict(B=65536), 2), (dict(mt=9), 2), (dict(page=8), 2), (dict(D=256), 2), (dict(qh=5), 2), (dict(qs=511), 2),
+    (dict(win=-1), 2), (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2), (dict(np_=1 << 28), 2),
+    (dict(B=65535, N=1 << 24, mt=1 << 24), 2),
+    (dict(q=A + 8), 6), (dict(qs=516), 6), (dict(out=A + 4), 6), (dict(ks=A + 2), 6), (dict(lse=A + 1), 6),
+    (dict(ws=A + 8), 4)])
+def test_attention_checks_its_arguments(kw, status):
+    assert attend(**kw) == status
+
+
+def test_workspace_sizes_outside_the_limits_are_zero():
+    f = sv.spec_kv_attention_workspace_bytes
+    assert f(0, 1, 8, 8, 64) == 0 and f(1, 0, 8, 8, 64) == 0 and f(1, 1, 9, 8, 64) == 0 and f(1, 1, 8, 8, 80) == 0
