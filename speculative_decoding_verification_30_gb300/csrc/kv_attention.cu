@@ -3,21 +3,23 @@
 //
 // A window has few query rows (new tokens x query heads of a kv head) and reads the
 // whole cache once, so the bound is HBM: 2 head_dim bytes for each cached token and
-// kv head. The work is cut into units of 32 cached tokens of one item = (sequence,
-// kv head, tile of up to 8 NT query rows), and every warp takes an equal share of
-// all units, whatever the sequences' lengths: it streams its units through a ring of
-// shared-memory stages of its own (cp.async; nothing waits on another warp) and
-// keeps a softmax of its own. An item that lies within one warp's share is written
-// out; the others leave (max, sum, weighted values) in the workspace for
-// kv_combine_kernel.
+// kv head. The work is cut into units of 64 cached tokens of one item = (sequence,
+// kv head, tile of up to 8 NT query rows), and every block takes an equal share of
+// all units, whatever the sequences' lengths. A fifth warp walks the share and copies
+// its units into a ring of shared-memory stages (cp.async, zeros for what is not
+// there), handing each over at a block barrier. An item that lies within one block's
+// share is written out; the others leave (max, sum, weighted values) in the workspace
+// for kv_combine_kernel.
 //
-// Per unit the products are transposed, S^T = K Q^T and O^T += V^T P^T, so that the
-// cached tokens (and head_dim) fill the 16-row side of the matrix instruction and
-// the query rows only its 8-column side: 20 rows cost 24 and not 32. e4m3 codes are
-// converted to fp16 in registers, which is exact. Both contractions may take their
-// index in any order, so each lane loads 16 neighbouring bytes and calls them
-// whatever the fragment wants; the value scale of a page enters through the exponent
-// (weight 2^(s + log2 scale - m)) and the key scale through the logit.
+// Both products are transposed, S^T = K Q^T and O^T += V^T P^T, so that the cached
+// tokens (and head_dim) fill the 16-row side of the matrix instruction and the query
+// rows only its 8-column side: 20 rows cost 24 and not 32. The four warps split the
+// unit's tokens for the first product and head_dim for the second: every code is
+// widened to fp16 once (exact), and a warp accumulates only a quarter of the output,
+// which leaves registers for three or four blocks on an SM. Both contractions may
+// take their index in any order, so each lane loads neighbouring bytes and calls
+// them whatever the fragment wants. The value scale of a page enters through the
+// exponent (weight 2^(s + log2 scale - m)) and the key scale through the logit.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -29,14 +31,15 @@
 
 namespace svkv {
 
-constexpr int TOK = 32;        // cached tokens of a unit
-constexpr int WARPS = 8;
-constexpr int MAX_NT = 4;      // query rows of an item: 8 NT
-constexpr int MIN_UNITS = 2;   // a warp takes at least this many
+constexpr int TOK = 64;        // cached tokens of a unit
+constexpr int NWARP = 4, NTHR = 32 * NWARP;   // computing; one warp more copies
+constexpr int MAX_NT = 8;      // query rows of an item: 8 NT
+constexpr int OVERHEAD = 1;    // what an item costs besides its tokens, in units
 // Weights are 2^(t - m) with m = LIFT below the running maximum of the exponents t,
 // and m moves only when a weight would exceed 2^TOP: they stay within fp16 (65504)
 // and the small ones keep as much of its range as there is.
 constexpr float LIFT = 7.f, TOP = 15.f;
+constexpr float NO_FRAME = -1e30f;   // m of a row that has seen nothing (finite: -inf - m stays -inf)
 constexpr float LN2F = 0.693147180559945309f, LOG2EF = 1.44269504088896341f;
 
 struct AttnArgs {
@@ -54,25 +57,43 @@ struct AttnArgs {
   int workers;
 };
 
-struct Meta {          // of a stage
-  int b, h, rt, tile;  // unit: 32 tokens from 32 tile of (b, h, rt)
-  int first, last;     // of the warp's share of the item
-  int slot;            // of the workspace, if the share is a part of the item
-  int pad;
-  float ks[2], vs[2];  // scales of the two halves of 16 tokens
+constexpr int FIRST = 1, LAST = 2, WHOLE = 4, MASKED = 8, END = 16;
+struct Meta {                  // of a stage: 64 tokens from 64 tile of item (b, h, rt)
+  float4 run[4];               // of each 16 tokens: key scale, log2 and reciprocal of the value scale
+  int flags;                   // FIRST, LAST of the block's share of the item; WHOLE: that is all of it;
+                               // MASKED: some row does not see all tokens; END: no unit
+  int tok0, row0, count;       // position of the first token; as in Seq: first, count
+  long long len;
+  int h, rt, slot, pad;        // slot of the workspace, if the share is not whole
+  int pad2[2];
 };
+static_assert(sizeof(Meta) % 16 == 0, "stages stay 16-byte aligned");
 
 template <int D>
 struct Stage {
   uint8_t k[TOK * D], v[TOK * D];
   Meta m;
 };
-static_assert(sizeof(Meta) % 16 == 0, "stages stay 16-byte aligned");
-template <int D>
-constexpr int stages() { return D == 128 ? 3 : 6; }
+// Blocks on an SM, and stages so that they fit its shared memory.
+template <int D, int NT>
+struct Shape {
+  static constexpr int BLOCKS = NT <= 2 ? 4 : NT <= 4 ? 3 : 2;
+  static constexpr bool QREG = NT <= 3;                  // query fragments in registers
+  static constexpr int PSTRIDE = 16 * (NT | 1);          // bytes of a token's weights: odd multiples of 16 spread the banks
+  // the queries' and the weights' buffers are one where the queries move on to registers
+  static constexpr int QBYTES = 8 * NT * D * 2, PBYTES = TOK * PSTRIDE, PAT = QREG ? 0 : QBYTES;
+  static constexpr int BUF = QREG ? (QBYTES > PBYTES ? QBYTES : PBYTES) : QBYTES + PBYTES;
+  static constexpr int FIXED = BUF + 8 * NT * 4 * (1 + NWARP);
+  static constexpr int ROOM = (227 * 1024) / BLOCKS - 1024 - 512 - FIXED;
+  static constexpr int FIT = ROOM / (int)sizeof(Stage<D>);
+  static constexpr int NS = FIT > 6 ? 6 : FIT;
+  static constexpr size_t SMEM = sizeof(Stage<D>) * NS + FIXED;
+  static_assert(NS >= 3, "three stages at least");
+};
 
-// Units of sequence b: kv_heads * row tiles * token tiles (at least one tile, so
-// that every row is written).
+// Units of sequence b: kv_heads * row tiles * (OVERHEAD + token tiles), at least one
+// tile, so that every row is written. The OVERHEAD units of an item come first and
+// hold no tokens: they only even out the shares.
 struct Span {
   int tile0, tiles, rts;
 };
@@ -92,7 +113,7 @@ __device__ __forceinline__ Span span(const AttnArgs& A, const Seq& s) {
 template <int NT>
 __device__ __forceinline__ long long units_of(const AttnArgs& A, int b) {
   const Span p = span<NT>(A, sequence(A.w, b));
-  return (long long)A.w.kv_heads * p.rts * p.tiles;
+  return (long long)A.w.kv_heads * p.rts * (p.tiles + OVERHEAD);
 }
 
 __device__ __forceinline__ long long share_start(long long w, long long units, long long workers) {
@@ -129,14 +150,40 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
-  return r;
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t* r, uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm2_trans(uint32_t* r, uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+               : "=r"(r[0]), "=r"(r[1])
+               : "r"(at)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void bar(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool bar_any(int id, int threads, bool x) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((int)x)
+      : "memory");
+  return r != 0;
 }
 
 // Byte offset of 16-byte chunk c of token t in a stage's tile: chunks are permuted by
@@ -146,27 +193,37 @@ __device__ __forceinline__ int chunk_at(int t, int c) {
   return D == 128 ? t * 128 + ((c ^ (t & 7)) << 4) : t * 64 + ((c ^ ((t >> 1) & 3)) << 4);
 }
 
+// The weights of run t as the value product wants them.
+template <int NT>
+__device__ __forceinline__ void load_weights(uint32_t (&pf)[NT][2], const unsigned char* sp, int t, int lane) {
+  constexpr int PS = 16 * (NT | 1);
+#pragma unroll
+  for (int n = 0; n + 1 < NT; n += 2)
+    ldsm4_trans(&pf[n][0], smem_u32(sp + (16 * t + (lane & 15)) * PS + (n + (lane >> 4)) * 16));
+  if (NT & 1) ldsm2_trans(&pf[NT - 1][0], smem_u32(sp + (16 * t + (lane & 15)) * PS + (NT - 1) * 16));
+}
+
 // The value product of 16 tokens one token at a time, each added only to the rows
 // that see it (rare: only where a masked unit holds NaN values). Works on copies, so
 // that the caller's accumulators stay in registers.
-template <int D, int NT>
+template <int DT, int NT>
 struct ByToken {
-  float o[D / 16][NT][4];
-  uint32_t v[4][D / 32], pf[NT][2];
+  float o[DT][NT][4];
+  uint32_t v[4], pf[NT][2];
   uint32_t seen[NT][2];   // bit k: the thread's row (n, e) sees token k
 };
-template <int D, int NT>
-__device__ __noinline__ void add_by_token(ByToken<D, NT>& x, int q) {
+template <int DT, int NT>
+__device__ __noinline__ void add_by_token(ByToken<DT, NT>& x, int q) {
 #pragma unroll 1
   for (int k = 0; k < 16; ++k) {
     const bool mine = q == (k & 7) >> 1;
     const int slot = (k & 1) + 2 * (k >> 3);
-#pragma unroll 1
-    for (int j = 0; j < D / 16; ++j) {
-      const uint32_t pick = j & 1 ? 0x7362u : 0x5140u;
+#pragma unroll
+    for (int j = 0; j < DT; ++j) {
+      const uint32_t pick = j ? 0x7362u : 0x5140u;
       uint32_t a0, a1, a2, a3, y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = mine && i == slot ? x.v[i][j >> 1] : 0u;
+      for (int i = 0; i < 4; ++i) y[i] = mine && i == slot ? x.v[i] : 0u;
       widen(__byte_perm(y[0], y[1], pick), a0, a1);
       widen(__byte_perm(y[2], y[3], pick), a2, a3);
 #pragma unroll
@@ -185,34 +242,41 @@ __device__ __noinline__ void add_by_token(ByToken<D, NT>& x, int q) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(WARPS * 32, 1) kv_attention_kernel(const AttnArgs A) {
-  constexpr int NS = stages<D>();
+__global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attention_kernel(const AttnArgs A) {
+  using Sh = Shape<D, NT>;
+  constexpr int NS = Sh::NS;
   constexpr int KW = D / 16;       // words (4 codes) of a token in a lane = steps of the key product
-  constexpr int DT = D / 16;       // 16-row tiles of head_dim in the value product
-  constexpr int VW = D / 32;       // words of a token's values in a lane
-  constexpr int ROWS = 8 * NT;
+  constexpr int DT = D / 64;       // 16-row tiles of head_dim in a warp's value product
+  constexpr int ROWS = 8 * NT, PS = Sh::PSTRIDE;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long s_sum[WARPS], s_start_pre[WARPS];
-  __shared__ int s_start_b[WARPS];
+  Stage<D>* ring = reinterpret_cast<Stage<D>*>(smem);
+  unsigned char* sq = smem + sizeof(Stage<D>) * NS;                     // queries, fp16, in fragment order
+  unsigned char* sp = sq + Sh::PAT;                                     // weights, fp16 [token][row]
+  float* srs = reinterpret_cast<float*>(sq + Sh::BUF);                  // logit factor of each row
+  float* swm = srs + ROWS;                                              // [warp][row]: maxima, later sums
+  __shared__ long long s_sum[NWARP + 1], s_pre;
+  __shared__ int s_b;
   const Window& w = A.w;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int G = w.q_heads / w.kv_heads;
 
-  // --- shares: total units, then the sequence in which each warp's share begins
+  // --- shares: total units, then the sequence in which this block's share begins
+  constexpr int ALL = NTHR + 32;
   long long mine = 0;
-  for (int b = tid; b < w.B; b += WARPS * 32) mine += units_of<NT>(A, b);
+  for (int b = tid; b < w.B; b += ALL) mine += units_of<NT>(A, b);
 #pragma unroll
   for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) s_sum[warp] = mine;
-  if (tid < WARPS) s_start_b[tid] = -1;
+  if (tid == 0) s_b = -1;
   __syncthreads();
   long long units = 0;
 #pragma unroll
-  for (int i = 0; i < WARPS; ++i) units += s_sum[i];
-  const long long workers = min((long long)A.workers, max(units / MIN_UNITS, 1ll));
-  __syncthreads();
+  for (int i = 0; i <= NWARP; ++i) units += s_sum[i];
+  const long long workers = min((long long)A.workers, max(units, 1ll));
+  const long long wk = blockIdx.x;
+  const long long u0 = share_start(wk, units, workers), u1 = wk < workers ? share_start(wk + 1, units, workers) : u0;
   long long before = 0;
-  for (int b0 = 0; b0 < w.B; b0 += WARPS * 32) {
+  for (int b0 = 0; b0 < w.B; b0 += ALL) {
     const int b = b0 + tid;
     const long long u = b < w.B ? units_of<NT>(A, b) : 0;
     long long inc = u;
@@ -221,128 +285,159 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_attention_kernel(const AttnA
       const long long v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
+    __syncthreads();   // the last values have been read
     if (lane == 31) s_sum[warp] = inc;
     __syncthreads();
     long long pre = before;
     for (int i = 0; i < warp; ++i) pre += s_sum[i];
-    for (int i = 0; i < WARPS; ++i) before += s_sum[i];
+    for (int i = 0; i <= NWARP; ++i) before += s_sum[i];
     pre += inc - u;
-    for (int i = 0; i < WARPS; ++i) {
-      const long long wk = (long long)blockIdx.x * WARPS + i;
-      if (wk < workers) {
-        const long long at = share_start(wk, units, workers);
-        if (u > 0 && at >= pre && at < pre + u) {
-          s_start_b[i] = b;
-          s_start_pre[i] = pre;
-        }
-      }
+    if (u > 0 && u0 >= pre && u0 < pre + u) {
+      s_b = b;
+      s_pre = pre;
     }
     if (blockIdx.x == 0 && b < w.B) A.prefix[b] = pre;
-    __syncthreads();
   }
   if (blockIdx.x == 0 && tid == 0) {
     A.prefix[w.B] = units;
     A.prefix[w.B + 1] = workers;
   }
-  const long long wk = (long long)blockIdx.x * WARPS + warp;
-  int cb = s_start_b[warp];
-  if (wk >= workers || cb < 0) return;
-  const long long u0 = share_start(wk, units, workers), u1 = share_start(wk + 1, units, workers);
-  Stage<D>* ring = reinterpret_cast<Stage<D>*>(smem) + warp * NS;
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (u0 >= u1 || s_b < 0) return;
 
-  // --- cursor of the copies: unit `cu` is tile `ct` of item (cb, ch, cr)
-  long long cu = u0;
-  Seq cs = sequence(w, cb);
-  Span cp = span<NT>(A, cs);
-  int ct, ch, cr;
-  {
-    const long long x = u0 - s_start_pre[warp];
-    const long long item = x / cp.tiles;
-    ct = (int)(x % cp.tiles);
-    ch = (int)(item / cp.rts);
-    cr = (int)(item % cp.rts);
-  }
-  const auto issue = [&](int stage) {
-    if (cu < u1) {
+  if (warp == NWARP) {
+    // --- the copying warp. Unit `cu` is number `ct` of item (cb, ch, cr)
+    int cb = s_b;
+    long long cu = u0;
+    Seq cs = sequence(w, cb);
+    Span cp = span<NT>(A, cs);
+    int ct, ch, cr;
+    {
+      const long long x = u0 - s_pre;
+      const int per = cp.tiles + OVERHEAD;
+      const long long item = x / per;
+      ct = (int)(x % per);
+      ch = (int)(item / cp.rts);
+      cr = (int)(item % cp.rts);
+    }
+    // entries window0 .. window0 + 31 of the sequence's row of the page table and those
+    // pages' scales, one in each lane
+    int entry = -1, window_b = -1, window_h = -1, window0 = 0;
+    float eks = 0.f, elv = 0.f, einv = 0.f;
+    const int P = w.page_size, shift = __ffs(P) - 1;
+    constexpr int CH = D / 16;            // chunks of a token
+    constexpr int RPI = 32 / CH;          // tokens copied at once: 4 or 8
+    const int c = lane % CH, t0 = lane / CH;
+    const auto issue = [&](int stage) {
       Stage<D>& S = ring[stage];
-      const int tile = cp.tile0 + ct;
-      const int left = (int)min((long long)cp.tiles - ct, u1 - cu);   // units to the end of the share of this item
-      const long long end = cs.len < 0 ? 0 : cs.len + cs.count;
-      constexpr int CH = D / 16;            // chunks of a token
-      constexpr int RPI = 32 / CH;          // tokens a warp copies at once
-      const int c = lane % CH;
-      int page[2];
+      if (ct < OVERHEAD) {
+        cu += OVERHEAD - ct;
+        ct = OVERHEAD;
+      }
+      const bool on = cu < u1;
+      if (!on) {
+        if (lane == 0) S.m.flags = END;
+      } else {
+        const int tok0 = (cp.tile0 + ct - OVERHEAD) * TOK;     // below 2^27
+        const int live = cs.len < 0 ? 0 : (int)min(cs.len + cs.count - tok0, (long long)TOK);
+        const int j0 = tok0 >> shift, j1 = (tok0 + TOK - 1) >> shift;
+        if (cb != window_b || j0 < window0 || j1 >= window0 + 32) {
+          window_b = cb;
+          window_h = -1;
+          window0 = j0;
+          entry = page_of(w, cb, (long long)j0 + lane);
+        }
+        if (ch != window_h) {
+          window_h = ch;
+          const size_t at = (size_t)max(entry, 0) * w.kv_heads + ch;
+          const float vs = entry < 0 ? 1.f : A.v_scale[at];
+          eks = entry < 0 ? 1.f : A.k_scale[at];
+          elv = log2f(vs);
+          einv = __frcp_rn(vs);
+        }
+        bool gap = false;
+        const uint32_t kd = smem_u32(S.k), vd = smem_u32(S.v);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) page[i] = page_of(w, cb, ((long long)tile * TOK + 16 * i) / w.page_size);
+        for (int run = 0; run < TOK / 16; ++run) {
+          const int at = tok0 + 16 * run, from = (at >> shift) - window0;
+          const int page = __shfl_sync(0xffffffffu, entry, from);
+          const float ks = __shfl_sync(0xffffffffu, eks, from), lv = __shfl_sync(0xffffffffu, elv, from),
+                      inv = __shfl_sync(0xffffffffu, einv, from);
+          if (lane == 0) S.m.run[run] = make_float4(ks, lv, inv, page < 0 ? 1.f : 0.f);
+          gap |= page < 0;
+          const size_t off = ((((size_t)max(page, 0) * w.kv_heads + ch) << shift) + (at & (P - 1)) + t0) * D + c * 16;
+          const uint8_t *kp = A.k_codes + off, *vp = A.v_codes + off;
+          const int n = (page < 0 ? 0 : live) - 16 * run - t0;
 #pragma unroll
-      for (int i = 0; i < TOK / RPI; ++i) {
-        const int t = i * RPI + lane / CH;
-        const long long pos = (long long)tile * TOK + t;
-        const int pg = page[t >> 4];
-        const bool on = pg >= 0 && pos < end;
-        const size_t off = (((size_t)(on ? pg : 0) * w.kv_heads + ch) * w.page_size + (size_t)(pos % w.page_size)) * D + c * 16;
-        copy16(smem_u32(S.k + chunk_at<D>(t, c)), A.k_codes + off, on);
-        copy16(smem_u32(S.v + chunk_at<D>(t, c)), A.v_codes + off, on);
-      }
-      if (lane < 4) {
-        const int i = lane & 1;
-        const int pg = i ? page[1] : page[0];
-        const size_t off = (size_t)max(pg, 0) * w.kv_heads + ch;
-        copy4(smem_u32(lane < 2 ? &S.m.ks[i] : &S.m.vs[i]), (lane < 2 ? A.k_scale : A.v_scale) + off, pg >= 0);
-      }
-      if (lane == 0) {
-        S.m.b = cb;
-        S.m.h = ch;
-        S.m.rt = cr;
-        S.m.tile = tile;
-        S.m.first = ct == 0 || cu == u0;
-        S.m.last = left == 1;
-        S.m.slot = cu - u0 < (long long)ct + 1 ? 0 : 1;
-      }
-      ++cu;
-      if (++ct == cp.tiles) {
-        ct = 0;
-        if (++cr == cp.rts) {
-          cr = 0;
-          if (++ch == w.kv_heads) {
-            ch = 0;
-            if (cu < u1) {
-              do {
-                cs = sequence(w, ++cb);
-                cp = span<NT>(A, cs);
-              } while (cp.rts == 0 && cb + 1 < w.B);
+          for (int i = 0; i < 16 / RPI; ++i) {
+            const uint32_t d = (uint32_t)chunk_at<D>(16 * run + i * RPI + t0, c);
+            copy16(kd + d, kp + i * RPI * D, i * RPI < n);
+            copy16(vd + d, vp + i * RPI * D, i * RPI < n);
+          }
+        }
+        if (lane == 0) {
+          const long long item0 = cu - ct, item1 = item0 + OVERHEAD + cp.tiles;
+          const bool masked = gap || cs.len < 0 || tok0 + TOK - 1 > cs.len ||
+                              (A.window && tok0 <= cs.len + cs.count - 1 - A.window);
+          S.m.flags = (ct == OVERHEAD || cu == u0 ? FIRST : 0) | (cu + 1 == item1 || cu + 1 == u1 ? LAST : 0) |
+                      (u0 <= item0 + OVERHEAD && u1 >= item1 ? WHOLE : 0) | (masked ? MASKED : 0);
+          S.m.tok0 = tok0;
+          S.m.row0 = cs.first;
+          S.m.count = cs.count;
+          S.m.len = cs.len;
+          S.m.h = ch;
+          S.m.rt = cr;
+          S.m.slot = u0 < item0 ? 1 : 0;
+        }
+        ++cu;
+        if (++ct == cp.tiles + OVERHEAD) {
+          ct = 0;
+          if (++cr == cp.rts) {
+            cr = 0;
+            if (++ch == w.kv_heads) {
+              ch = 0;
+              if (cu < u1) {
+                do {
+                  cs = sequence(w, ++cb);
+                  cp = span<NT>(A, cs);
+                } while (cp.rts == 0 && cb + 1 < w.B);
+              }
             }
           }
         }
       }
+      copies_commit();
+      return on;
+    };
+    int ahead = 0;               // units copied or on their way, not yet handed over
+#pragma unroll 1
+    for (int i = 0; i < NS - 1; ++i) ahead += issue(i);
+    for (int stage = 0;; stage = stage + 1 == NS ? 0 : stage + 1) {
+      copies_wait<NS - 2>();
+      bar(1, ALL);               // the unit is there, and the one before it is done with
+      if (ahead == 0) return;    // that was the END
+      ahead += issue(stage == 0 ? NS - 1 : stage - 1) - 1;
     }
-    copies_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < NS - 1; ++i) issue(i);
+  }
 
-  uint32_t qf[NT][2 * KW];     // query fragments
-  float rs[NT][2];             // logit factor of the thread's rows 8 n + 2 q + {0, 1}
-  float m[NT][2], l[NT][2], o[DT][NT][4];
-  int stage = 0, begin = 0;    // begin: the tile at which the share of the item began
-  Seq s{};
-  for (long long u = u0; u < u1; ++u) {
-    copies_wait<NS - 2>();
-    __syncwarp();
-    issue(stage == 0 ? NS - 1 : stage - 1);
+  uint32_t qf[Sh::QREG ? NT : 1][2 * KW];   // query fragments
+  float m[NT][2], l[NT][2], o[DT][NT][4];   // of rows 8 n + 2 q + {0, 1}
+  for (int stage = 0;; stage = stage + 1 == NS ? 0 : stage + 1) {
+    bar(1, ALL);
     const Stage<D>& S = ring[stage];
     const Meta& M = S.m;
-    const int row0 = M.rt * ROWS;
-    if (M.first) {
-      begin = M.tile;
-      s = sequence(w, M.b);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        // the lane's row is 8 n + g, its D / 4 elements from q D / 4
-        const int row = row0 + 8 * n + g, i = row / G, hd = M.h * G + row % G;
+    const int flags = M.flags;
+    if (flags & END) return;
+    if (flags & FIRST) {
+      // Queries: four threads to a row, each D / 4 elements; scaled by a power of two
+      // so that the row's largest element lies in [2^7, 2^8)
+#pragma unroll 1
+      for (int r = tid >> 2; r < ROWS; r += NTHR / 4) {
+        const int row = M.rt * ROWS + r, i = row / G, hd = M.h * G + row % G;
         uint32_t x[D / 8];
-        if (i < s.count) {
-          const uint4* p = reinterpret_cast<const uint4*>(A.q + (size_t)(s.first + i) * (size_t)A.q_stride + (size_t)hd * D + q * (D / 4));
+        if (i < M.count) {
+          const uint4* p = reinterpret_cast<const uint4*>(A.q + (size_t)(M.row0 + i) * (size_t)A.q_stride + (size_t)hd * D + q * (D / 4));
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
             const uint4 v = p[k];
@@ -352,7 +447,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_attention_kernel(const AttnA
 #pragma unroll
           for (int k = 0; k < D / 8; ++k) x[k] = 0u;
         }
-        // scaled by a power of two so that the row's largest element lies in [2^7, 2^8)
         uint32_t top = 0u;
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
@@ -360,17 +454,27 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_attention_kernel(const AttnA
           if (a < 0x7F800000u) top = max(top, a);
           if (b < 0x7F800000u) top = max(top, b);
         }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const unsigned four = 0xFu << (lane & ~3);
+        top = max(top, __shfl_xor_sync(four, top, 1));
+        top = max(top, __shfl_xor_sync(four, top, 2));
         const int e = top ? min(max((int)(top >> 23) - 127 - 7, -100), 119) : 0;   // 2^e times [2^7, 2^8)
         const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+        // word k of lane q (elements q D / 4 + 2 k, + 1) goes to pair q of 16-byte segment k
 #pragma unroll
         for (int k = 0; k < D / 8; ++k)
-          qf[n][k] = pack_h2(__uint_as_float(x[k] << 16) * down, __uint_as_float(x[k] & 0xFFFF0000u) * down);
-        const float f = up * A.scale;
-        rs[n][0] = __shfl_sync(0xffffffffu, f, 8 * q);
-        rs[n][1] = __shfl_sync(0xffffffffu, f, 8 * q + 4);
-        m[n][0] = m[n][1] = -INFINITY;
+          *reinterpret_cast<uint32_t*>(sq + r * (D * 2) + ((k ^ (r & 7)) << 4) + q * 4) =
+              pack_h2(__uint_as_float(x[k] << 16) * down, __uint_as_float(x[k] & 0xFFFF0000u) * down);
+        if (q == 0) srs[r] = up * A.scale;
+      }
+      bar(2, NTHR);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (Sh::QREG) {
+#pragma unroll
+          for (int k = 0; k < KW / 2; ++k)
+            ldsm4(&qf[n][4 * k], smem_u32(sq + (8 * n + (lane & 7)) * (D * 2) + (((4 * k + (lane >> 3)) ^ (lane & 7)) << 4)));
+        }
+        m[n][0] = m[n][1] = NO_FRAME;
         l[n][0] = l[n][1] = 0.f;
 #pragma unroll
         for (int j = 0; j < DT; ++j)
@@ -379,12 +483,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_attention_kernel(const AttnA
       }
     }
 
-    // --- logits: sc[t][n] holds tokens 16 t + g (+ 8), rows 8 n + 2 q (+ 1)
-    float sc[2][NT][4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    // --- logits of the warp's 16 tokens: sc[n] holds tokens g and g + 8, rows 8 n + 2 q (+ 1)
+    float sc[NT][4];
+    {
       uint32_t ka[KW], kb[KW];
-      const int ta = 16 * t + g;
+      const int ta = 16 * warp + g;
       if (D == 128) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -402,70 +505,81 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_attention_kernel(const AttnA
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sc[t][n][k] = 0.f;
+        for (int k = 0; k < 4; ++k) sc[n][k] = 0.f;
 #pragma unroll
-      for (int k = 0; k < KW; ++k) {
-        uint32_t a0, a1, a2, a3;
-        widen(ka[k], a0, a2);
-        widen(kb[k], a1, a3);
+      for (int k2 = 0; k2 < KW / 2; ++k2) {
+        uint32_t a[2][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816(sc[t][n], a0, a1, a2, a3, qf[n][2 * k], qf[n][2 * k + 1]);
+        for (int k = 0; k < 2; ++k) {
+          widen(ka[2 * k2 + k], a[k][0], a[k][2]);
+          widen(kb[2 * k2 + k], a[k][1], a[k][3]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint32_t f[4];
+          if (Sh::QREG) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[k] = qf[Sh::QREG ? n : 0][4 * k2 + k];
+          } else {
+            ldsm4(f, smem_u32(sq + (8 * n + (lane & 7)) * (D * 2) + (((4 * k2 + (lane >> 3)) ^ (lane & 7)) << 4)));
+          }
+          mma16816(sc[n], a[0][0], a[0][1], a[0][2], a[0][3], f[0], f[1]);
+          mma16816(sc[n], a[1][0], a[1][1], a[1][2], a[1][3], f[2], f[3]);
+        }
       }
     }
 
     // --- weights. A token's exponent is its logit (base 2) plus log2 of its value scale
-    const int tok0 = M.tile * TOK;
-    float inv[2];
-    bool gap = false;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const float ks = M.ks[t], vs = M.vs[t], lv = log2f(vs);
-      inv[t] = vs > 0.f ? __frcp_rn(vs) : 0.f;
-      gap |= vs == 0.f;     // an unmapped page (its copies were zeros)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc[t][n][k] = fmaf(sc[t][n][k], rs[n][k & 1] * ks, lv);
-    }
-    const long long first_pos = s.len;    // the earliest query's position
-    const bool masked = gap || s.len < 0 || tok0 + TOK - 1 > first_pos ||
-                        (A.window && tok0 <= s.len + s.count - 1 - A.window);
+    const float4 run = M.run[warp];
+    const float inv = run.z;
     // whether the thread's row e of tile n sees position p
     const auto sees = [&](int n, int e, int p) {
-      const long long pos = s.len + (row0 + 8 * n + 2 * q + e) / G;
-      return s.len >= 0 && p <= pos && !(A.window && p <= pos - A.window) && inv[((p - tok0) >> 4) & 1] != 0.f;
+      const long long pos = M.len + (M.rt * ROWS + 8 * n + 2 * q + e) / G;
+      return M.len >= 0 && p <= pos && !(A.window && p <= pos - A.window);
     };
-    if (masked) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float2 rs = *reinterpret_cast<const float2*>(srs + 8 * n + 2 * q);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sc[n][k] = fmaf(sc[n][k], (k & 1 ? rs.y : rs.x) * run.x, run.y);
+    }
+    if (flags & MASKED) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              if (!sees(n, e, tok0 + 16 * t + g + 8 * k)) sc[t][n][2 * k + e] = -INFINITY;
+        for (int k = 0; k < 4; ++k)   // run.w: an unmapped page
+          if (run.w != 0.f || !sees(n, k & 1, M.tok0 + 16 * warp + g + 8 * (k >> 1))) sc[n][k] = -INFINITY;
     }
-    bool over = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float top = fmaxf(fmaxf(sc[0][n][e], sc[0][n][2 + e]), fmaxf(sc[1][n][e], sc[1][n][2 + e]));
-        over |= top > m[n][e] + TOP;
+        top = fmaxf(top, fmaxf(sc[n][e], sc[n][2 + e]) - m[n][e]);
       }
-    if (__any_sync(0xffffffffu, over)) {
+    if (bar_any(2, NTHR, top > TOP)) {
+      // some weight would leave its range: move every row's frame to its maximum
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float top = fmaxf(fmaxf(sc[0][n][e], sc[0][n][2 + e]), fmaxf(sc[1][n][e], sc[1][n][2 + e]));
+          float t = fmaxf(sc[n][e], sc[n][2 + e]);
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          top -= LIFT;
-          if (top > m[n][e]) {
-            const float f = ex2f(m[n][e] - top);   // 0 the first time
-            m[n][e] = top;
+          for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+          if (g == 0) swm[warp * ROWS + 8 * n + 2 * q + e] = t;
+        }
+      bar(2, NTHR);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t = swm[8 * n + 2 * q + e];
+#pragma unroll
+          for (int i = 1; i < NWARP; ++i) t = fmaxf(t, swm[i * ROWS + 8 * n + 2 * q + e]);
+          t -= LIFT;
+          if (t > m[n][e]) {
+            const float f = ex2f(m[n][e] - t);   // 0 the first time
+            m[n][e] = t;
             l[n][e] *= f;
 #pragma unroll
             for (int j = 0; j < DT; ++j) {
@@ -475,176 +589,215 @@ __global__ void __launch_bounds__(WARPS * 32, 1) kv_attention_kernel(const AttnA
           }
         }
     }
-    uint32_t pf[2][NT][2];
+    // the warp's value words, ahead of the barrier: word i of run t is of token 16 t + 2 q + {0, 1, 8, 9}
+    uint32_t v[TOK / 16][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float p0 = ex2f(sc[t][n][2 * k] - m0), p1 = ex2f(sc[t][n][2 * k + 1] - m1);
-          l[n][0] = fmaf(p0, inv[t], l[n][0]);
-          l[n][1] = fmaf(p1, inv[t], l[n][1]);
-          pf[t][n][k] = transpose8(pack_h2(p0, p1));
-        }
-    }
-
-    // --- values: o[j][n] holds head_dim (D / 8) g + 2 j + {0: k < 2, 1: k >= 2}, rows 8 n + 2 q + (k & 1)
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      uint32_t v[4][VW];
+    for (int t = 0; t < TOK / 16; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tk = 16 * t + 2 * q + (i & 1) + 8 * (i >> 1);
-        if (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(S.v + chunk_at<D>(tk, g));
-          v[i][0] = x.x, v[i][1 % VW] = x.y, v[i][2 % VW] = x.z, v[i][3 % VW] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(S.v + chunk_at<D>(tk, g >> 1) + 8 * (g & 1));
-          v[i][0] = x.x, v[i][1] = x.y;
-        }
-      }
-      if (masked) {
-        // NaN values of tokens that only some rows see: 0 * NaN must not reach the others
-        bool nan = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int x = 0; x < VW; ++x) nan |= (((v[i][x] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
-        if (__any_sync(0xffffffffu, nan)) {
-          ByToken<D, NT> x;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              x.pf[n][e] = pf[t][n][e];
-              x.seen[n][e] = 0u;
-#pragma unroll 1
-              for (int k = 0; k < 16; ++k) x.seen[n][e] |= (uint32_t)sees(n, e, tok0 + 16 * t + k) << k;
-            }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int y = 0; y < VW; ++y) x.v[i][y] = v[i][y];
-#pragma unroll
-          for (int j = 0; j < DT; ++j)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) x.o[j][n][k] = o[j][n][k];
-          add_by_token<D, NT>(x, q);
-#pragma unroll
-          for (int j = 0; j < DT; ++j)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[j][n][k] = x.o[j][n][k];
-          continue;
-        }
+        if (D == 128)
+          v[t][i] = *reinterpret_cast<const uint32_t*>(S.v + chunk_at<D>(tk, 2 * warp + (g >> 2)) + 4 * (g & 3));
+        else
+          v[t][i] = *reinterpret_cast<const uint16_t*>(S.v + chunk_at<D>(tk, warp) + 2 * g);
       }
 #pragma unroll
-      for (int j = 0; j < DT; ++j) {
-        const uint32_t pick = j & 1 ? 0x7362u : 0x5140u;   // bytes 2, 3 or 0, 1 of two neighbouring tokens, interleaved
-        uint32_t a0, a1, a2, a3;
-        widen(__byte_perm(v[0][j >> 1], v[1][j >> 1], pick), a0, a1);
-        widen(__byte_perm(v[2][j >> 1], v[3][j >> 1], pick), a2, a3);
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816(o[j][n], a0, a1, a2, a3, pf[t][n][0], pf[t][n][1]);
+      for (int k = 0; k < 2; ++k) {
+        const float p0 = ex2f(sc[n][2 * k] - m[n][0]), p1 = ex2f(sc[n][2 * k + 1] - m[n][1]);
+        l[n][0] = fmaf(p0, inv, l[n][0]);
+        l[n][1] = fmaf(p1, inv, l[n][1]);
+        *reinterpret_cast<uint32_t*>(sp + (16 * warp + g + 8 * k) * PS + n * 16 + q * 4) = pack_h2(p0, p1);
       }
     }
+    bool by_token = false;
+    if (flags & MASKED) {
+      // NaN values of tokens that only some rows see: 0 * NaN must not reach the others
+      bool nan = false;
+#pragma unroll
+      for (int t = 0; t < TOK / 16; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) nan |= (((v[t][i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
+      by_token = __any_sync(0xffffffffu, nan);
+    }
+    bar(2, NTHR);
 
-    if (M.last) {
-      const Span p = span<NT>(A, s);
-      const bool whole = begin == p.tile0 && M.tile == p.tile0 + p.tiles - 1;
+    // --- values: o[j][n] holds head_dim (D / 4) warp + (D / 32) g + 2 j + {0: k < 2, 1: k >= 2}
+    if (__builtin_expect(!by_token, 1)) {
+#pragma unroll
+      for (int t = 0; t < TOK / 16; ++t) {
+        uint32_t pf[NT][2];
+        load_weights<NT>(pf, sp, t, lane);
+#pragma unroll
+        for (int j = 0; j < DT; ++j) {
+          const uint32_t pick = j ? 0x7362u : 0x5140u;   // bytes 2, 3 or 0, 1 of two neighbouring tokens, interleaved
+          uint32_t a0, a1, a2, a3;
+          widen(__byte_perm(v[t][0], v[t][1], pick), a0, a1);
+          widen(__byte_perm(v[t][2], v[t][3], pick), a2, a3);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(o[j][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+        }
+      }
+    } else {
+      ByToken<DT, NT> x;
+#pragma unroll
+      for (int j = 0; j < DT; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x.o[j][n][k] = o[j][n][k];
+#pragma unroll
+      for (int t = 0; t < TOK / 16; ++t) {
+        load_weights<NT>(x.pf, sp, t, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.v[i] = v[t][i];
+        for (int n = 0; n < NT; ++n)
+          for (int e = 0; e < 2; ++e) {
+            x.seen[n][e] = 0u;
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) x.seen[n][e] |= (uint32_t)sees(n, e, M.tok0 + 16 * t + k) << k;
+          }
+        add_by_token<DT, NT>(x, q);
+      }
+#pragma unroll
+      for (int j = 0; j < DT; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[j][n][k] = x.o[j][n][k];
+    }
+
+    if (flags & LAST) {
+      // the warps' sums of the weights (fixed order), then the rows
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
-          const int r = 8 * n + 2 * q + e, row = row0 + r, i = row / G;
-          if (i >= s.count) continue;
-          const int hd = M.h * G + row % G;
-          const size_t at = (size_t)(s.first + i) * w.q_heads + hd;
-          if (whole) {
-            const float f = l[n][e] == 0.f ? 0.f : 1.f / l[n][e];
-            uint32_t y[D / 16];
+          if (g == 0) swm[warp * ROWS + 8 * n + 2 * q + e] = l[n][e];
+        }
+      bar(2, NTHR);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * n + 2 * q + e, row = M.rt * ROWS + r, i = row / G;
+          float sum = swm[r];
+#pragma unroll
+          for (int k = 1; k < NWARP; ++k) sum += swm[k * ROWS + r];
+          if (i >= M.count) continue;
+          const int d0 = (D / 4) * warp + (D / 32) * g;
+          if (flags & WHOLE) {
+            const size_t at = (size_t)(M.row0 + i) * w.q_heads + M.h * G + row % G;
+            const float f = sum == 0.f ? 0.f : 1.f / sum;
+            uint32_t y[DT];
 #pragma unroll
             for (int j = 0; j < DT; ++j) {
               const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[j][n][e] * f, o[j][n][2 + e] * f);
               y[j] = *reinterpret_cast<const uint32_t*>(&b2);
             }
-            uint4* dst = reinterpret_cast<uint4*>(A.out + at * D + g * (D / 8));
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) dst[j] = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-            if (A.lse && g == 0) A.lse[at] = LN2F * (m[n][e] + log2f(l[n][e]));
+            for (int j = 0; j < DT; ++j) *reinterpret_cast<uint32_t*>(A.out + at * D + d0 + 2 * j) = y[j];
+            if (A.lse && warp == 0 && g == 0) A.lse[at] = LN2F * (m[n][e] + log2f(sum));
           } else {
             float* slot = A.part + ((size_t)wk * 2 + M.slot) * ROWS * (D + 2);
-            if (g == 0) {
+            if (warp == 0 && g == 0) {
               slot[2 * r] = m[n][e];
-              slot[2 * r + 1] = l[n][e];
+              slot[2 * r + 1] = sum;
             }
-            float4* dst = reinterpret_cast<float4*>(slot + 2 * ROWS + r * D + g * (D / 8));
 #pragma unroll
-            for (int j = 0; j < DT / 2; ++j)
-              dst[j] = make_float4(o[2 * j][n][e], o[2 * j][n][2 + e], o[2 * j + 1][n][e], o[2 * j + 1][n][2 + e]);
+            for (int j = 0; j < DT; ++j)
+              *reinterpret_cast<float2*>(slot + 2 * ROWS + r * D + d0 + 2 * j) = make_float2(o[j][n][e], o[j][n][2 + e]);
           }
         }
     }
-    stage = stage + 1 == NS ? 0 : stage + 1;
   }
 }
 
-// Joins the shares of the items that several warps worked on: a block takes the
-// query heads of one (token, kv head).
-constexpr int CT = 128;
+// Joins the shares of the items that several blocks worked on: a warp takes one query
+// row. It gathers the shares' frames and sums a lane each, then adds the weighted
+// values, D / 32 elements a lane, in the shares' order.
+constexpr int CW = 4;   // warps of a block
 template <int D, int NT>
-__global__ void __launch_bounds__(CT) kv_combine_kernel(const AttnArgs A) {
-  constexpr int ROWS = 8 * NT, SUB = CT / D;   // rows a block works on at once
+__global__ void __launch_bounds__(CW * 32) kv_combine_kernel(const AttnArgs A) {
+  constexpr int ROWS = 8 * NT, E = D / 32;
+  // first of all, in every thread: this grid ends only after the one before it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Window& w = A.w;
-  const int G = w.q_heads / w.kv_heads;
-  long long blk = blockIdx.x;
-  const int h = (int)(blk % w.kv_heads);
-  blk /= w.kv_heads;
-  const int i = (int)(blk % w.max_tokens), b = (int)(blk / w.max_tokens);
+  const int lane = threadIdx.x & 31, G = w.q_heads / w.kv_heads;
+  const long long id = (long long)blockIdx.x * CW + (threadIdx.x >> 5);
+  const int qh = (int)(id % w.q_heads);
+  const long long bi = id / w.q_heads;
+  const int i = (int)(bi % w.max_tokens);
+  if (bi / w.max_tokens >= w.B) return;
+  const int b = (int)(bi / w.max_tokens), h = qh / G;
   const Seq s = sequence(w, b);
   if (i >= s.count) return;
   const Span p = span<NT>(A, s);
   const long long units = A.prefix[w.B], workers = A.prefix[w.B + 1], pre = A.prefix[b];
-  const int d = threadIdx.x % D;
-  for (int gq = threadIdx.x / D; gq < G; gq += SUB) {
-    const int row = i * G + gq, rt = row / ROWS, r = row % ROWS;
-    const long long i0 = pre + ((long long)h * p.rts + rt) * p.tiles, i1 = i0 + p.tiles;
-    const long long w0 = ((i0 + 1) * workers - 1) / units, w1 = (i1 * workers - 1) / units;
-    if (w0 == w1) continue;   // written already
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (long long k = w0; k <= w1; ++k) {
-      const float* slot = A.part + ((size_t)k * 2 + (share_start(k, units, workers) < i0 ? 1 : 0)) * ROWS * (D + 2);
-      const float mk = slot[2 * r], lk = slot[2 * r + 1], ok = slot[2 * ROWS + r * D + d];
-      const float top = fmaxf(m, mk);
-      if (top > -INFINITY) {
-        const float f = ex2f(m - top), fk = ex2f(mk - top);
-        l = fmaf(lk, fk, l * f);
-        o = fmaf(ok, fk, o * f);
-        m = top;
-      } else if (lk != lk) {
-        l = lk;
+  const int row = i * G + qh % G, rt = row / ROWS, r = row % ROWS;
+  const long long i0 = pre + ((long long)h * p.rts + rt) * (p.tiles + OVERHEAD), i1 = i0 + OVERHEAD + p.tiles;
+  // the blocks that hold its first and its last unit with tokens
+  const long long w0 = ((i0 + OVERHEAD + 1) * workers - 1) / units, w1 = (i1 * workers - 1) / units;
+  if (w0 == w1) return;   // written already
+  const auto slot = [&](long long k) {
+    return A.part + ((size_t)k * 2 + (share_start(k, units, workers) < i0 ? 1 : 0)) * ROWS * (D + 2);
+  };
+  float m = NO_FRAME, l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (long long k0 = w0; k0 <= w1; k0 += 32) {
+    const int n = (int)min(w1 - k0 + 1, 32ll);
+    float mk = NO_FRAME, lk = 0.f;
+    const float* at = nullptr;
+    if (lane < n) {
+      at = slot(k0 + lane);
+      mk = at[2 * r], lk = at[2 * r + 1];
+    }
+    float top = fmaxf(m, mk);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float f = ex2f(m - top), fk = ex2f(mk - top);
+    float sum = lk * fk;
+#pragma unroll
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    l = fmaf(l, f, sum);
+    m = top;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), k));
+      const float fs = __shfl_sync(0xffffffffu, fk, k);
+      src += 2 * ROWS + r * D + lane * E;
+      if (E == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(src);
+        o[0] = fmaf(y.x, fs, o[0]), o[1 % E] = fmaf(y.y, fs, o[1 % E]);
+        o[2 % E] = fmaf(y.z, fs, o[2 % E]), o[3 % E] = fmaf(y.w, fs, o[3 % E]);
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(src);
+        o[0] = fmaf(y.x, fs, o[0]), o[1] = fmaf(y.y, fs, o[1]);
       }
     }
-    const size_t at = (size_t)(s.first + i) * w.q_heads + h * G + gq;
-    A.out[at * D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
-    if (A.lse && d == 0) A.lse[at] = LN2F * (m + log2f(l));
   }
+  const size_t at = (size_t)(s.first + i) * w.q_heads + qh;
+  const float f = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(A.out + at * D + lane * E + e) = __floats2bfloat162_rn(o[e] * f, o[e + 1] * f);
+  if (A.lse && lane == 0) A.lse[at] = LN2F * (m + log2f(l));
 }
 
 static sv::LaunchCache g_attn_cache;
 
-// Row tiles of an item: just enough for the window, at most MAX_NT.
+// Tiles of 8 rows of an item: just enough for the window, at most MAX_NT.
 static int row_tiles(int max_tokens, int group) {
-  const long long rows = (long long)max_tokens * group;
-  return rows >= 8 * MAX_NT ? MAX_NT : (int)((rows + 7) / 8);
+  const long long nt = ((long long)max_tokens * group + 7) / 8;
+  return nt <= 4 ? (int)nt : nt <= 6 ? 6 : MAX_NT;
 }
+static int blocks_per_sm(int nt) { return nt <= 2 ? 4 : nt <= 4 ? 3 : 2; }   // Shape::BLOCKS
 
 static int sm_count() {
   int dev = 0, n = 0;
@@ -661,7 +814,7 @@ static size_t part_bytes(int workers, int nt, int D) { return (size_t)workers * 
 
 template <int D, int NT>
 static sv_status launch_attention(AttnArgs& A, cudaStream_t st) {
-  constexpr size_t SMEM = sizeof(Stage<D>) * stages<D>() * WARPS;
+  constexpr size_t SMEM = Shape<D, NT>::SMEM;
   int dev = 0, done = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       g_attn_cache.get(dev, reinterpret_cast<const void*>(kv_attention_kernel<D, NT>), SMEM, 0, &done, [](int* v) {
@@ -669,11 +822,19 @@ static sv_status launch_attention(AttnArgs& A, cudaStream_t st) {
         return cudaFuncSetAttribute(kv_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
       }) != cudaSuccess)
     return SV_ERR_CUDA;
-  kv_attention_kernel<D, NT><<<A.workers / WARPS, WARPS * 32, SMEM, st>>>(A);
+  kv_attention_kernel<D, NT><<<A.workers, NTHR + 32, SMEM, st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  const long long blocks = (long long)A.w.B * A.w.max_tokens * A.w.kv_heads;
-  kv_combine_kernel<D, NT><<<(unsigned)blocks, CT, 0, st>>>(A);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  // launched while the first kernel still runs; waits for its results on the device
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((long long)A.w.B * A.w.max_tokens * A.w.q_heads + CW - 1) / CW));
+  cfg.blockDim = dim3(CW * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, NT>, A) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 template <int D>
@@ -682,7 +843,9 @@ static sv_status pick_attention(int nt, AttnArgs& A, cudaStream_t st) {
     case 1: return launch_attention<D, 1>(A, st);
     case 2: return launch_attention<D, 2>(A, st);
     case 3: return launch_attention<D, 3>(A, st);
-    default: return launch_attention<D, 4>(A, st);
+    case 4: return launch_attention<D, 4>(A, st);
+    case 6: return launch_attention<D, 6>(A, st);
+    default: return launch_attention<D, 8>(A, st);
   }
 }
 
@@ -693,7 +856,8 @@ size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int
   if (B < 1 || B > 65535 || max_tokens < 1 || max_tokens > (1 << 24) || kv_heads < 1 || kv_heads > 256 ||
       q_heads < kv_heads || q_heads % kv_heads || q_heads / kv_heads > 64 || (head_dim != 64 && head_dim != 128))
     return 0;
-  return prefix_bytes(B) + part_bytes(sm_count() * WARPS, row_tiles(max_tokens, q_heads / kv_heads), head_dim);
+  const int nt = row_tiles(max_tokens, q_heads / kv_heads);
+  return prefix_bytes(B) + part_bytes(sm_count() * blocks_per_sm(nt), nt, head_dim);
 }
 
 sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_codes, const float* k_scale,
@@ -708,7 +872,7 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   const Window w{seq_len, cu_tokens, page_table, B,       N,        max_tokens, max_pages,
                  num_pages, page_size, q_heads,  kv_heads, head_dim};
   if (bad_window(w) || q_stride < (long long)q_heads * head_dim || window < 0 || !isfinite(scale)) return SV_ERR_SHAPE;
-  if ((long long)B * max_tokens * kv_heads > 2147483647ll) return SV_ERR_SHAPE;
+  if ((long long)B * max_tokens * q_heads > 2147483647ll) return SV_ERR_SHAPE;
   if (!aligned(q, 16) || (q_stride * 2) % 16 || !aligned(out, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) ||
       !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(seq_len, 4) || !aligned(cu_tokens, 4) ||
       !aligned(page_table, 4) || !aligned(lse, 4))
@@ -716,7 +880,7 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   const int nt = row_tiles(max_tokens, q_heads / kv_heads);
   const int sms = aligned(workspace, 16) ? sm_count() : 1;
   if (sms < 1) return SV_ERR_CUDA;
-  if (!aligned(workspace, 16) || workspace_bytes < prefix_bytes(B) + part_bytes(sms * WARPS, nt, head_dim))
+  if (!aligned(workspace, 16) || workspace_bytes < prefix_bytes(B) + part_bytes(sms * blocks_per_sm(nt), nt, head_dim))
     return SV_ERR_WORKSPACE;
   AttnArgs A = {};
   A.w = w;
@@ -730,7 +894,7 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   A.lse = lse;
   A.prefix = static_cast<long long*>(workspace);
   A.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + prefix_bytes(B));
-  A.workers = sms * WARPS;
+  A.workers = sms * blocks_per_sm(nt);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return head_dim == 128 ? pick_attention<128>(nt, A, st) : pick_attention<64>(nt, A, st);
 }
