@@ -94,8 +94,9 @@ size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int
  * Products are formed from queries and weights in fp16 (queries scaled by a power of
  * two for each row, so their 8 significant bits are kept; weights to 11 bits) and
  * codes as they are, all sums in fp32. Repeated calls give the same bits.
+ * Every wait for a copy is bounded (0.2 s); if one runs out, all outputs are NaN.
  * Returns SV_ERR_NULL, SV_ERR_SHAPE, SV_ERR_ALIGN or SV_ERR_WORKSPACE before
- * launching, SV_ERR_CUDA when a launch fails. */
+ * launching, SV_ERR_CUDA when the tensor-map encoder or a launch fails. */
 sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_codes, const float* k_scale,
                             const void* v_codes, const float* v_scale, const int32_t* seq_len,
                             const int32_t* cu_tokens, const int32_t* page_table, int B, int N, int max_tokens,

@@ -3,11 +3,12 @@
 //
 // A window has few query rows (new tokens x query heads of a kv head) and reads the
 // whole cache once, so the bound is HBM: 2 head_dim bytes for each cached token and
-// kv head. The work is cut into units of 64 cached tokens of one item = (sequence,
+// kv head. The work is cut into units of 64 or 128 cached tokens of one item = (sequence,
 // kv head, tile of up to 8 NT query rows), and every block takes an equal share of
-// all units, whatever the sequences' lengths. A fifth warp walks the share and copies
-// its units into a ring of shared-memory stages (cp.async, zeros for what is not
-// there), handing each over at a block barrier. An item that lies within one block's
+// all units, whatever the sequences' lengths. A fifth warp walks the share and has its
+// units copied into a ring of shared-memory stages (TMA, one box for each page and
+// array, swizzled so that the fragments' loads meet no bank conflict), handing each
+// over at a block barrier once it is there. An item that lies within one block's
 // share is written out; the others leave (max, sum, weighted values) in the workspace
 // for kv_combine_kernel.
 //
@@ -20,6 +21,7 @@
 // take their index in any order, so each lane loads neighbouring bytes and calls
 // them whatever the fragment wants. The value scale of a page enters through the
 // exponent (weight 2^(s + log2 scale - m)) and the key scale through the logit.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -31,10 +33,12 @@
 
 namespace svkv {
 
-constexpr int TOK = 64;        // cached tokens of a unit
 constexpr int NWARP = 4, NTHR = 32 * NWARP;   // computing; one warp more copies
 constexpr int MAX_NT = 8;      // query rows of an item: 8 NT
-constexpr int OVERHEAD = 1;    // what an item costs besides its tokens, in units
+#ifndef OVH
+#define OVH 5
+#endif
+constexpr int OVERHEAD = OVH;    // what an item costs besides its tokens, in units
 // Weights are 2^(t - m) with m = LIFT below the running maximum of the exponents t,
 // and m moves only when a weight would exceed 2^TOP: they stay within fp16 (65504)
 // and the small ones keep as much of its range as there is.
@@ -52,43 +56,63 @@ struct AttnArgs {
   int window;
   __nv_bfloat16* out;
   float* lse;
-  long long* prefix;   // workspace: units before each sequence, [B + 1], then the warps in use
+  long long* prefix;   // workspace: units before each sequence [B + 1], the blocks in use, whether a wait ran out
   float* part;         // workspace: 2 slots for each warp
   int workers;
+  int group;           // query heads of a kv head
+  int group_mul;       // 2^16 / group, rounded up
 };
+// x / group for 0 <= x < 2^8: group_mul is too large by less than 1, and x group < 2^16
+__device__ __forceinline__ int over_group(const AttnArgs& A, int x) { return x * A.group_mul >> 16; }
 
+constexpr long long FAR = 1ll << 30;   // past every position of a cache
 constexpr int FIRST = 1, LAST = 2, WHOLE = 4, MASKED = 8, END = 16;
-struct Meta {                  // of a stage: 64 tokens from 64 tile of item (b, h, rt)
-  float4 run[4];               // of each 16 tokens: key scale, log2 and reciprocal of the value scale
+constexpr int MAX_RUNS = 8;    // runs of 16 tokens in a unit
+struct Meta {                  // of a stage: a unit of item (b, h, rt)
+  float4 run[MAX_RUNS];               // of each 16 tokens: key scale, log2 and reciprocal of the value scale
   int flags;                   // FIRST, LAST of the block's share of the item; WHOLE: that is all of it;
                                // MASKED: some row does not see all tokens; END: no unit
-  int tok0, row0, count;       // position of the first token; as in Seq: first, count
-  long long len;
-  int h, rt, slot, pad;        // slot of the workspace, if the share is not whole
-  int pad2[2];
+  int row0, count;             // as in Seq: first, count
+  int i0, r0;                  // the item's first query row is number r0 of new token i0
+  int hi0, lo0;                // new token i sees the unit's tokens up to hi0 + i and after lo0 + i
+  int h, slot, live, pad;      // slot of the workspace, if the share is not whole; tokens that are there
+  int pad2;
 };
 static_assert(sizeof(Meta) % 16 == 0, "stages stay 16-byte aligned");
 
-template <int D>
+constexpr uint64_t WAIT_NS = 200ull * 1000 * 1000;   // a copy that takes longer is given up
+
+template <int D, int TOK>
 struct Stage {
   uint8_t k[TOK * D], v[TOK * D];
-  Meta m;
 };
 // Blocks on an SM, and stages so that they fit its shared memory.
 template <int D, int NT>
 struct Shape {
-  static constexpr int BLOCKS = NT <= 2 ? 4 : NT <= 4 ? 3 : 2;
-  static constexpr bool QREG = NT <= 3;                  // query fragments in registers
+#ifndef MT128
+#define MT128 (NT == 4 ? 2 : 1)
+#endif
+  static constexpr int MT = D == 128 ? MT128 : 2;        // runs of 16 tokens of a warp
+  static constexpr int TOK = 16 * MT * NWARP;            // cached tokens of a unit
+  #ifdef BLK
+  static constexpr int BLOCKS = BLK;
+#else
+  static constexpr int BLOCKS = NT <= 2 ? 4 : NT <= 3 ? 3 : 2;
+#endif
+  #ifndef QR
+#define QR 3
+#endif
+  static constexpr bool QREG = NT <= QR;                  // query fragments in registers
   static constexpr int PSTRIDE = 16 * (NT | 1);          // bytes of a token's weights: odd multiples of 16 spread the banks
   // the queries' and the weights' buffers are one where the queries move on to registers
   static constexpr int QBYTES = 8 * NT * D * 2, PBYTES = TOK * PSTRIDE, PAT = QREG ? 0 : QBYTES;
   static constexpr int BUF = QREG ? (QBYTES > PBYTES ? QBYTES : PBYTES) : QBYTES + PBYTES;
-  static constexpr int FIXED = BUF + 8 * NT * 4 * (1 + NWARP);
-  static constexpr int ROOM = (227 * 1024) / BLOCKS - 1024 - 512 - FIXED;
-  static constexpr int FIT = ROOM / (int)sizeof(Stage<D>);
+  static constexpr int FIXED = 1024 /* stages lie on 1024-byte boundaries */ + BUF + 8 * NT * 4 * (1 + NWARP);
+  static constexpr int ROOM = (227 * 1024) / BLOCKS - 1024 - 256 - FIXED;
+  static constexpr int FIT = ROOM / (int)(sizeof(Stage<D, TOK>) + sizeof(Meta) + 8);
   static constexpr int NS = FIT > 6 ? 6 : FIT;
-  static constexpr size_t SMEM = sizeof(Stage<D>) * NS + FIXED;
-  static_assert(NS >= 3, "three stages at least");
+  static constexpr size_t SMEM = (sizeof(Stage<D, TOK>) + sizeof(Meta) + 8) * NS + FIXED;
+  static_assert(NS >= 2, "three stages at least");
 };
 
 // Units of sequence b: kv_heads * row tiles * (OVERHEAD + token tiles), at least one
@@ -97,8 +121,9 @@ struct Shape {
 struct Span {
   int tile0, tiles, rts;
 };
-template <int NT>
+template <int D, int NT>
 __device__ __forceinline__ Span span(const AttnArgs& A, const Seq& s) {
+  constexpr int TOK = Shape<D, NT>::TOK;
   Span p{0, 0, 0};
   if (s.count == 0) return p;
   const long long cap = (long long)A.w.max_pages * A.w.page_size;
@@ -107,12 +132,12 @@ __device__ __forceinline__ Span span(const AttnArgs& A, const Seq& s) {
   lo = min(lo, end);
   p.tile0 = (int)(lo / TOK);
   p.tiles = max((int)((end + TOK - 1) / TOK) - p.tile0, 1);
-  p.rts = (int)(((long long)s.count * (A.w.q_heads / A.w.kv_heads) + 8 * NT - 1) / (8 * NT));
+  p.rts = (s.count * A.group + 8 * NT - 1) / (8 * NT);   // below 2^30
   return p;
 }
-template <int NT>
+template <int D, int NT>
 __device__ __forceinline__ long long units_of(const AttnArgs& A, int b) {
-  const Span p = span<NT>(A, sequence(A.w, b));
+  const Span p = span<D, NT>(A, sequence(A.w, b));
   return (long long)A.w.kv_heads * p.rts * (p.tiles + OVERHEAD);
 }
 
@@ -121,15 +146,35 @@ __device__ __forceinline__ long long share_start(long long w, long long units, l
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {   // zeros when off
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+__device__ __forceinline__ bool arrived(uint32_t b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(b), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Waits for the copies of a stage, for at most WAIT_NS.
+__device__ __forceinline__ bool wait_copies(uint32_t b, uint32_t parity) {
+  if (arrived(b, parity)) return true;
+  const uint64_t t0 = now_ns();
+  while (!arrived(b, parity))
+    if (now_ns() - t0 > WAIT_NS) return false;
+  return true;
+}
+// A box of rows of codes from row y; the first coordinate is 0, the second has no alignment rule.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int y, uint32_t b) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(b)
+      : "memory");
+}
 
 __device__ __forceinline__ float ex2f(float x) {
   float r;
@@ -186,8 +231,8 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool x) {
   return r != 0;
 }
 
-// Byte offset of 16-byte chunk c of token t in a stage's tile: chunks are permuted by
-// the token so that the fragments' loads touch every bank once (head_dim 64: twice).
+// Byte offset of 16-byte chunk c of token t in a stage's tile: TMA's 128-byte (64-byte)
+// swizzle, under which the fragments' loads touch every bank once.
 template <int D>
 __device__ __forceinline__ int chunk_at(int t, int c) {
   return D == 128 ? t * 128 + ((c ^ (t & 7)) << 4) : t * 64 + ((c ^ ((t >> 1) & 3)) << 4);
@@ -242,32 +287,43 @@ __device__ __noinline__ void add_by_token(ByToken<DT, NT>& x, int q) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attention_kernel(const AttnArgs A) {
+__global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
+    kv_attention_kernel(const AttnArgs A, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v) {
   using Sh = Shape<D, NT>;
-  constexpr int NS = Sh::NS;
+  constexpr int NS = Sh::NS, MT = Sh::MT, TOK = Sh::TOK;
   constexpr int KW = D / 16;       // words (4 codes) of a token in a lane = steps of the key product
   constexpr int DT = D / 64;       // 16-row tiles of head_dim in a warp's value product
   constexpr int ROWS = 8 * NT, PS = Sh::PSTRIDE;
-  extern __shared__ __align__(128) unsigned char smem[];
-  Stage<D>* ring = reinterpret_cast<Stage<D>*>(smem);
-  unsigned char* sq = smem + sizeof(Stage<D>) * NS;                     // queries, fp16, in fragment order
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  using Unit = Stage<D, TOK>;
+  Unit* ring = reinterpret_cast<Unit*>(smem);
+  Meta* meta = reinterpret_cast<Meta*>(smem + sizeof(Unit) * NS);
+  unsigned char* sq = smem + (sizeof(Unit) + sizeof(Meta)) * NS;    // queries, fp16, in fragment order
   unsigned char* sp = sq + Sh::PAT;                                     // weights, fp16 [token][row]
   float* srs = reinterpret_cast<float*>(sq + Sh::BUF);                  // logit factor of each row
   float* swm = srs + ROWS;                                              // [warp][row]: maxima, later sums
+  unsigned long long* full = reinterpret_cast<unsigned long long*>(swm + NWARP * ROWS);   // a stage's copies have landed
   __shared__ long long s_sum[NWARP + 1], s_pre;
   __shared__ int s_b;
   const Window& w = A.w;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const int G = w.q_heads / w.kv_heads;
+  const int G = A.group;
 
   // --- shares: total units, then the sequence in which this block's share begins
   constexpr int ALL = NTHR + 32;
   long long mine = 0;
-  for (int b = tid; b < w.B; b += ALL) mine += units_of<NT>(A, b);
+  for (int b = tid; b < w.B; b += ALL) mine += units_of<D, NT>(A, b);
 #pragma unroll
   for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) s_sum[warp] = mine;
-  if (tid == 0) s_b = -1;
+  if (tid == 0) {
+    s_b = -1;
+    for (int i = 0; i < NS; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(full + i)) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   __syncthreads();
   long long units = 0;
 #pragma unroll
@@ -278,7 +334,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
   long long before = 0;
   for (int b0 = 0; b0 < w.B; b0 += ALL) {
     const int b = b0 + tid;
-    const long long u = b < w.B ? units_of<NT>(A, b) : 0;
+    const long long u = b < w.B ? units_of<D, NT>(A, b) : 0;
     long long inc = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -301,6 +357,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
   if (blockIdx.x == 0 && tid == 0) {
     A.prefix[w.B] = units;
     A.prefix[w.B + 1] = workers;
+    A.prefix[w.B + 2] = 0;
   }
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -311,7 +368,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
     int cb = s_b;
     long long cu = u0;
     Seq cs = sequence(w, cb);
-    Span cp = span<NT>(A, cs);
+    Span cp = span<D, NT>(A, cs);
     int ct, ch, cr;
     {
       const long long x = u0 - s_pre;
@@ -326,18 +383,17 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
     int entry = -1, window_b = -1, window_h = -1, window0 = 0;
     float eks = 0.f, elv = 0.f, einv = 0.f;
     const int P = w.page_size, shift = __ffs(P) - 1;
-    constexpr int CH = D / 16;            // chunks of a token
-    constexpr int RPI = 32 / CH;          // tokens copied at once: 4 or 8
-    const int c = lane % CH, t0 = lane / CH;
+    const int box = min(P, TOK);          // tokens of a copy
     const auto issue = [&](int stage) {
-      Stage<D>& S = ring[stage];
+      Unit& S = ring[stage];
+      Meta& M = meta[stage];
       if (ct < OVERHEAD) {
         cu += OVERHEAD - ct;
         ct = OVERHEAD;
       }
       const bool on = cu < u1;
       if (!on) {
-        if (lane == 0) S.m.flags = END;
+        if (lane == 0) M.flags = END;
       } else {
         const int tok0 = (cp.tile0 + ct - OVERHEAD) * TOK;     // below 2^27
         const int live = cs.len < 0 ? 0 : (int)min(cs.len + cs.count - tok0, (long long)TOK);
@@ -356,39 +412,43 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
           elv = log2f(vs);
           einv = __frcp_rn(vs);
         }
-        bool gap = false;
-        const uint32_t kd = smem_u32(S.k), vd = smem_u32(S.v);
-#pragma unroll
-        for (int run = 0; run < TOK / 16; ++run) {
-          const int at = tok0 + 16 * run, from = (at >> shift) - window0;
-          const int page = __shfl_sync(0xffffffffu, entry, from);
-          const float ks = __shfl_sync(0xffffffffu, eks, from), lv = __shfl_sync(0xffffffffu, elv, from),
-                      inv = __shfl_sync(0xffffffffu, einv, from);
-          if (lane == 0) S.m.run[run] = make_float4(ks, lv, inv, page < 0 ? 1.f : 0.f);
-          gap |= page < 0;
-          const size_t off = ((((size_t)max(page, 0) * w.kv_heads + ch) << shift) + (at & (P - 1)) + t0) * D + c * 16;
-          const uint8_t *kp = A.k_codes + off, *vp = A.v_codes + off;
-          const int n = (page < 0 ? 0 : live) - 16 * run - t0;
-#pragma unroll
-          for (int i = 0; i < 16 / RPI; ++i) {
-            const uint32_t d = (uint32_t)chunk_at<D>(16 * run + i * RPI + t0, c);
-            copy16(kd + d, kp + i * RPI * D, i * RPI < n);
-            copy16(vd + d, vp + i * RPI * D, i * RPI < n);
-          }
+        // the first lanes: the runs of 16 tokens
+        const int from = ((tok0 + (16 * lane & (TOK - 1))) >> shift) - window0;
+        const int page = __shfl_sync(0xffffffffu, entry, from);
+        const float ks = __shfl_sync(0xffffffffu, eks, from), lv = __shfl_sync(0xffffffffu, elv, from),
+                    inv = __shfl_sync(0xffffffffu, einv, from);
+        const bool gap = __any_sync(0xffffffffu, page < 0);
+        if (lane < TOK / 16) M.run[lane] = make_float4(ks, lv, inv, page < 0 ? 1.f : 0.f);
+        // the first TOK / box lanes: a copy of the keys and one of the values
+        const int at = tok0 + (lane * box & (TOK - 1));
+        const int pg = __shfl_sync(0xffffffffu, entry, (at >> shift) - window0);
+        const bool mine = lane * box < TOK && pg >= 0 && at - tok0 < live;
+        const int copies = __popc(__ballot_sync(0xffffffffu, mine));
+        const uint32_t bar_at = smem_u32(full + stage);
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar_at), "r"(copies * 2 * box * D) : "memory");
+        __syncwarp();
+        if (mine) {
+          const int y = (pg * w.kv_heads + ch) * P + (at & (P - 1)), d = (at - tok0) * D;
+          copy_box(smem_u32(S.k) + d, &map_k, y, bar_at);
+          copy_box(smem_u32(S.v) + d, &map_v, y, bar_at);
         }
         if (lane == 0) {
           const long long item0 = cu - ct, item1 = item0 + OVERHEAD + cp.tiles;
           const bool masked = gap || cs.len < 0 || tok0 + TOK - 1 > cs.len ||
                               (A.window && tok0 <= cs.len + cs.count - 1 - A.window);
-          S.m.flags = (ct == OVERHEAD || cu == u0 ? FIRST : 0) | (cu + 1 == item1 || cu + 1 == u1 ? LAST : 0) |
+          M.flags = (ct == OVERHEAD || cu == u0 ? FIRST : 0) | (cu + 1 == item1 || cu + 1 == u1 ? LAST : 0) |
                       (u0 <= item0 + OVERHEAD && u1 >= item1 ? WHOLE : 0) | (masked ? MASKED : 0);
-          S.m.tok0 = tok0;
-          S.m.row0 = cs.first;
-          S.m.count = cs.count;
-          S.m.len = cs.len;
-          S.m.h = ch;
-          S.m.rt = cr;
-          S.m.slot = u0 < item0 ? 1 : 0;
+          M.row0 = cs.first;
+          M.count = cs.count;
+          const long long hi = cs.len < 0 ? -FAR : cs.len - tok0;
+          M.hi0 = (int)min(hi, FAR);
+          M.lo0 = A.window ? (int)max(min(hi - A.window, FAR), -FAR) : (int)-FAR;
+          M.h = ch;
+          M.i0 = cr * ROWS / G;
+          M.r0 = cr * ROWS % G;
+          M.slot = u0 < item0 ? 1 : 0;
+          M.live = live;
         }
         ++cu;
         if (++ct == cp.tiles + OVERHEAD) {
@@ -400,24 +460,38 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
               if (cu < u1) {
                 do {
                   cs = sequence(w, ++cb);
-                  cp = span<NT>(A, cs);
+                  cp = span<D, NT>(A, cs);
                 } while (cp.rts == 0 && cb + 1 < w.B);
               }
             }
           }
         }
       }
-      copies_commit();
       return on;
     };
     int ahead = 0;               // units copied or on their way, not yet handed over
 #pragma unroll 1
     for (int i = 0; i < NS - 1; ++i) ahead += issue(i);
-    for (int stage = 0;; stage = stage + 1 == NS ? 0 : stage + 1) {
-      copies_wait<NS - 2>();
+    uint32_t parity = 0;
+    for (int stage = 0;;) {
+      if (ahead > 0 && !__all_sync(0xffffffffu, wait_copies(smem_u32(full + stage), parity))) {
+        // given up: the others stop, the join makes every output NaN
+        if (lane == 0) {
+          meta[stage].flags = END;
+          A.prefix[w.B + 2] = 1;
+        }
+        __syncwarp();
+        bar(1, ALL);
+        for (int i = 1; i < ahead; ++i) {
+          if (++stage == NS) stage = 0, parity ^= 1;
+          wait_copies(smem_u32(full + stage), parity);
+        }
+        return;
+      }
       bar(1, ALL);               // the unit is there, and the one before it is done with
       if (ahead == 0) return;    // that was the END
       ahead += issue(stage == 0 ? NS - 1 : stage - 1) - 1;
+      if (++stage == NS) stage = 0, parity ^= 1;
     }
   }
 
@@ -425,8 +499,8 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
   float m[NT][2], l[NT][2], o[DT][NT][4];   // of rows 8 n + 2 q + {0, 1}
   for (int stage = 0;; stage = stage + 1 == NS ? 0 : stage + 1) {
     bar(1, ALL);
-    const Stage<D>& S = ring[stage];
-    const Meta& M = S.m;
+    const Unit& S = ring[stage];
+    const Meta& M = meta[stage];
     const int flags = M.flags;
     if (flags & END) return;
     if (flags & FIRST) {
@@ -434,7 +508,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
       // so that the row's largest element lies in [2^7, 2^8)
 #pragma unroll 1
       for (int r = tid >> 2; r < ROWS; r += NTHR / 4) {
-        const int row = M.rt * ROWS + r, i = row / G, hd = M.h * G + row % G;
+        const int i = M.i0 + over_group(A, M.r0 + r), hd = M.h * G + M.r0 + r - (i - M.i0) * G;
         uint32_t x[D / 8];
         if (i < M.count) {
           const uint4* p = reinterpret_cast<const uint4*>(A.q + (size_t)(M.row0 + i) * (size_t)A.q_stride + (size_t)hd * D + q * (D / 4));
@@ -483,37 +557,35 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
       }
     }
 
-    // --- logits of the warp's 16 tokens: sc[n] holds tokens g and g + 8, rows 8 n + 2 q (+ 1)
-    float sc[NT][4];
+    // --- logits of the warp's runs of 16 tokens: sc[t][n] holds tokens g and g + 8, rows 8 n + 2 q (+ 1)
+    float sc[MT][NT][4];
     {
-      uint32_t ka[KW], kb[KW];
-      const int ta = 16 * warp + g;
-      if (D == 128) {
+      uint32_t ka[MT][KW], kb[MT][KW];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 a = *reinterpret_cast<const uint4*>(S.k + chunk_at<D>(ta, 2 * q + i));
-          const uint4 b = *reinterpret_cast<const uint4*>(S.k + chunk_at<D>(ta + 8, 2 * q + i));
-          ka[4 * i % KW] = a.x, ka[(4 * i + 1) % KW] = a.y, ka[(4 * i + 2) % KW] = a.z, ka[(4 * i + 3) % KW] = a.w;
-          kb[4 * i % KW] = b.x, kb[(4 * i + 1) % KW] = b.y, kb[(4 * i + 2) % KW] = b.z, kb[(4 * i + 3) % KW] = b.w;
+      for (int t = 0; t < MT; ++t) {
+        const int ta = 16 * (MT * warp + t) + g;
+#pragma unroll
+        for (int i = 0; i < KW / 4; ++i) {
+          const uint4 a = *reinterpret_cast<const uint4*>(S.k + chunk_at<D>(ta, (KW / 4) * q + i));
+          const uint4 b = *reinterpret_cast<const uint4*>(S.k + chunk_at<D>(ta + 8, (KW / 4) * q + i));
+          ka[t][4 * i] = a.x, ka[t][4 * i + 1] = a.y, ka[t][4 * i + 2] = a.z, ka[t][4 * i + 3] = a.w;
+          kb[t][4 * i] = b.x, kb[t][4 * i + 1] = b.y, kb[t][4 * i + 2] = b.z, kb[t][4 * i + 3] = b.w;
         }
-      } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(S.k + chunk_at<D>(ta, q));
-        const uint4 b = *reinterpret_cast<const uint4*>(S.k + chunk_at<D>(ta + 8, q));
-        ka[0] = a.x, ka[1] = a.y, ka[2] = a.z, ka[3] = a.w;
-        kb[0] = b.x, kb[1] = b.y, kb[2] = b.z, kb[3] = b.w;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[t][n][k] = 0.f;
       }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc[n][k] = 0.f;
-#pragma unroll
       for (int k2 = 0; k2 < KW / 2; ++k2) {
-        uint32_t a[2][4];
+        uint32_t a[MT][2][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          widen(ka[2 * k2 + k], a[k][0], a[k][2]);
-          widen(kb[2 * k2 + k], a[k][1], a[k][3]);
-        }
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            widen(ka[t][2 * k2 + k], a[t][k][0], a[t][k][2]);
+            widen(kb[t][2 * k2 + k], a[t][k][1], a[t][k][3]);
+          }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           uint32_t f[4];
@@ -523,39 +595,57 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
           } else {
             ldsm4(f, smem_u32(sq + (8 * n + (lane & 7)) * (D * 2) + (((4 * k2 + (lane >> 3)) ^ (lane & 7)) << 4)));
           }
-          mma16816(sc[n], a[0][0], a[0][1], a[0][2], a[0][3], f[0], f[1]);
-          mma16816(sc[n], a[1][0], a[1][1], a[1][2], a[1][3], f[2], f[3]);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            mma16816(sc[t][n], a[t][0][0], a[t][0][1], a[t][0][2], a[t][0][3], f[0], f[1]);
+            mma16816(sc[t][n], a[t][1][0], a[t][1][1], a[t][1][2], a[t][1][3], f[2], f[3]);
+          }
         }
       }
     }
 
     // --- weights. A token's exponent is its logit (base 2) plus log2 of its value scale
-    const float4 run = M.run[warp];
-    const float inv = run.z;
-    // whether the thread's row e of tile n sees position p
+    // whether the thread's row e of tile n sees token p of the unit
     const auto sees = [&](int n, int e, int p) {
-      const long long pos = M.len + (M.rt * ROWS + 8 * n + 2 * q + e) / G;
-      return M.len >= 0 && p <= pos && !(A.window && p <= pos - A.window);
+      const int i = M.i0 + over_group(A, M.r0 + 8 * n + 2 * q + e);
+      return p <= M.hi0 + i && p > M.lo0 + i;
     };
-    float top = -INFINITY;
+    float inv[MT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float2 rs = *reinterpret_cast<const float2*>(srs + 8 * n + 2 * q);
+    for (int t = 0; t < MT; ++t) {
+      const float4 run = M.run[MT * warp + t];
+      inv[t] = run.z;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sc[n][k] = fmaf(sc[n][k], (k & 1 ? rs.y : rs.x) * run.x, run.y);
+      for (int n = 0; n < NT; ++n) {
+        const float2 rs = *reinterpret_cast<const float2*>(srs + 8 * n + 2 * q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sc[t][n][k] = fmaf(sc[t][n][k], (k & 1 ? rs.y : rs.x) * run.x, run.y);
+      }
     }
     if (flags & MASKED) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)   // run.w: an unmapped page
-          if (run.w != 0.f || !sees(n, k & 1, M.tok0 + 16 * warp + g + 8 * (k >> 1))) sc[n][k] = -INFINITY;
+        for (int e = 0; e < 2; ++e) {
+          const int i = M.i0 + over_group(A, M.r0 + 8 * n + 2 * q + e), hi = M.hi0 + i, lo = M.lo0 + i;
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int p = 16 * (MT * warp + t) + g + 8 * k;
+              if (p > hi || p <= lo || M.run[MT * warp + t].w != 0.f) sc[t][n][2 * k + e] = -INFINITY;   // w: unmapped
+            }
+        }
     }
+    float top = -INFINITY;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        top = fmaxf(top, fmaxf(sc[n][e], sc[n][2 + e]) - m[n][e]);
+        float x = fmaxf(sc[0][n][e], sc[0][n][2 + e]);
+#pragma unroll
+        for (int t = 1; t < MT; ++t) x = fmaxf(x, fmaxf(sc[t][n][e], sc[t][n][2 + e]));
+        top = fmaxf(top, x - m[n][e]);
       }
     if (bar_any(2, NTHR, top > TOP)) {
       // some weight would leave its range: move every row's frame to its maximum
@@ -563,10 +653,12 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(sc[n][e], sc[n][2 + e]);
+          float x = fmaxf(sc[0][n][e], sc[0][n][2 + e]);
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
-          if (g == 0) swm[warp * ROWS + 8 * n + 2 * q + e] = t;
+          for (int t = 1; t < MT; ++t) x = fmaxf(x, fmaxf(sc[t][n][e], sc[t][n][2 + e]));
+#pragma unroll
+          for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
+          if (g == 0) swm[warp * ROWS + 8 * n + 2 * q + e] = x;
         }
       bar(2, NTHR);
 #pragma unroll
@@ -602,17 +694,24 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
           v[t][i] = *reinterpret_cast<const uint16_t*>(S.v + chunk_at<D>(tk, warp) + 2 * g);
       }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float p0 = ex2f(sc[n][2 * k] - m[n][0]), p1 = ex2f(sc[n][2 * k + 1] - m[n][1]);
-        l[n][0] = fmaf(p0, inv, l[n][0]);
-        l[n][1] = fmaf(p1, inv, l[n][1]);
-        *reinterpret_cast<uint32_t*>(sp + (16 * warp + g + 8 * k) * PS + n * 16 + q * 4) = pack_h2(p0, p1);
-      }
-    }
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float p0 = ex2f(sc[t][n][2 * k] - m[n][0]), p1 = ex2f(sc[t][n][2 * k + 1] - m[n][1]);
+          l[n][0] = fmaf(p0, inv[t], l[n][0]);
+          l[n][1] = fmaf(p1, inv[t], l[n][1]);
+          *reinterpret_cast<uint32_t*>(sp + (16 * (MT * warp + t) + g + 8 * k) * PS + n * 16 + q * 4) = pack_h2(p0, p1);
+        }
     bool by_token = false;
     if (flags & MASKED) {
+      // what is not there reads as zero
+#pragma unroll
+      for (int t = 0; t < TOK / 16; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (16 * t + 2 * q + (i & 1) + 8 * (i >> 1) >= M.live || M.run[t].w != 0.f) v[t][i] = 0u;
       // NaN values of tokens that only some rows see: 0 * NaN must not reach the others
       bool nan = false;
 #pragma unroll
@@ -656,7 +755,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
           for (int e = 0; e < 2; ++e) {
             x.seen[n][e] = 0u;
 #pragma unroll 1
-            for (int k = 0; k < 16; ++k) x.seen[n][e] |= (uint32_t)sees(n, e, M.tok0 + 16 * t + k) << k;
+            for (int k = 0; k < 16; ++k) x.seen[n][e] |= (uint32_t)sees(n, e, 16 * t + k) << k;
           }
         add_by_token<DT, NT>(x, q);
       }
@@ -683,14 +782,14 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS)) kv_attentio
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = 8 * n + 2 * q + e, row = M.rt * ROWS + r, i = row / G;
+          const int r = 8 * n + 2 * q + e, i = M.i0 + over_group(A, M.r0 + r);
           float sum = swm[r];
 #pragma unroll
           for (int k = 1; k < NWARP; ++k) sum += swm[k * ROWS + r];
           if (i >= M.count) continue;
           const int d0 = (D / 4) * warp + (D / 32) * g;
           if (flags & WHOLE) {
-            const size_t at = (size_t)(M.row0 + i) * w.q_heads + M.h * G + row % G;
+            const size_t at = (size_t)(M.row0 + i) * w.q_heads + M.h * G + M.r0 + r - (i - M.i0) * G;
             const float f = sum == 0.f ? 0.f : 1.f / sum;
             uint32_t y[DT];
 #pragma unroll
@@ -726,7 +825,7 @@ __global__ void __launch_bounds__(CW * 32) kv_combine_kernel(const AttnArgs A) {
   // first of all, in every thread: this grid ends only after the one before it
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Window& w = A.w;
-  const int lane = threadIdx.x & 31, G = w.q_heads / w.kv_heads;
+  const int lane = threadIdx.x & 31, G = A.group;
   const long long id = (long long)blockIdx.x * CW + (threadIdx.x >> 5);
   const int qh = (int)(id % w.q_heads);
   const long long bi = id / w.q_heads;
@@ -735,8 +834,15 @@ __global__ void __launch_bounds__(CW * 32) kv_combine_kernel(const AttnArgs A) {
   const int b = (int)(bi / w.max_tokens), h = qh / G;
   const Seq s = sequence(w, b);
   if (i >= s.count) return;
-  const Span p = span<NT>(A, s);
+  const Span p = span<D, NT>(A, s);
   const long long units = A.prefix[w.B], workers = A.prefix[w.B + 1], pre = A.prefix[b];
+  const size_t at = (size_t)(s.first + i) * w.q_heads + qh;
+  if (A.prefix[w.B + 2] != 0) {   // a copy never came
+#pragma unroll
+    for (int e = 0; e < E; ++e) A.out[at * D + lane * E + e] = __float2bfloat16_rn(NAN);
+    if (A.lse && lane == 0) A.lse[at] = NAN;
+    return;
+  }
   const int row = i * G + qh % G, rt = row / ROWS, r = row % ROWS;
   const long long i0 = pre + ((long long)h * p.rts + rt) * (p.tiles + OVERHEAD), i1 = i0 + OVERHEAD + p.tiles;
   // the blocks that hold its first and its last unit with tokens
@@ -751,10 +857,10 @@ __global__ void __launch_bounds__(CW * 32) kv_combine_kernel(const AttnArgs A) {
   for (long long k0 = w0; k0 <= w1; k0 += 32) {
     const int n = (int)min(w1 - k0 + 1, 32ll);
     float mk = NO_FRAME, lk = 0.f;
-    const float* at = nullptr;
+    const float* part = nullptr;
     if (lane < n) {
-      at = slot(k0 + lane);
-      mk = at[2 * r], lk = at[2 * r + 1];
+      part = slot(k0 + lane);
+      mk = part[2 * r], lk = part[2 * r + 1];
     }
     float top = fmaxf(m, mk);
 #pragma unroll
@@ -769,7 +875,7 @@ __global__ void __launch_bounds__(CW * 32) kv_combine_kernel(const AttnArgs A) {
     for (int e = 0; e < E; ++e) o[e] *= f;
 #pragma unroll 8
     for (int k = 0; k < n; ++k) {
-      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), k));
+      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(part), k));
       const float fs = __shfl_sync(0xffffffffu, fk, k);
       src += 2 * ROWS + r * D + lane * E;
       if (E == 4) {
@@ -782,7 +888,6 @@ __global__ void __launch_bounds__(CW * 32) kv_combine_kernel(const AttnArgs A) {
       }
     }
   }
-  const size_t at = (size_t)(s.first + i) * w.q_heads + qh;
   const float f = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
@@ -797,7 +902,11 @@ static int row_tiles(int max_tokens, int group) {
   const long long nt = ((long long)max_tokens * group + 7) / 8;
   return nt <= 4 ? (int)nt : nt <= 6 ? 6 : MAX_NT;
 }
-static int blocks_per_sm(int nt) { return nt <= 2 ? 4 : nt <= 4 ? 3 : 2; }   // Shape::BLOCKS
+#ifdef BLK
+static int blocks_per_sm(int nt) { return BLK; }
+#else
+static int blocks_per_sm(int nt) { return nt <= 2 ? 4 : nt <= 3 ? 3 : 2; }   // Shape::BLOCKS
+#endif
 
 static int sm_count() {
   int dev = 0, n = 0;
@@ -809,8 +918,37 @@ static int sm_count() {
   return n;
 }
 
-static size_t prefix_bytes(int B) { return ((size_t)(B + 2) * sizeof(long long) + 127) & ~(size_t)127; }
+static size_t prefix_bytes(int B) { return ((size_t)(B + 3) * sizeof(long long) + 127) & ~(size_t)127; }
 static size_t part_bytes(int workers, int nt, int D) { return (size_t)workers * 2 * 8 * nt * (D + 2) * sizeof(float); }
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return (EncodeTiled) nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// The codes as rows of head_dim bytes, one for each (page, kv head, token).
+static bool code_map(CUtensorMap* map, const void* codes, const Window& w, int TOK) {
+  EncodeTiled enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)w.head_dim, (cuuint64_t)w.num_pages * w.kv_heads * w.page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)w.head_dim};
+  const cuuint32_t box[2] = {(cuuint32_t)w.head_dim, (cuuint32_t)(w.page_size < TOK ? w.page_size : TOK)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, w.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <int D, int NT>
 static sv_status launch_attention(AttnArgs& A, cudaStream_t st) {
@@ -822,7 +960,9 @@ static sv_status launch_attention(AttnArgs& A, cudaStream_t st) {
         return cudaFuncSetAttribute(kv_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
       }) != cudaSuccess)
     return SV_ERR_CUDA;
-  kv_attention_kernel<D, NT><<<A.workers, NTHR + 32, SMEM, st>>>(A);
+  CUtensorMap map_k, map_v;
+  if (!code_map(&map_k, A.k_codes, A.w, Shape<D, NT>::TOK) || !code_map(&map_v, A.v_codes, A.w, Shape<D, NT>::TOK)) return SV_ERR_CUDA;
+  kv_attention_kernel<D, NT><<<A.workers, NTHR + 32, SMEM, st>>>(A, map_k, map_v);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   // launched while the first kernel still runs; waits for its results on the device
   cudaLaunchConfig_t cfg = {};
@@ -895,6 +1035,8 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   A.prefix = static_cast<long long*>(workspace);
   A.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + prefix_bytes(B));
   A.workers = sms * blocks_per_sm(nt);
+  A.group = q_heads / kv_heads;
+  A.group_mul = ((1 << 16) + A.group - 1) / A.group;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return head_dim == 128 ? pick_attention<128>(nt, A, st) : pick_attention<64>(nt, A, st);
 }
