@@ -35,10 +35,8 @@ namespace svkv {
 
 constexpr int NWARP = 4, NTHR = 32 * NWARP;   // computing; one warp more copies
 constexpr int MAX_NT = 8;      // query rows of an item: 8 NT
-#ifndef OVH
-#define OVH 5
-#endif
-constexpr int OVERHEAD = OVH;    // what an item costs besides its tokens, in units
+constexpr int OVERHEAD = 5;    // what an item costs besides its tokens, in units
+constexpr int MIN_SHARE = 4;   // units of a block at least: shares of a few units cost more to join than they save
 // Weights are 2^(t - m) with m = LIFT below the running maximum of the exponents t,
 // and m moves only when a weight would exceed 2^TOP: they stay within fp16 (65504)
 // and the small ones keep as much of its range as there is.
@@ -46,6 +44,10 @@ constexpr float LIFT = 7.f, TOP = 15.f;
 constexpr float NO_FRAME = -1e30f;   // m of a row that has seen nothing (finite: -inf - m stays -inf)
 constexpr float LN2F = 0.693147180559945309f, LOG2EF = 1.44269504088896341f;
 
+struct Start {
+  long long unit0;     // its first unit
+  int tiles, h, rt, row0, count, pad;
+};
 struct AttnArgs {
   Window w;
   const __nv_bfloat16* q;
@@ -57,7 +59,8 @@ struct AttnArgs {
   __nv_bfloat16* out;
   float* lse;
   long long* prefix;   // workspace: units before each sequence [B + 1], the blocks in use, whether a wait ran out
-  float* part;         // workspace: 2 slots for each warp
+  Start* start;        // workspace: the item in which each block's share begins
+  float* part;         // workspace: 2 slots for each block
   int workers;
   int group;           // query heads of a kv head
   int group_mul;       // 2^16 / group, rounded up
@@ -141,8 +144,12 @@ __device__ __forceinline__ long long units_of(const AttnArgs& A, int b) {
   return (long long)A.w.kv_heads * p.rts * (p.tiles + OVERHEAD);
 }
 
+// Quotient of non-negative numbers; the 64-bit division is slow and rarely needed.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 __device__ __forceinline__ long long share_start(long long w, long long units, long long workers) {
-  return w * units / workers;
+  return quotient(w * units, workers);
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
   long long units = 0;
 #pragma unroll
   for (int i = 0; i <= NWARP; ++i) units += s_sum[i];
-  const long long workers = min((long long)A.workers, max(units, 1ll));
+    const long long workers = min((long long)A.workers, max(units / MIN_SHARE, 1ll));
   const long long wk = blockIdx.x;
   const long long u0 = share_start(wk, units, workers), u1 = wk < workers ? share_start(wk + 1, units, workers) : u0;
   long long before = 0;
@@ -373,10 +380,11 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
     {
       const long long x = u0 - s_pre;
       const int per = cp.tiles + OVERHEAD;
-      const long long item = x / per;
-      ct = (int)(x % per);
-      ch = (int)(item / cp.rts);
-      cr = (int)(item % cp.rts);
+      const long long item = quotient(x, per);
+      ct = (int)(x - item * per);
+      ch = (int)quotient(item, cp.rts);
+      cr = (int)(item - (long long)ch * cp.rts);
+      if (lane == 0) A.start[wk] = Start{u0 - ct, cp.tiles, ch, cr, cs.first, cs.count, 0};
     }
     // entries window0 .. window0 + 31 of the sequence's row of the page table and those
     // pages' scales, one in each lane
@@ -815,53 +823,55 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
   }
 }
 
-// Joins the shares of the items that several blocks worked on: a warp takes one query
-// row. It gathers the shares' frames and sums a lane each, then adds the weighted
-// values, D / 32 elements a lane, in the shares' order.
-constexpr int CW = 4;   // warps of a block
+// Joins the shares of the items that several blocks worked on. At most one item is cut
+// at the start of each share: block (k, n) looks whether share k is the second of its
+// item, and if so takes rows 8 n .. 8 n + 7 of it. Eight warps share the rows that are
+// there; a warp gathers the frames and sums of its part of the shares, a lane each,
+// and adds their weighted values, D / 32 elements a lane. Then the warps of a row are
+// joined, in their order.
+constexpr int JOIN = 8;   // warps
 template <int D, int NT>
-__global__ void __launch_bounds__(CW * 32) kv_combine_kernel(const AttnArgs A) {
+__global__ void __launch_bounds__(JOIN * 32) kv_combine_kernel(const AttnArgs A) {
   constexpr int ROWS = 8 * NT, E = D / 32;
   // first of all, in every thread: this grid ends only after the one before it
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Window& w = A.w;
-  const int lane = threadIdx.x & 31, G = A.group;
-  const long long id = (long long)blockIdx.x * CW + (threadIdx.x >> 5);
-  const int qh = (int)(id % w.q_heads);
-  const long long bi = id / w.q_heads;
-  const int i = (int)(bi % w.max_tokens);
-  if (bi / w.max_tokens >= w.B) return;
-  const int b = (int)(bi / w.max_tokens), h = qh / G;
-  const Seq s = sequence(w, b);
-  if (i >= s.count) return;
-  const Span p = span<D, NT>(A, s);
-  const long long units = A.prefix[w.B], workers = A.prefix[w.B + 1], pre = A.prefix[b];
-  const size_t at = (size_t)(s.first + i) * w.q_heads + qh;
+  __shared__ float sm[JOIN], sl[JOIN], so[JOIN][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = A.group;
+  const long long k = blockIdx.x, units = A.prefix[w.B], workers = A.prefix[w.B + 1];
   if (A.prefix[w.B + 2] != 0) {   // a copy never came
-#pragma unroll
-    for (int e = 0; e < E; ++e) A.out[at * D + lane * E + e] = __float2bfloat16_rn(NAN);
-    if (A.lse && lane == 0) A.lse[at] = NAN;
+    const long long n = (long long)w.N * w.q_heads;
+    for (long long x = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * (JOIN * 32) + threadIdx.x; x < n * D;
+         x += (long long)gridDim.x * gridDim.y * (JOIN * 32)) {
+      A.out[x] = __float2bfloat16_rn(NAN);
+      if (A.lse && x < n) A.lse[x] = NAN;
+    }
     return;
   }
-  const int row = i * G + qh % G, rt = row / ROWS, r = row % ROWS;
-  const long long i0 = pre + ((long long)h * p.rts + rt) * (p.tiles + OVERHEAD), i1 = i0 + OVERHEAD + p.tiles;
-  // the blocks that hold its first and its last unit with tokens
-  const long long w0 = ((i0 + OVERHEAD + 1) * workers - 1) / units, w1 = (i1 * workers - 1) / units;
-  if (w0 == w1) return;   // written already
-  const auto slot = [&](long long k) {
-    return A.part + ((size_t)k * 2 + (share_start(k, units, workers) < i0 ? 1 : 0)) * ROWS * (D + 2);
-  };
+  if (k == 0 || k >= workers) return;
+  const Start item = A.start[k];
+  const long long i0 = item.unit0;
+  // the shares that hold its first and its last unit with tokens
+  const long long w0 = quotient((i0 + OVERHEAD + 1) * workers - 1, units);
+  if (w0 != k - 1) return;
+  const long long w1 = quotient((i0 + OVERHEAD + item.tiles) * workers - 1, units);
+  const int first_row = item.rt * ROWS + 8 * blockIdx.y;
+  const int rows = min(item.count * G - first_row, 8);
+  if (rows <= 0) return;
+  const int team = rows > 4 ? 1 : rows > 2 ? 2 : rows > 1 ? 4 : 8;   // warps of a row
+  const int mine = warp / team, r = 8 * blockIdx.y + mine;
   float m = NO_FRAME, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (long long k0 = w0; k0 <= w1; k0 += 32) {
-    const int n = (int)min(w1 - k0 + 1, 32ll);
+  const int per = (int)((w1 - w0 + team) / team);   // shares of a warp
+  const long long from = w0 + (long long)(warp % team) * per, last = mine < rows ? min(w1, from + per - 1) : from - 1;
+  // share w0 is the second of its block unless it begins with the item
+  const int second = share_start(w0, units, workers) < i0;
+  for (long long k0 = from; k0 <= last; k0 += 32) {
+    const int n = (int)min(last - k0 + 1, 32ll);
     float mk = NO_FRAME, lk = 0.f;
-    const float* part = nullptr;
-    if (lane < n) {
-      part = slot(k0 + lane);
-      mk = part[2 * r], lk = part[2 * r + 1];
-    }
+    const float* part = A.part + ((size_t)(k0 + lane) * 2 + (k0 + lane == w0 ? second : 0)) * (ROWS * (D + 2));
+    if (lane < n) mk = part[2 * r], lk = part[2 * r + 1];
     float top = fmaxf(m, mk);
 #pragma unroll
     for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -873,10 +883,14 @@ __global__ void __launch_bounds__(CW * 32) kv_combine_kernel(const AttnArgs A) {
     m = top;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] *= f;
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(part), k));
-      const float fs = __shfl_sync(0xffffffffu, fk, k);
+    // eight at a time; those past the end are the last one again, with weight 0
+#pragma unroll 1
+    for (int x0 = 0; x0 < n; x0 += 8)
+#pragma unroll
+    for (int x1 = 0; x1 < 8; ++x1) {
+      const int x = min(x0 + x1, n - 1);
+      const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(part), x));
+      const float fx = __shfl_sync(0xffffffffu, fk, x), fs = x0 + x1 < n ? fx : 0.f;
       src += 2 * ROWS + r * D + lane * E;
       if (E == 4) {
         const float4 y = *reinterpret_cast<const float4*>(src);
@@ -888,6 +902,24 @@ __global__ void __launch_bounds__(CW * 32) kv_combine_kernel(const AttnArgs A) {
       }
     }
   }
+  if (lane == 0) sm[warp] = m, sl[warp] = l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+  __syncthreads();
+  if (warp % team || mine >= rows) return;
+  m = sm[warp];
+  for (int x = 1; x < team; ++x) m = fmaxf(m, sm[warp + x]);
+  l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int x = 0; x < team; ++x) {
+    const float f = ex2f(sm[warp + x] - m);
+    l = fmaf(sl[warp + x], f, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(so[warp + x][lane * E + e], f, o[e]);
+  }
+  const int row = first_row + mine, i = row / G;
+  const size_t at = (size_t)(item.row0 + i) * w.q_heads + item.h * G + row % G;
   const float f = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
@@ -919,6 +951,7 @@ static int sm_count() {
 }
 
 static size_t prefix_bytes(int B) { return ((size_t)(B + 3) * sizeof(long long) + 127) & ~(size_t)127; }
+static size_t start_bytes(int workers) { return (size_t)workers * sizeof(Start); }
 static size_t part_bytes(int workers, int nt, int D) { return (size_t)workers * 2 * 8 * nt * (D + 2) * sizeof(float); }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -966,8 +999,8 @@ static sv_status launch_attention(AttnArgs& A, cudaStream_t st) {
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   // launched while the first kernel still runs; waits for its results on the device
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((long long)A.w.B * A.w.max_tokens * A.w.q_heads + CW - 1) / CW));
-  cfg.blockDim = dim3(CW * 32);
+  cfg.gridDim = dim3((unsigned)A.workers, (unsigned)NT);
+  cfg.blockDim = dim3(JOIN * 32);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -997,7 +1030,8 @@ size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int
       q_heads < kv_heads || q_heads % kv_heads || q_heads / kv_heads > 64 || (head_dim != 64 && head_dim != 128))
     return 0;
   const int nt = row_tiles(max_tokens, q_heads / kv_heads);
-  return prefix_bytes(B) + part_bytes(sm_count() * blocks_per_sm(nt), nt, head_dim);
+  const int workers = sm_count() * blocks_per_sm(nt);
+  return prefix_bytes(B) + start_bytes(workers) + part_bytes(workers, nt, head_dim);
 }
 
 sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_codes, const float* k_scale,
@@ -1012,7 +1046,6 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   const Window w{seq_len, cu_tokens, page_table, B,       N,        max_tokens, max_pages,
                  num_pages, page_size, q_heads,  kv_heads, head_dim};
   if (bad_window(w) || q_stride < (long long)q_heads * head_dim || window < 0 || !isfinite(scale)) return SV_ERR_SHAPE;
-  if ((long long)B * max_tokens * q_heads > 2147483647ll) return SV_ERR_SHAPE;
   if (!aligned(q, 16) || (q_stride * 2) % 16 || !aligned(out, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) ||
       !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(seq_len, 4) || !aligned(cu_tokens, 4) ||
       !aligned(page_table, 4) || !aligned(lse, 4))
@@ -1020,7 +1053,8 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   const int nt = row_tiles(max_tokens, q_heads / kv_heads);
   const int sms = aligned(workspace, 16) ? sm_count() : 1;
   if (sms < 1) return SV_ERR_CUDA;
-  if (!aligned(workspace, 16) || workspace_bytes < prefix_bytes(B) + part_bytes(sms * blocks_per_sm(nt), nt, head_dim))
+  const int workers = sms * blocks_per_sm(nt);
+  if (!aligned(workspace, 16) || workspace_bytes < prefix_bytes(B) + start_bytes(workers) + part_bytes(workers, nt, head_dim))
     return SV_ERR_WORKSPACE;
   AttnArgs A = {};
   A.w = w;
@@ -1033,8 +1067,9 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   A.out = static_cast<__nv_bfloat16*>(out);
   A.lse = lse;
   A.prefix = static_cast<long long*>(workspace);
-  A.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + prefix_bytes(B));
-  A.workers = sms * blocks_per_sm(nt);
+  A.start = reinterpret_cast<Start*>(static_cast<char*>(workspace) + prefix_bytes(B));
+  A.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + prefix_bytes(B) + start_bytes(workers));
+  A.workers = workers;
   A.group = q_heads / kv_heads;
   A.group_mul = ((1 << 16) + A.group - 1) / A.group;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
