@@ -17,8 +17,8 @@ def row(x, token, temperature=1.0, top_n=0):
         return None
     z = x / t
     m = z.max()
-    lse = m + np.log(np.exp(z - m).sum())
-    lp = z - lse
+    lsum = np.log(np.exp(z - m).sum())     # relative to the maximum: logits may be as large as 1e38
+    lse, lp = m + lsum, (z - m) - lsum
     p = np.exp(lp)
     live = p > 0
     H = -float((p[live] * lp[live]).sum())

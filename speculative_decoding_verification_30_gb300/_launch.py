@@ -5,10 +5,13 @@ import contextlib
 
 import torch
 
+from . import SpecVerifyError
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 
 def ptr(t: torch.Tensor, name: str, dtype, device) -> int:
     """Device address of a contiguous tensor of this type on this device."""
-    from . import SpecVerifyError
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise SpecVerifyError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -22,6 +25,7 @@ def ptr(t: torch.Tensor, name: str, dtype, device) -> int:
 
 class _Here:
     """The device's current stream on the current device: nothing to set or restore."""
+    __slots__ = ("handle",)
 
     def __init__(self, handle):
         self.handle = handle
@@ -51,5 +55,5 @@ def on_device(device, stream, *tensors):
     """Context in which outputs are allocated and the call is made; gives the stream's
     handle. The caller orders `stream` after the work that produces the tensors."""
     if stream is None and device.index == torch.cuda.current_device():
-        return _Here(int(torch.cuda.current_stream().cuda_stream))
+        return _Here(_raw_stream(device.index) if _raw_stream else int(torch.cuda.current_stream().cuda_stream))
     return _there(device, stream, tensors)

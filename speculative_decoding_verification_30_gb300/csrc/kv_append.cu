@@ -20,7 +20,7 @@
 namespace svkv {
 
 constexpr int MIN_EXP = -60, MAX_EXP = 119;   // of a scale
-constexpr int QI = 4;                         // units of a thread in a query block
+constexpr int QI = 4;                         // heads of a thread in a query block
 
 struct AppendArgs {
   Window w;
@@ -77,26 +77,58 @@ __device__ __forceinline__ Unit unit_at(int u, int rot, int interleaved) {
   return t;
 }
 
-// Each product and each sum is rounded once (no contraction), so the result does not
-// depend on how the compiler groups them.
-__device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
-  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-  a = x;
+// Pairs of floats in one 64-bit register.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
-__device__ __forceinline__ void rotate_unit(float* x, const Unit& u, const AppendArgs& A, long long pos) {
-  if (u.pair < 0) return;
-  float c[8], s[8];
-  load8(A.cos + pos * (A.rot / 2) + u.pair, c);
-  load8(A.sin + pos * (A.rot / 2) + u.pair, s);
-  if (A.interleaved) {
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Sums of two packed pairs, one by one: a packed addition after a packed
+// multiplication is joined with it into one rounding.
+__device__ __forceinline__ void add_each(uint64_t p, uint64_t q, float& x, float& y) {
+  float a, b, c, d;
+  unpair(p, a, b);
+  unpair(q, c, d);
+  x = __fadd_rn(a, c);
+  y = __fadd_rn(b, d);
+}
+
+// The angles of a unit: cosines, sines and the sines' negatives, two at a time. Each
+// product and each sum of the rotation is rounded once (no contraction), so the result
+// does not depend on how the compiler groups them.
+struct Angles {
+  uint64_t c[4], s[4], n[4];
+  __device__ __forceinline__ void load(const AppendArgs& A, int u, long long pos) {
+    float x[8], y[8];
+    load8(A.cos + pos * (A.rot / 2) + u, x);
+    load8(A.sin + pos * (A.rot / 2) + u, y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rotate(x[2 * i], x[2 * i + 1], c[i], s[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) rotate(x[i], x[8 + i], c[i], s[i]);
+    for (int i = 0; i < 4; ++i) {
+      c[i] = pair(x[2 * i], x[2 * i + 1]);
+      s[i] = pair(y[2 * i], y[2 * i + 1]);
+      n[i] = pair(-y[2 * i], -y[2 * i + 1]);
+    }
   }
-}
+  // (a, b) -> (a c - b s, b c + a s); pairs are (x[i], x[8 + i]) or (x[2 i], x[2 i + 1])
+  __device__ __forceinline__ void rotate(float* x, int interleaved) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float &a0 = x[interleaved ? 4 * i : 2 * i], &a1 = x[interleaved ? 4 * i + 2 : 2 * i + 1];
+      float &b0 = x[interleaved ? 4 * i + 1 : 8 + 2 * i], &b1 = x[interleaved ? 4 * i + 3 : 9 + 2 * i];
+      const uint64_t a = pair(a0, a1), b = pair(b0, b1);
+      add_each(mul2(a, c[i]), mul2(b, n[i]), a0, a1);
+      add_each(mul2(b, c[i]), mul2(a, s[i]), b0, b1);
+    }
+  }
+};
 
 __device__ __forceinline__ uint32_t encode4(const float* x) {
   const uint16_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
@@ -124,7 +156,7 @@ __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-template <typename T, int NT, int ITEMS>
+template <typename T, int NT, int ITEMS, int IL>
 __device__ __forceinline__ void append_page(const AppendArgs& A, long long blk) {
   const Window& w = A.w;
   __shared__ uint32_t wmax[NT / 32];
@@ -135,8 +167,8 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, long long blk) 
   const int jj = (int)(blk % A.pages_per_seq), b = (int)(blk / A.pages_per_seq);
   const Seq s = sequence(w, b);
   if (s.len < 0 || s.count == 0) return;
-  const int P = w.page_size, D = w.head_dim, units = D / 16;
-  const long long j = s.len / P + jj;
+  const int P = w.page_size, D = w.head_dim, ush = D == 128 ? 3 : 2, units = 1 << ush;   // units of a head
+  const long long j = (s.len >> (__ffs(P) - 1)) + jj;
   const long long lo = max(j * P, s.len), hi = min((j + 1) * P, s.len + s.count);
   const bool first = h == 0 && !is_v && threadIdx.x == 0 && A.flag;
   if (first && jj == 0 && s.given > s.count) *A.flag = 1;
@@ -156,21 +188,34 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, long long blk) 
   const int rot = is_v ? 0 : A.rot;
 
   float y[ITEMS][16];
-  uint32_t top = 0u;
+  float big = 0.f;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const int it = i * NT + threadIdx.x, t = it / units;
+    const int it = i * NT + threadIdx.x, t = it >> ush;
     if (t < n) {
-      const Unit u = unit_at(it % units, rot, A.interleaved);
+      const Unit u = unit_at(it & (units - 1), rot, IL);
       load8(x + (size_t)t * stride + u.lo, y[i]);
       load8(x + (size_t)t * stride + u.hi, y[i] + 8);
-      rotate_unit(y[i], u, A, lo + t);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const uint32_t a = __float_as_uint(y[i][e]) & 0x7FFFFFFFu;
-        if (a < 0x7F800000u) top = max(top, a);   // finite values only
+      if (u.pair >= 0) {
+        Angles g;
+        g.load(A, u.pair, lo + t);
+        g.rotate(y[i], IL);
       }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) big = fmaxf(big, fabsf(y[i][e]));   // passes over NaN
     }
+  }
+  uint32_t top = __float_as_uint(big);
+  if (top == 0x7F800000u) {   // infinities do not count
+    top = 0u;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+      if ((i * NT + threadIdx.x) >> ush < n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t a = __float_as_uint(y[i][e]) & 0x7FFFFFFFu;
+          if (a < 0x7F800000u) top = max(top, a);
+        }
   }
   top = __reduce_max_sync(0xffffffffu, top);
   if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = top;
@@ -195,11 +240,16 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, long long blk) 
   if (threadIdx.x == 0) *scale = sc;   // every thread has read the old one before the barrier
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const int it = i * NT + threadIdx.x, t = it / units;
+    const int it = i * NT + threadIdx.x, t = it >> ush;
     if (t < n) {
-      const Unit u = unit_at(it % units, rot, A.interleaved);
+      const Unit u = unit_at(it & (units - 1), rot, IL);
+      if (pow2) {   // the same quotient, exactly
 #pragma unroll
-      for (int e = 0; e < 16; ++e) y[i][e] = pow2 ? __fmul_rn(y[i][e], inv) : __fdiv_rn(y[i][e], sc);
+        for (int e = 0; e < 16; e += 2) unpair(mul2(pair(y[i][e], y[i][e + 1]), pair(inv, inv)), y[i][e], y[i][e + 1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[i][e] = __fdiv_rn(y[i][e], sc);
+      }
       uint8_t* o = codes + (size_t)(keep + t) * D;
       *reinterpret_cast<uint2*>(o + u.lo) = encode8(y[i]);
       *reinterpret_cast<uint2*>(o + u.hi) = encode8(y[i] + 8);
@@ -207,47 +257,51 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, long long blk) 
   }
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int IL>
 __device__ __forceinline__ void rotate_queries(const AppendArgs& A, long long blk) {
   const Window& w = A.w;
   const int part = (int)(blk % A.q_blocks_per_seq), b = (int)(blk / A.q_blocks_per_seq);
   const Seq s = sequence(w, b);
-  const int D = w.head_dim, units = D / 16, per = w.q_heads * units;
-  const T* q = static_cast<const T*>(A.q);
-  T* out = static_cast<T*>(A.q_out);
+  const int D = w.head_dim, ush = D == 128 ? 3 : 2, units = 1 << ush, groups = (w.q_heads + QI - 1) / QI;
+  // the thread's token, group of QI heads and unit
+  const int it = part * NT + threadIdx.x, e = it >> ush, t = e / groups, h0 = (e - t * groups) * QI;
+  if (t >= s.count) return;
+  const Unit u = unit_at(it & (units - 1), A.rot, IL);
+  const long long pos = s.len + t;
+  const T* p = static_cast<const T*>(A.q) + (size_t)(s.first + t) * (size_t)A.q_stride + h0 * D;
+  T* o = static_cast<T*>(A.q_out) + ((size_t)(s.first + t) * w.q_heads + h0) * D;
+  const int heads = min(QI, w.q_heads - h0);
+  const bool blank = s.len < 0, past = A.rot && pos >= A.max_pos;
+  float x[QI][16];
 #pragma unroll
-  for (int i = 0; i < QI; ++i) {
-    const long long it = ((long long)part * QI + i) * NT + threadIdx.x;
-    const int t = (int)(it / per), e = (int)(it % per), h = e / units;
-    if (t >= s.count) continue;
-    const Unit u = unit_at(e % units, A.rot, A.interleaved);
-    float x[16];
-    const T* p = q + (size_t)(s.first + t) * (size_t)A.q_stride + h * D;
-    load8(p + u.lo, x);
-    load8(p + u.hi, x + 8);
-    const long long pos = s.len + t;
-    if (s.len < 0) {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = 0.f;
-    } else if (A.rot && pos >= A.max_pos) {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(0x7FC00000u);
-    } else {
-      rotate_unit(x, u, A, pos);
+  for (int i = 0; i < QI; ++i)
+    if (i < heads) {
+      load8(p + i * D + u.lo, x[i]);
+      load8(p + i * D + u.hi, x[i] + 8);
     }
-    T* o = out + ((size_t)(s.first + t) * w.q_heads + h) * D;
-    store8(o + u.lo, x);
-    store8(o + u.hi, x + 8);
-  }
+  Angles g;
+  const bool turn = u.pair >= 0 && !blank && !past;
+  if (turn) g.load(A, u.pair, pos);
+#pragma unroll
+  for (int i = 0; i < QI; ++i)
+    if (i < heads) {
+      if (turn) g.rotate(x[i], IL);
+      if (blank || past) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[i][k] = blank ? 0.f : __uint_as_float(0x7FC00000u);
+      }
+      store8(o + i * D + u.lo, x[i]);
+      store8(o + i * D + u.hi, x[i] + 8);
+    }
 }
 
-template <typename T, int NT, int ITEMS>
+template <typename T, int NT, int ITEMS, int IL>
 __global__ void __launch_bounds__(NT) kv_append_kernel(const AppendArgs A) {
   const long long blk = blockIdx.x;
   if (blk < A.kv_blocks)
-    append_page<T, NT, ITEMS>(A, blk);
+    append_page<T, NT, ITEMS, IL>(A, blk);
   else
-    rotate_queries<T, NT>(A, blk - A.kv_blocks);
+    rotate_queries<T, NT, IL>(A, blk - A.kv_blocks);
 }
 
 template <typename T, int NT, int ITEMS>
@@ -255,11 +309,14 @@ static sv_status launch_append(AppendArgs& A, cudaStream_t st) {
   const Window& w = A.w;
   A.pages_per_seq = (w.page_size - 1 + w.max_tokens + w.page_size - 1) / w.page_size;
   A.kv_blocks = 2ll * w.B * A.pages_per_seq * w.kv_heads;
-  const long long units = (long long)w.max_tokens * w.q_heads * (w.head_dim / 16);
-  A.q_blocks_per_seq = A.q ? (int)((units + NT * QI - 1) / (NT * QI)) : 0;
-  const long long blocks = A.kv_blocks + (long long)A.q_blocks_per_seq * w.B;
-  if (blocks > 2147483647ll) return SV_ERR_SHAPE;
-  kv_append_kernel<T, NT, ITEMS><<<(unsigned)blocks, NT, 0, st>>>(A);
+  const long long units = (long long)w.max_tokens * ((w.q_heads + QI - 1) / QI) * (w.head_dim / 16);
+  const long long per_seq = A.q ? (units + NT - 1) / NT : 0, blocks = A.kv_blocks + per_seq * w.B;
+  if (blocks > 2147483647ll || units > 2147483647ll - NT) return SV_ERR_SHAPE;
+  A.q_blocks_per_seq = (int)per_seq;
+  if (A.interleaved)
+    kv_append_kernel<T, NT, ITEMS, 1><<<(unsigned)blocks, NT, 0, st>>>(A);
+  else
+    kv_append_kernel<T, NT, ITEMS, 0><<<(unsigned)blocks, NT, 0, st>>>(A);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 

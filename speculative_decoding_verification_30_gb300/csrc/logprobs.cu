@@ -6,10 +6,10 @@
 // (256 bf16 or 128 fp32 logits), four groups a wave, the next wave's loads in
 // flight while the current one is reduced. Per wave it needs
 //   - each group's maximum (a warp reduction), kept in shared memory;
-//   - the online softmax sums, in the warp's own frame M = fl(m c), c = log2(e)/T:
-//     s = sum 2^(x c - M) and w = sum 2^(x c - M) (x c - M). Every exponent is one
-//     fused multiply-add, so lse = ln2 (M + log2 s) and H = ln2 (log2 s - w / s)
-//     hold for the frame as it was rounded;
+//   - the online softmax sums, in the warp's own frame M = fl(m c) for its maximum m,
+//     c = log2(e)/T: s = sum 2^(x c - M) and w = sum 2^(x c - M) (x c - M), two logits
+//     an instruction. At the end they are made relative to m (the rounding of M is
+//     known exactly): lse = m / T + ln2 log2 s and H = ln2 (log2 s - w / s);
 //   - the number of logits that come before the token's in the rank order.
 // The top n tokens of a segment lie in the n groups with the largest maxima (ties:
 // the lower group, whose ids are lower): were one outside, n groups would each hold
@@ -33,13 +33,13 @@ namespace cg = cooperative_groups;
 
 namespace svlp {
 
-constexpr int NT = 512, NW = NT / 32;
+constexpr int NT = 256, NW = NT / 32;
 constexpr int UNR = 4;                 // groups a warp loads at once
 constexpr int MAX_TOP = SV_LOGPROBS_MAX_TOP;
 constexpr int MAX_GROUPS = 2048;       // 262,144 fp32 logits in groups of 128
 constexpr int SEL_EXTRA = 16;          // the bisection stops at n..n+SEL_EXTRA groups
 constexpr int MAX_SEL = MAX_TOP + SEL_EXTRA;
-constexpr int MAX_CAND = NT;           // candidates ranked by counting
+constexpr int MAX_CAND = 512;          // candidates ranked by counting
 constexpr int MAX_CLUSTER = 8;
 constexpr float LN2 = 0.693147180559945309f;
 constexpr float LOG2E = 1.44269504088896341f;
@@ -138,56 +138,166 @@ __device__ __forceinline__ float vec_max(const uint4& v) {   // NaN if any is Na
   return max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
 }
 
-// Logits of the vector that are >= thr, as a float.
+// Logits of the vectors that are >= thr, as a float.
 template <typename T>
-__device__ __forceinline__ float count_ge(const uint4& v, float thr) {
+__device__ __forceinline__ float count_ge(const uint4 (&v)[UNR], float thr) {
   if (sizeof(T) == 2) {
     const __nv_bfloat162 t = __float2bfloat162_rn(thr);   // exact: thr is a value of the type
-    const __nv_bfloat162 a = __hadd2(__hadd2(__hge2(as_b2(v.x), t), __hge2(as_b2(v.y), t)),
-                                     __hadd2(__hge2(as_b2(v.z), t), __hge2(as_b2(v.w), t)));
-    return __low2float(a) + __high2float(a);
+    __nv_bfloat162 n = __float2bfloat162_rn(0.f);         // up to 4 UNR each: exact too
+#pragma unroll
+    for (int u = 0; u < UNR; ++u)
+      n = __hadd2(n, __hadd2(__hadd2(__hge2(as_b2(v[u].x), t), __hge2(as_b2(v[u].y), t)),
+                             __hadd2(__hge2(as_b2(v[u].z), t), __hge2(as_b2(v[u].w), t))));
+    return __low2float(n) + __high2float(n);
   }
-  float x[4];
-  unpack<float>(v, x);
-  return (float)((x[0] >= thr) + (x[1] >= thr) + (x[2] >= thr) + (x[3] >= thr));
+  int n = 0;
+#pragma unroll
+  for (int u = 0; u < UNR; ++u) {
+    float x[4];
+    unpack<float>(v[u], x);
+    n += (x[0] >= thr) + (x[1] >= thr) + (x[2] >= thr) + (x[3] >= thr);
+  }
+  return (float)n;
 }
 
-// Softmax sums in the frame M (s and w as above); m is the maximum they have seen.
+// Pairs of floats in one 64-bit register: the sums run on packed instructions.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Softmax sums relative to the maximum m: s = sum 2^((x - m) c), w = sum 2^((x - m) c) (x - m) c.
 struct Sums {
-  float M, s, w;
+  float m, s, w;
   __device__ __forceinline__ void add(float x, float c) {
-    const float u = fmaxf(fmaf(x, c, -M), U_MIN);
+    const float u = fmaxf((x - m) * c, U_MIN);
     const float e = ex2(u);
     s += e;
     w = fmaf(e, u, w);
   }
-  // the same sums in the frame M2 >= M
-  __device__ __forceinline__ void move(float M2) {
-    if (M == M2) return;
-    const float d = fmaxf(M - M2, U_MIN);
+  // the same sums relative to m2 >= m
+  __device__ __forceinline__ void move(float m2, float c) {
+    if (m == m2) return;
+    const float d = fmaxf((m - m2) * c, U_MIN);
     const float f = s > 0.f ? ex2(d) : 0.f;
     w = f * fmaf(s, d, w);
     s = f * s;
+    m = m2;
+  }
+};
+
+// The same sums, two at a time, in the frame M = fl(m c): an exponent is one fused
+// multiply-add, x c - M. Logits are raised to `floor` first, which lies 1000 below the
+// frame (weight 0), so that -inf needs no case of its own. Where no such floor exists
+// in the type, or M is so large that its rounding would matter (2^-8 at 2^16), `off` is
+// set and the sums are taken again by clamped_sums().
+struct PairSums {
+  float M = -INFINITY, floor = -INFINITY;
+  uint64_t s = 0, w = 0, c2 = 0, nm2 = 0;
+  bool off = false;
+  template <typename T>
+  __device__ __forceinline__ void move(float m, float c) {
+    float a, b, y, z;
+    unpair(s, a, b);
+    unpair(w, y, z);
+    const float M2 = m * c, d = fmaxf(M - M2, U_MIN), sum = a + b;
+    const float f = sum > 0.f ? ex2(d) : 0.f;
+    s = pair(f * sum, 0.f);
+    w = pair(f * fmaf(sum, d, y + z), 0.f);
     M = M2;
+    c2 = pair(c, c);
+    nm2 = pair(-M, -M);
+    floor = (M - fmaxf(1000.f, fabsf(M) * 0.03125f)) / c;   // below M also after its rounding
+    if (sizeof(T) == 2) floor = __bfloat162float(__float2bfloat16_rd(floor));
+    off |= !(fabsf(M) < 65536.f && floor > -1e38f);
+  }
+  __device__ __forceinline__ void add(float x0, float x1) {
+    const uint64_t u = fma2(pair(x0, x1), c2, nm2);
+    float a, b;
+    unpair(u, a, b);
+    const uint64_t e = pair(ex2(a), ex2(b));
+    s = add2(s, e);
+    w = fma2(e, u, w);
+  }
+  template <typename T>
+  __device__ __forceinline__ void add(const uint4& v) {
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+    if (sizeof(T) == 2) {
+      const __nv_bfloat162 f = __float2bfloat162_rn(floor);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 m = __hmax2(as_b2(q[i]), f);
+        const uint32_t r = *reinterpret_cast<const uint32_t*>(&m);
+        add(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        add(fmaxf(__uint_as_float(q[2 * i]), floor), fmaxf(__uint_as_float(q[2 * i + 1]), floor));
+    }
+  }
+  // Relative to m itself: x c - M = (x - m) c + d with d = m c - M, known exactly.
+  __device__ __forceinline__ Sums relative(float m, float c) const {
+    float a, b, y, z;
+    unpair(s, a, b);
+    unpair(w, y, z);
+    if (m == -INFINITY) return Sums{m, 0.f, 0.f};
+    const float d = fmaf(m, c, -M), f = ex2(-d);
+    return Sums{m, (a + b) * f, fmaf(-d, a + b, y + z) * f};
   }
 };
 
 struct Partial {   // of one CTA
-  float M, s, w;
-  int count, bad, any;
+  float m, s, w;
+  int count, bad, ntop;
 };
+
+// The lanes' partial results as one, in every lane (a butterfly: the same order always).
+__device__ __forceinline__ Partial join(Partial p, float c) {
+  float m = p.m;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  Sums b{p.m, p.s, p.w};
+  if (p.s > 0.f) b.move(m, c);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    b.s += __shfl_xor_sync(0xffffffffu, b.s, o);
+    b.w += __shfl_xor_sync(0xffffffffu, b.w, o);
+  }
+  return Partial{m, b.s, b.w, (int)__reduce_add_sync(0xffffffffu, (unsigned)p.count),
+                 (int)__reduce_or_sync(0xffffffffu, (unsigned)p.bad), (int)__reduce_add_sync(0xffffffffu, (unsigned)p.ntop)};
+}
 
 struct Smem {
   float gmax[MAX_GROUPS];
+  uint32_t key[MAX_GROUPS];
   unsigned long long cand[MAX_CAND];
   unsigned long long top[MAX_TOP];
   unsigned long long merge[MAX_CLUSTER * MAX_TOP];
   int sel[MAX_SEL];
-  float wM[NW], ws[NW], ww[NW];
-  int wcount[NW], wbad[NW];
+  Partial warps[NW];
+  Partial parts[MAX_CLUSTER];                          // the cluster's, in its first CTA
   uint32_t wmin[NW], wmax[NW];
-  int nsel, ncand;
-  Partial part;
+  int nsel, ncand, cnt[3], bad;
   unsigned long long best[NW];
 };
 
@@ -207,45 +317,75 @@ __device__ __forceinline__ unsigned long long pack_key(float x, int id) {
   return ((unsigned long long)okey(x) << 32) | (uint32_t)~(uint32_t)id;
 }
 
-// The best n (key descending) of the segment's groups [g0, g0 + G) and, in the first
-// CTA, of the loose logits, into S.top (0: none). All threads take part.
+// The thread's sums of the CTA's vectors [v0, v1) relative to m, every exponent clamped (rare).
 template <typename T>
-__device__ void select_top(Smem& S, const Row<T>& r, int g0, int G, int n, bool loose) {
-  constexpr int EPV = Elem<T>::EPV;
-  constexpr int SLOTS = MAX_GROUPS / NT;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) S.nsel = S.ncand = 0;
-  uint32_t key[SLOTS], kmin = 0xFFFFFFFFu, kmax = 0u;
+__device__ __noinline__ Sums clamped_sums(const Row<T>& r, int v0, int v1, float m, float c) {
+  Sums a{m, 0.f, 0.f};
+#pragma unroll 1
+  for (int v = v0 + threadIdx.x; v < v1; v += NT) {
+    float x[Elem<T>::EPV];
+    unpack<T>(*reinterpret_cast<const uint4*>(r.x + r.a0 + (size_t)v * Elem<T>::EPV), x);
 #pragma unroll
-  for (int i = 0; i < SLOTS; ++i) {
-    const int g = i * NT + tid;
-    key[i] = g < G ? okey(S.gmax[g]) : 0u;   // 0 lies below every key
-    if (g < G) {
-      kmin = min(kmin, key[i]);
-      kmax = max(kmax, key[i]);
-    }
+    for (int i = 0; i < Elem<T>::EPV; ++i) a.add(x[i], c);
+  }
+  return a;
+}
+
+// Logits of the lane's vectors v, v + 32, ... (UNR of them, below v1) that come before
+// the token's, id by id: for the waves that hold it, or padding.
+template <typename T>
+__device__ __noinline__ float count_by_id(const Row<T>& r, int v, int v1, float xt, int tok) {
+  float n = 0.f;
+#pragma unroll 1
+  for (int u = 0; u < UNR; ++u, v += 32) {
+    if (v >= v1) break;
+    float x[Elem<T>::EPV];
+    const int id = r.a0 + v * Elem<T>::EPV;
+    unpack<T>(*reinterpret_cast<const uint4*>(r.x + id), x);
+#pragma unroll
+    for (int i = 0; i < Elem<T>::EPV; ++i) n += x[i] > xt || (x[i] == xt && id + i < tok);
+  }
+  return n;
+}
+
+// The best n (key descending) of the segment's entries [0, G) and, in the first CTA,
+// of the loose logits, into S.top (0: none); returns how many there are. An entry is
+// the maximum of a group, or (fine) of a vector. All threads take part. The loops are
+// kept rolled: this runs once a CTA, and fetching long code costs more than running it.
+template <typename T>
+__device__ __noinline__ int select_top(Smem& S, const Row<T>& r, int g0, int G, int n, bool loose, bool fine) {
+  constexpr int EPV = Elem<T>::EPV;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
+#pragma unroll 1
+  for (int g = tid; g < G; g += NT) {
+    const uint32_t k = okey(S.gmax[g]);
+    S.key[g] = k;                       // a thread's own entries, also below
+    kmin = min(kmin, k);
+    kmax = max(kmax, k);
   }
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
-  if (lane == 0) {
-    S.wmin[warp] = kmin;
-    S.wmax[warp] = kmax;
-  }
+  if (tid == 0) S.nsel = S.ncand = S.cnt[0] = S.cnt[1] = S.cnt[2] = 0;
+  if (lane == 0) S.wmin[warp] = kmin, S.wmax[warp] = kmax;
+  if (tid < MAX_TOP) S.top[tid] = 0ull;
   __syncthreads();
-  for (int w = 0; w < NW; ++w) {
-    kmin = min(kmin, S.wmin[w]);
-    kmax = max(kmax, S.wmax[w]);
-  }
-  // lo: at least n groups reach it; hi: fewer than n do
+  kmin = __reduce_min_sync(0xffffffffu, S.wmin[lane % NW]);
+  kmax = __reduce_max_sync(0xffffffffu, S.wmax[lane % NW]);
+  // lo: at least n entries reach it; hi: fewer than n do
   uint32_t lo = kmin, hi = kmax + 1u;
   bool tied = G > n + SEL_EXTRA;
   if (!tied) lo = 0u;
-  while (tied && hi - lo > 1u) {
+  for (int step = 0; tied && hi - lo > 1u; step = step == 2 ? 0 : step + 1) {
     const uint32_t mid = lo + (hi - lo) / 2u;
     int cnt = 0;
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i)
-      if (i * NT < G) cnt += __syncthreads_count(key[i] >= mid);
+#pragma unroll 1
+    for (int g = tid; g < G; g += NT) cnt += S.key[g] >= mid;
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if (lane == 0 && cnt) atomicAdd(&S.cnt[step], cnt);
+    __syncthreads();
+    cnt = S.cnt[step];
+    if (tid == 0) S.cnt[step == 0 ? 2 : step - 1] = 0;   // read by all before this barrier, next used after another
     if (cnt >= n) {
       lo = mid;
       tied = cnt > n + SEL_EXTRA;
@@ -253,95 +393,107 @@ __device__ void select_top(Smem& S, const Row<T>& r, int g0, int G, int n, bool 
       hi = mid;
     }
   }
-  if (tied) {
-    // more than n + SEL_EXTRA groups reach lo, and fewer than n exceed it: those,
-    // then the lowest groups whose maximum is lo
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i)
-      if (key[i] > lo) S.sel[atomicAdd(&S.nsel, 1)] = i * NT + tid;
-    __syncthreads();
-    if (warp == 0) {
-      int have = S.nsel;
-      for (int g = lane; g - lane < G && have < n; g += 32) {
-        const bool eq = g < G && okey(S.gmax[g]) == lo;
-        const unsigned b = __ballot_sync(0xffffffffu, eq);
-        const int at = have + __popc(b & ((1u << lane) - 1u));
-        if (eq && at < n) S.sel[at] = g;
-        have += __popc(b);
-      }
-      if (lane == 0) S.nsel = min(have, n);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i)
-      if (i * NT + tid < G && key[i] >= lo) S.sel[atomicAdd(&S.nsel, 1)] = i * NT + tid;
-  }
+  // a tie: more than n + SEL_EXTRA entries reach lo, and fewer than n exceed it: those,
+  // then the lowest entries whose maximum is lo
+#pragma unroll 1
+  for (int g = tid; g < G; g += NT)
+    if (S.key[g] >= lo + (tied ? 1u : 0u)) S.sel[atomicAdd(&S.nsel, 1)] = g;
   __syncthreads();
+  if (tied && warp == 0) {
+    int have = S.nsel;
+    for (int g = lane; g - lane < G && have < n; g += 32) {
+      const bool eq = g < G && S.key[g] == lo;
+      const unsigned b = __ballot_sync(0xffffffffu, eq);
+      const int at = have + __popc(b & ((1u << lane) - 1u));
+      if (eq && at < n) S.sel[at] = g;
+      have += __popc(b);
+    }
+    __syncwarp();
+    if (lane == 0) S.nsel = min(have, n);
+  }
+  if (tied) __syncthreads();
   const int nsel = S.nsel;
   const uint32_t least = max(lo, KEY_NEG_INF + 1u);   // -inf is never listed
-  const int nloose = loose ? r.a0 + r.tail : 0;
-  const auto push = [&](float x, int id) {
-    if (okey(x) < least) return;
-    const int at = atomicAdd(&S.ncand, 1);
-    if (at < MAX_CAND) S.cand[at] = pack_key(x, id);
-  };
-  for (int s = warp; s < nsel; s += NW) {
-    const int v = (g0 + S.sel[s]) * 32 + lane;
-    if (v < r.nvec) {
-      float x[EPV];
-      const int id = r.a0 + v * EPV;
-      unpack<T>(*reinterpret_cast<const uint4*>(r.x + id), x);
-#pragma unroll
-      for (int i = 0; i < EPV; ++i) push(x[i], id + i);
-    }
-  }
-  if (tid < nloose) push(Elem<T>::get(r.x + loose_id(r, tid)), loose_id(r, tid));
-  if (tid < MAX_TOP) S.top[tid] = 0ull;
-  __syncthreads();
-  const int nc = S.ncand;
-  if (nc <= MAX_CAND) {
-    if (tid < nc) {
-      const unsigned long long k = S.cand[tid];
-      int before = 0;
-      for (int i = 0; i < nc; ++i) before += S.cand[i] > k;
-      if (before < n) S.top[before] = k;
-    }
-    __syncthreads();
-    return;
-  }
-  // more logits at or above the bound than are ranked by counting (rows that rise
-  // steadily, long runs of ties): n rounds, each the largest key below the last
+  // Every logit of the selected entries that is at or above the bound: first listed;
+  // if there are too many to be ranked by counting (groups only: rows that rise
+  // steadily, long runs of ties), n rounds follow, each for the largest key below the last.
   unsigned long long last = ~0ull;
-  for (int j = 0; j < n; ++j) {
+  int nc = 0;
+#pragma unroll 1
+  for (int j = -1; j < n; ++j) {
     unsigned long long best = 0ull;
+    const int items = fine ? nsel : nsel * 32;
     const auto take = [&](float x, int id) {
+      if (okey(x) < least) return;
       const unsigned long long k = pack_key(x, id);
-      if (okey(x) >= least && k < last && k > best) best = k;
+      if (j >= 0) {
+        if (k < last && k > best) best = k;
+      } else {
+        const int at = atomicAdd(&S.ncand, 1);
+        if (at < MAX_CAND) S.cand[at] = k;
+      }
     };
-    for (int s = warp; s < nsel; s += NW) {
-      const int v = (g0 + S.sel[s]) * 32 + lane;
-      if (v < r.nvec) {
-        float x[EPV];
-        const int id = r.a0 + v * EPV;
-        unpack<T>(*reinterpret_cast<const uint4*>(r.x + id), x);
+    constexpr int AHEAD = 4;   // loads on their way at once
+#pragma unroll 1
+    for (int s0 = tid; s0 < items; s0 += AHEAD * NT) {
+      uint4 y[AHEAD];
+      int id[AHEAD];
 #pragma unroll
-        for (int i = 0; i < EPV; ++i) take(x[i], id + i);
+      for (int i = 0; i < AHEAD; ++i) {
+        const int s = s0 + i * NT;
+        id[i] = -1;
+        if (s < items) {
+          const int v = fine ? g0 * 32 + S.sel[s] : (g0 + S.sel[s >> 5]) * 32 + (s & 31);
+          if (v < r.nvec) {
+            id[i] = r.a0 + v * EPV;
+            y[i] = *reinterpret_cast<const uint4*>(r.x + id[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (id[i] < 0) continue;
+        float top = vec_max<T>(y[i]);
+        if (okey(top) < least) continue;
+        float x[EPV];
+        unpack<T>(y[i], x);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) take(x[e], id[i] + e);
       }
     }
-    if (tid < nloose) take(Elem<T>::get(r.x + loose_id(r, tid)), loose_id(r, tid));
+    if (loose && tid < r.a0 + r.tail) take(Elem<T>::get(r.x + loose_id(r, tid)), loose_id(r, tid));
+    if (j < 0) {
+      __syncthreads();
+      nc = S.ncand;
+      if (nc > MAX_CAND) continue;
+      // a warp for each candidate: its place is the number of larger keys
+#pragma unroll 1
+      for (int c = warp; c < nc; c += NW) {
+        const unsigned long long k = S.cand[c];
+        int before = 0;
+#pragma unroll 1
+        for (int i = lane; i < nc; i += 32) before += S.cand[i] > k;
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (lane == 0 && before < n) S.top[before] = k;
+      }
+      break;
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
     if (lane == 0) S.best[warp] = best;
     __syncthreads();
+#pragma unroll 1
     for (int w = 0; w < NW; ++w) best = max(best, S.best[w]);
     if (tid == 0) S.top[j] = best;
     last = best;
     __syncthreads();
   }
+  __syncthreads();
+  return min(nc, n);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(NT, 2)
+__global__ void __launch_bounds__(NT, 1024 / NT)
     logprobs_kernel(const T* __restrict__ logits, int V, long long ld, const int32_t* __restrict__ tokens,
                     const float* __restrict__ temperature, int n, float* __restrict__ logprob,
                     int32_t* __restrict__ rank, float* __restrict__ entropy, float* __restrict__ lse,
@@ -370,6 +522,7 @@ __global__ void __launch_bounds__(NT, 2)
     }
     return;
   }
+  if (C > 1) cl.barrier_arrive();   // this CTA runs: its shared memory may be written
   Row<T> r;
   r.x = logits + row * ld;
   r.V = V;
@@ -380,62 +533,78 @@ __global__ void __launch_bounds__(NT, 2)
   const int groups = (r.nvec + 31) / 32;
   const int per = (groups + C - 1) / C;
   const int g0 = min(crank * per, groups), G = min(per, groups - g0);
+  const bool fine = per * 32 <= MAX_GROUPS;   // short segments keep each vector's maximum, long ones each group's
 
+  constexpr int STEP = NW * UNR;
+  const int v1 = min((g0 + G) * 32, r.nvec);     // the segment's last vector, past it
+  const uint4* const base = reinterpret_cast<const uint4*>(r.x + r.a0);
+  uint4 nxt[UNR];
+  const auto fetch = [&](int v0) {               // v0: the lane's first vector of the wave
+    if (v0 - lane + UNR * 32 <= v1) {
+#pragma unroll
+      for (int u = 0; u < UNR; ++u) nxt[u] = load_stream(base + v0 + u * 32);
+    } else {
+#pragma unroll
+      for (int u = 0; u < UNR; ++u) nxt[u] = v0 + u * 32 < v1 ? load_stream(base + v0 + u * 32) : none_vec<T>();
+    }
+  };
+  fetch((g0 + warp * UNR) * 32 + lane);          // ahead of the token's own logit
   const float xt = Elem<T>::get(r.x + tok);
   const float thr_after = succ<T>(xt);
 
-  Sums a{-INFINITY, 0.f, 0.f};
+  PairSums acc;
   float m = -INFINITY, count = 0.f;
   bool bad = false;
-  uint4 nxt[UNR];
-  const auto fetch = [&](int g) {
+#pragma unroll 1
+  for (int g = warp * UNR; g < G; g += STEP) {   // a wave: groups g .. g + UNR - 1
+    const int v0 = (g0 + g) * 32 + lane;
+    const bool whole = v0 - lane + UNR * 32 <= v1;
+    uint4 v[UNR];
 #pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-      const int v = (g0 + g + u) * 32 + lane;
-      nxt[u] = g + u < G && v < r.nvec ? load_stream(r.x + r.a0 + (size_t)v * EPV) : none_vec<T>();
+    for (int u = 0; u < UNR; ++u) v[u] = nxt[u];
+    if (g + STEP < G) fetch(v0 + STEP * 32);
+    float wm = -INFINITY;
+    if (n > 0 && !fine) {
+      float mine = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < UNR; ++u) {
+        const float x = warp_max_nan(vec_max<T>(v[u]));
+        wm = max_nan(wm, x);
+        mine = lane == u ? x : mine;
+      }
+      if (lane < UNR && g + lane < G) S.gmax[g + lane] = mine;
+    } else {
+#pragma unroll
+      for (int u = 0; u < UNR; ++u) {
+        const float x = vec_max<T>(v[u]);
+        wm = max_nan(wm, x);
+        if (n > 0 && g + u < G) S.gmax[(g + u) * 32 + lane] = x;
+      }
+      wm = warp_max_nan(wm);
     }
-  };
-  int g = warp * UNR;
-  if (g < G) fetch(g);
-  for (; g < G; g += NW * UNR) {
-    uint4 cur[UNR];
-#pragma unroll
-    for (int u = 0; u < UNR; ++u) cur[u] = nxt[u];
-    if (g + NW * UNR < G) fetch(g + NW * UNR);
-    float wm = -INFINITY, gm[UNR];
-#pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-      gm[u] = warp_max_nan(vec_max<T>(cur[u]));
-      wm = max_nan(wm, gm[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < UNR; ++u)
-      if (lane == u && g + u < G) S.gmax[g + u] = gm[u];
-    if (!(wm < INFINITY)) {   // NaN or +inf
-      bad = true;
-      break;
-    }
+    bad |= !(wm < INFINITY);   // NaN or +inf: the row's numbers do not matter any more
     if (wm > m) {
       m = wm;
-      a.move(m * c);
+      acc.move<T>(m, c);
     }
-    const bool live = m > -INFINITY;   // else nothing but -inf so far
+    if (m > -INFINITY) {       // else nothing but -inf so far
 #pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-      float x[EPV];
-      unpack<T>(cur[u], x);
-#pragma unroll
-      for (int i = 0; i < EPV; ++i)
-        if (live) a.add(x[i], c);
-      const int v = (g0 + g + u) * 32 + lane, id = r.a0 + v * EPV;
-      if (g + u >= G || v >= r.nvec) continue;   // padding: would count beside a -inf token
-      if (id + EPV <= tok || id > tok) {
-        count += count_ge<T>(cur[u], id > tok ? thr_after : xt);
-      } else {
-#pragma unroll
-        for (int i = 0; i < EPV; ++i) count += x[i] > xt || (x[i] == xt && id + i < tok);
-      }
+      for (int u = 0; u < UNR; ++u) acc.add<T>(v[u]);
     }
+    // padding would count beside a -inf token, so a wave that holds it goes id by id
+    const int id0 = r.a0 + (v0 - lane) * EPV;
+    if (whole && (unsigned)(tok - id0) >= (unsigned)(UNR * 32 * EPV))
+      count += count_ge<T>(v, id0 > tok ? thr_after : xt);
+    else
+      count += count_by_id<T>(r, v0, v1, xt, tok);
+  }
+  Sums a = acc.relative(m, c);
+  if (__syncthreads_or(acc.off)) {   // logits near the type's lowest value: once more, clamped
+    if (lane == 0) S.warps[warp].m = m;
+    __syncthreads();
+    for (int w = 0; w < NW; ++w) m = fmaxf(m, S.warps[w].m);
+    __syncthreads();
+    a = m > -INFINITY && m < INFINITY ? clamped_sums(r, g0 * 32, v1, m, c) : Sums{m, 0.f, 0.f};
   }
   if (crank == 0 && warp == 0) {
     const int nl = r.a0 + r.tail;
@@ -449,7 +618,7 @@ __global__ void __launch_bounds__(NT, 2)
     if (!(wm < INFINITY)) bad = true;
     if (!bad && wm > m) {
       m = wm;
-      a.move(m * c);
+      a.move(m, c);
     }
     if (!bad && m > -INFINITY && lane < nl) a.add(x, c);
   }
@@ -460,92 +629,76 @@ __global__ void __launch_bounds__(NT, 2)
     a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
   }
   const int wcount = __reduce_add_sync(0xffffffffu, (int)count);
-  if (lane == 0) {
-    S.wM[warp] = a.M;
-    S.ws[warp] = a.s;
-    S.ww[warp] = a.w;
-    S.wcount[warp] = wcount;
-    S.wbad[warp] = bad || isinf(a.M) != (m == -INFINITY) || a.M == INFINITY;
-  }
+  if (lane == 0)
+    S.warps[warp] = Partial{m, a.s, a.w, wcount, bad, 0};
   __syncthreads();
+  if (C > 1) cl.barrier_wait();
+  if (warp == 0) {
+    Partial p = lane < NW ? S.warps[lane] : Partial{-INFINITY, 0.f, 0.f, 0, 0, 0};
+    p = join(p, c);
+    if (lane == 0) {
+      S.bad = p.bad;
+      *cl.map_shared_rank(&S.parts[crank], 0) = p;
+    }
+  }
+  if (n > 0) {
+    __syncthreads();
+    int nt = 0;
+    if (!S.bad) nt = select_top<T>(S, r, g0, fine ? min(G * 32, r.nvec - g0 * 32) : G, n, crank == 0, fine);
+    if (tid < nt) *cl.map_shared_rank(&S.merge[crank * MAX_TOP + tid], 0) = S.top[tid];
+    if (tid == 0) cl.map_shared_rank(&S.parts[crank], 0)->ntop = nt;
+  }
+  if (C > 1)
+    cl.sync();
+  else
+    __syncthreads();
+  if (crank != 0) return;
+  // the first CTA puts the cluster together
+  const Partial p = join(lane < C ? S.parts[lane] : Partial{-INFINITY, 0.f, 0.f, 0, 0, 0}, c);
+  const float l2 = log2f(p.s), all = p.m / temp + LN2 * l2;
+  const bool none = p.bad || !(p.s > 0.f) || !(fabsf(all) < INFINITY);
   if (tid == 0) {
-    Partial p{-INFINITY, 0.f, 0.f, 0, 0, 0};
-    for (int w = 0; w < NW; ++w) {
-      p.M = fmaxf(p.M, S.wM[w]);
-      p.count += S.wcount[w];
-      p.bad |= S.wbad[w];
-    }
-    for (int w = 0; w < NW; ++w) {
-      Sums b{S.wM[w], S.ws[w], S.ww[w]};
-      if (b.s > 0.f) {
-        b.move(p.M);
-        p.s += b.s;
-        p.w += b.w;
-      }
-    }
-    S.part = p;
+    logprob[row] = none ? NAN : LN2 * fmaf(xt - p.m, c, -l2);
+    entropy[row] = none ? NAN : fmaxf(LN2 * (l2 - p.w / p.s), 0.f);
+    lse[row] = none ? NAN : all;
+    rank[row] = none ? -1 : p.count;
   }
-  __syncthreads();
-  if (n > 0 && !S.part.bad) select_top<T>(S, r, g0, G, n, crank == 0);
-  if (C > 1) cl.sync();
-  if (crank == 0) {
-    Partial p = S.part;
-    if (C > 1) {
-      for (int k = 1; k < C; ++k) {
-        const Partial* q = cl.map_shared_rank(&S.part, k);
-        p.M = fmaxf(p.M, q->M);
-        p.count += q->count;
-        p.bad |= q->bad;
+  if (n == 0) return;
+  const int total = none ? 0 : p.ntop;
+  if (tid < n && tid >= total) {   // places past the last finite logit
+    top_ids[row * n + tid] = -1;
+    top_lp[row * n + tid] = none ? NAN : -INFINITY;
+  }
+  // a warp for each list, a lane for each token: its place is its place in its own list and, in each
+  // of the others (sorted, all keys different), the number of larger keys
+  for (int list = warp; list < C && !none; list += NW) {
+    const int i = lane;
+    if (i >= S.parts[list].ntop) continue;
+    const unsigned long long k = S.merge[list * MAX_TOP + i];
+    int at = i;
+    for (int j = 0; j < C; ++j) {
+      if (j == list) continue;
+      int lo = 0, hi = S.parts[j].ntop;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (S.merge[j * MAX_TOP + mid] > k)
+          lo = mid + 1;
+        else
+          hi = mid;
       }
-      p.s = p.w = 0.f;
-      for (int k = 0; k < C; ++k) {
-        const Partial* q = cl.map_shared_rank(&S.part, k);
-        Sums b{q->M, q->s, q->w};
-        if (b.s > 0.f) {
-          b.move(p.M);
-          p.s += b.s;
-          p.w += b.w;
-        }
-      }
+      at += lo;
     }
-    const bool none = p.bad || !(p.s > 0.f);
-    const float l2 = log2f(p.s);
-    if (tid == 0) {
-      logprob[row] = none ? NAN : LN2 * (fmaf(xt, c, -p.M) - l2);
-      entropy[row] = none ? NAN : fmaxf(LN2 * (l2 - p.w / p.s), 0.f);
-      lse[row] = none ? NAN : LN2 * (p.M + l2);
-      rank[row] = none ? -1 : p.count;
-    }
-    if (n > 0) {
-      unsigned long long k = 0ull;
-      int at = tid;
-      if (C == 1 || none) {
-        if (tid < n && !none) k = S.top[tid];
-      } else {
-        if (tid < C * n) S.merge[tid] = k = cl.map_shared_rank(&S.top[0], tid / n)[tid % n];
-        __syncthreads();
-        if (tid < C * n) {
-          // equal keys are the empty places only: they keep their order
-          at = 0;
-          for (int i = 0; i < C * n; ++i) at += S.merge[i] > k || (S.merge[i] == k && i < tid);
-        } else {
-          at = n;
-        }
-      }
-      if (at < n) {
-        const float x = okey_value((uint32_t)(k >> 32));
-        top_ids[row * n + at] = k ? (int)~(uint32_t)k : -1;
-        top_lp[row * n + at] = none ? NAN : (k ? LN2 * (fmaf(x, c, -p.M) - l2) : -INFINITY);
-      }
+    if (at < n) {
+      top_ids[row * n + at] = (int)~(uint32_t)k;
+      top_lp[row * n + at] = LN2 * fmaf(okey_value((uint32_t)(k >> 32)) - p.m, c, -l2);
     }
   }
-  if (C > 1) cl.sync();   // the other CTAs' shared memory lives until it has been read
 }
 
 // --- gradient ----------------------------------------------------------------
 
 constexpr int BT = 256;      // threads
-constexpr int BU = 4;        // vectors a thread has in flight
+constexpr int BU = 8;        // vectors a thread has in flight: 49 us for 512 rows of 151,936 bf16, with four 51, with two 62
 constexpr int MAX_FIX = MAX_TOP + 1;
 
 struct Coef {
@@ -553,10 +706,14 @@ struct Coef {
   float k0, k1;               // dx = p (k0 + k1 u), u = log2 p
 };
 
-template <typename T>
-__device__ __forceinline__ float grad_at(float x, const Coef& f) {
-  const float u = fmaxf(fmaf(x, f.chi, -f.lhi) + fmaf(x, f.clo, -f.llo), U_MIN);
-  return ex2(u) * fmaf(f.k1, u, f.k0);
+// Two logits at a time.
+__device__ __forceinline__ void grad_at(float& x0, float& x1, const Coef& f) {
+  const uint64_t x = pair(x0, x1);
+  float a, b;
+  unpair(add2(fma2(x, pair(f.chi, f.chi), pair(-f.lhi, -f.lhi)), fma2(x, pair(f.clo, f.clo), pair(-f.llo, -f.llo))), a, b);
+  a = fmaxf(a, U_MIN), b = fmaxf(b, U_MIN);
+  const uint64_t k = fma2(pair(f.k1, f.k1), pair(a, b), pair(f.k0, f.k0));
+  unpair(mul2(pair(ex2(a), ex2(b)), k), x0, x1);
 }
 
 template <typename T>
@@ -571,6 +728,8 @@ __global__ void __launch_bounds__(BT)
   __shared__ int fix_id[MAX_FIX];
   __shared__ float fix_g[MAX_FIX];
   __shared__ int nfix;
+  __shared__ Coef coef;
+  __shared__ float fill;   // what a row without a gradient gets: 0, or NaN for a data error
   const long long row = blockIdx.x / chunks;
   const int e0 = (int)(blockIdx.x % chunks) * CHUNK;   // the chunk's first element
   const int tid = threadIdx.x;
@@ -578,88 +737,97 @@ __global__ void __launch_bounds__(BT)
   T* y = grad + row * gld;
   const int e1 = min(V, e0 + CHUNK);
   const int tok = tokens[row];
-  float temp = temperature ? temperature[row] : 1.f;
-  if (temp == 0.f) temp = 1.f;
-  const float L = lse[row];
-  const bool skip = tok < 0, bad = !skip && !(fabsf(L) < INFINITY);
-  Coef f{};
-  if (!skip && !bad) {
-    // Two-float products: |x c| reaches tens, and the rounding of one float there
-    // would be an error of 1e-6 in every probability.
-    f.chi = LOG2E / temp;
-    f.clo = (fmaf(-f.chi, temp, LOG2E) + LOG2E_LO) / temp;
-    f.lhi = L * LOG2E;
-    f.llo = fmaf(L, LOG2E, -f.lhi) + L * LOG2E_LO;
-    const float gl = grad_lp ? grad_lp[row] : 0.f, gh = grad_h ? grad_h[row] : 0.f;
-    float gsum = gl;
-    for (int i = 0; i < n; ++i) {
-      const int id = top_ids[row * n + i];
-      if (id >= 0 && id < V) gsum += grad_top[row * n + i];
-    }
-    f.k0 = -(gsum + gh * entropy[row]) / temp;
-    f.k1 = -gh * LN2 / temp;
-    if (tid == 0) {
-      int k = 0;
-      if (gl != 0.f && tok >= e0 && tok < e1) {
-        fix_id[k] = tok;
-        fix_g[k++] = gl / temp;
-      }
-      for (int i = 0; i < n; ++i) {
-        const int id = top_ids[row * n + i];
-        if (id >= e0 && id < e1) {
-          fix_id[k] = id;
-          fix_g[k++] = grad_top[row * n + i] / temp;
-        }
-      }
-      nfix = k;
-    }
-  } else if (tid == 0) {
-    nfix = 0;
-  }
-  __syncthreads();
-  const int nf = nfix;
-  const auto one = [&](int id, float v) {
-    float d = skip ? 0.f : bad ? NAN : grad_at<T>(v, f);
-    for (int k = 0; k < nf; ++k)
-      if (fix_id[k] == id) d += fix_g[k];
-    return Elem<T>::put(d);
-  };
   const uintptr_t xa = reinterpret_cast<uintptr_t>(x + e0), ya = reinterpret_cast<uintptr_t>(y + e0);
-  if (((xa ^ ya) & 15) != 0) {   // rows that sit differently to 16 bytes: element by element
-    for (int id = e0 + tid; id < e1; id += BT) y[id] = one(id, skip ? 0.f : Elem<T>::get(x + id));
-    return;
-  }
+  const bool alike = ((xa ^ ya) & 15) == 0;   // else element by element
   const int a0 = min((int)(((16 - (xa & 15)) & 15) / sizeof(T)), e1 - e0);
-  const int nvec = (e1 - e0 - a0) / EPV;
-  const int loose = e1 - e0 - nvec * EPV;   // a0 before the vectors, the rest after them
-  if (tid < loose) {
-    const int id = tid < a0 ? e0 + tid : e0 + nvec * EPV + tid;
-    y[id] = one(id, skip ? 0.f : Elem<T>::get(x + id));
-  }
+  const int nvec = alike ? (e1 - e0 - a0) / EPV : 0;
   uint4 v[BU];
 #pragma unroll
   for (int u = 0; u < BU; ++u) {
     const int i = u * BT + tid;
-    if (i < nvec && !skip) v[u] = *reinterpret_cast<const uint4*>(x + e0 + a0 + i * EPV);
+    if (i < nvec && tok >= 0) v[u] = *reinterpret_cast<const uint4*>(x + e0 + a0 + i * EPV);
   }
+  if (tid < 32) {   // the row's coefficients, and the places of t and the top ids in this chunk
+    float temp = temperature ? temperature[row] : 1.f;
+    if (temp == 0.f) temp = 1.f;
+    const float L = lse[row], gl = grad_lp ? grad_lp[row] : 0.f, gh = grad_h ? grad_h[row] : 0.f, H = entropy[row];
+    const int id = tid < n ? top_ids[row * n + tid] : -1;
+    const float g = tid < n && id >= 0 && id < V ? grad_top[row * n + tid] : 0.f;
+    float sum = g;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const bool here = id >= e0 && id < e1;
+    const unsigned b = __ballot_sync(0xffffffffu, here);
+    const int at = __popc(b & ((1u << tid) - 1u));
+    if (here) {
+      fix_id[at] = id;
+      fix_g[at] = g / temp;
+    }
+    if (tid == 0) {
+      const bool ok = tok >= 0 && fabsf(L) < INFINITY;
+      int k = __popc(b);
+      if (gl != 0.f && tok >= e0 && tok < e1) {
+        fix_id[k] = tok;
+        fix_g[k++] = gl / temp;
+      }
+      nfix = ok ? k : 0;
+      fill = tok < 0 ? 0.f : NAN;
+      Coef f{};
+      // Two-float products: |x c| reaches tens, and the rounding of one float there
+      // would be an error of 1e-6 in every probability. Without a gradient the
+      // coefficients make every element `fill`.
+      f.chi = LOG2E / temp;
+      f.clo = (fmaf(-f.chi, temp, LOG2E) + LOG2E_LO) / temp;
+      f.lhi = L * LOG2E;
+      f.llo = fmaf(L, LOG2E, -f.lhi) + L * LOG2E_LO;
+      f.k0 = -(gl + sum + gh * H) / temp;
+      f.k1 = -gh * LN2 / temp;
+      if (!ok) f.chi = NAN;
+      coef = f;
+    }
+  }
+  __syncthreads();
+  const int nf = nfix;
+  const Coef f = coef;
+  const bool none = f.chi != f.chi;
+  const float blank = fill;
+  const auto one = [&](int id) {
+    float d = blank, unused = 0.f;
+    if (!none) {
+      d = Elem<T>::get(x + id);
+      grad_at(d, unused, f);
+      for (int k = 0; k < nf; ++k)
+        if (fix_id[k] == id) d += fix_g[k];
+    }
+    y[id] = Elem<T>::put(d);
+  };
+  if (!alike) {
+#pragma unroll 1
+    for (int id = e0 + tid; id < e1; id += BT) one(id);
+    return;
+  }
+  const int loose = e1 - e0 - nvec * EPV;   // a0 before the vectors, the rest after them
+  if (tid < loose) one(tid < a0 ? e0 + tid : e0 + nvec * EPV + tid);
 #pragma unroll
   for (int u = 0; u < BU; ++u) {
     const int i = u * BT + tid;
     if (i >= nvec) break;
     const int id = e0 + a0 + i * EPV;
     float z[EPV];
-    if (skip || bad) {
+    if (none) {
 #pragma unroll
-      for (int j = 0; j < EPV; ++j) z[j] = skip ? 0.f : NAN;
+      for (int j = 0; j < EPV; ++j) z[j] = blank;
     } else {
       unpack<T>(v[u], z);
 #pragma unroll
-      for (int j = 0; j < EPV; ++j) z[j] = grad_at<T>(z[j], f);
+      for (int j = 0; j < EPV; j += 2) grad_at(z[j], z[j + 1], f);
       for (int k = 0; k < nf; ++k) {
         const int at = fix_id[k] - id;
+        if ((unsigned)at < (unsigned)EPV) {
 #pragma unroll
-        for (int j = 0; j < EPV; ++j)
-          if (at == j) z[j] += fix_g[k];
+          for (int j = 0; j < EPV; ++j)
+            if (at == j) z[j] += fix_g[k];
+        }
       }
     }
     uint4 o;
@@ -677,12 +845,15 @@ __global__ void __launch_bounds__(BT)
 
 static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// CTAs a row is spread over: as many as keep 304 CTAs (two on each of 152 SMs) busy,
-// while each still has two waves of groups to stream.
+// CTAs a row is spread over: as many as give every SM two, while each still has a wave
+// of groups to stream. More would cost more than they balance: a CTA spends 4 us on its
+// start, its alternatives and its share of the join (320 rows of 151,936 with 20
+// alternatives: 38 us with one CTA a row, 42 with two, 49 with four; 40 rows with eight
+// CTAs 18 us, 100 rows with four 20 us, with eight 31).
 static int cluster_size(int R, int V, int epv) {
   const int groups = (V / epv + 31) / 32;
   int c = 1;
-  while (c < MAX_CLUSTER && (long long)R * c < 304 && groups >= 2 * c * NW * UNR) c *= 2;
+  while (c < MAX_CLUSTER && (long long)R * c < 304 && groups >= c * NW * UNR) c *= 2;
   return c;
 }
 

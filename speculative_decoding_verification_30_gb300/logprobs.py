@@ -52,11 +52,10 @@ def _forward(logits, tokens, temperature, top_n, stream):
     tok = _per_row(tokens, "tokens", torch.int32, R, dev)
     temp = _per_row(temperature, "temperature", torch.float32, R, dev)
     with on_device(dev, stream, logits, tokens, temperature) as st:
-        f = torch.empty((3, *lead), dtype=torch.float32, device=dev)
+        logprob, entropy, lse = (torch.empty(lead, dtype=torch.float32, device=dev) for _ in range(3))
         rank = torch.empty(lead, dtype=torch.int32, device=dev)
         ids = torch.empty((*lead, top_n), dtype=torch.int32, device=dev)
         lps = torch.empty((*lead, top_n), dtype=torch.float32, device=dev)
-        logprob, entropy, lse = f.unbind(0)
         rc = load().spec_token_logprobs(logits.data_ptr(), _dtype_code(logits), R, V, ld, tok, temp, top_n,
                                         logprob.data_ptr(), rank.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
                                         ids.data_ptr(), lps.data_ptr(), st)
