@@ -20,7 +20,11 @@
 namespace svkv {
 
 constexpr int MIN_EXP = -60, MAX_EXP = 119;   // of a scale
-constexpr int QI = 4;                         // heads of a thread in a query block
+// Heads of a thread in a query block, and blocks of 128 threads on an SM: the loads are
+// what takes the time, so threads on the SM count more than the angles that more heads
+// would save (440 MB of prompts: 88 us with 2 and 9, 91 with 2 and 8, 93 with 2 and 10,
+// 108 with 4 and 8, 98 with 1 and 10).
+constexpr int QI = 2, BLOCKS = 9;
 
 struct AppendArgs {
   Window w;
@@ -173,22 +177,14 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, long long blk) 
   const bool first = h == 0 && !is_v && threadIdx.x == 0 && A.flag;
   if (first && jj == 0 && s.given > s.count) *A.flag = 1;
   if (lo >= hi) return;
-  const int page = page_of(w, b, j);
   const long long end = A.rot ? min(hi, (long long)A.max_pos) : hi;   // past max_pos: not stored
-  if (first && (page < 0 || end < hi)) *A.flag = 1;
-  if (page < 0 || lo >= end) return;
-  const int keep = (int)(lo - j * P), n = (int)(end - lo);   // kept tokens, new tokens
-  const size_t base = ((size_t)page * w.kv_heads + h) * (size_t)(P * D);
-  uint8_t* codes = (is_v ? A.v_codes : A.k_codes) + base;
-  float* scale = (is_v ? A.v_scale : A.k_scale) + (size_t)page * w.kv_heads + h;
-  const float old = keep ? *scale : 0.f;
+  const int keep = (int)(lo - j * P), n = (int)(max(end, lo) - lo);   // kept tokens, new tokens
   const T* x = static_cast<const T*>(is_v ? A.v : A.k) + (size_t)(s.first + (int)(lo - s.len)) *
                (size_t)(is_v ? A.v_stride : A.k_stride) + h * D;
   const long long stride = is_v ? A.v_stride : A.k_stride;
   const int rot = is_v ? 0 : A.rot;
-
+  // the values are on their way while the page is looked up
   float y[ITEMS][16];
-  float big = 0.f;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int it = i * NT + threadIdx.x, t = it >> ush;
@@ -196,6 +192,21 @@ __device__ __forceinline__ void append_page(const AppendArgs& A, long long blk) 
       const Unit u = unit_at(it & (units - 1), rot, IL);
       load8(x + (size_t)t * stride + u.lo, y[i]);
       load8(x + (size_t)t * stride + u.hi, y[i] + 8);
+    }
+  }
+  const int page = page_of(w, b, j);
+  if (first && (page < 0 || end < hi)) *A.flag = 1;
+  if (page < 0 || n == 0) return;
+  const size_t base = ((size_t)page * w.kv_heads + h) * (size_t)(P * D);
+  uint8_t* codes = (is_v ? A.v_codes : A.k_codes) + base;
+  float* scale = (is_v ? A.v_scale : A.k_scale) + (size_t)page * w.kv_heads + h;
+  const float old = keep ? *scale : 0.f;
+  float big = 0.f;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int it = i * NT + threadIdx.x, t = it >> ush;
+    if (t < n) {
+      const Unit u = unit_at(it & (units - 1), rot, IL);
       if (u.pair >= 0) {
         Angles g;
         g.load(A, u.pair, lo + t);
@@ -296,7 +307,7 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& A, long long bl
 }
 
 template <typename T, int NT, int ITEMS, int IL>
-__global__ void __launch_bounds__(NT) kv_append_kernel(const AppendArgs A) {
+__global__ void __launch_bounds__(NT, BLOCKS * 128 / NT) kv_append_kernel(const AppendArgs A) {
   const long long blk = blockIdx.x;
   if (blk < A.kv_blocks)
     append_page<T, NT, ITEMS, IL>(A, blk);
@@ -320,16 +331,18 @@ static sv_status launch_append(AppendArgs& A, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
-// Threads and units of a thread so that a full page fits the block's registers.
+// Threads and units of a thread so that a page's new tokens fit the block's registers.
+// Full pages of bf16 run faster with fewer threads and some spilled registers (440 MB of
+// prompts in pages of 64: 94.6 us against 96.5 with 256 threads of two units; pages of
+// 128: 100 against 106), those of fp32 with more (835 MB, pages of 64: 142 against 162).
 template <typename T>
 static sv_status pick_append(AppendArgs& A, cudaStream_t st) {
-  switch (A.w.page_size * A.w.head_dim / 16) {
-    case 64:
-    case 128: return launch_append<T, 128, 1>(A, st);
-    case 256: return launch_append<T, 128, 2>(A, st);
-    case 512: return launch_append<T, 128, 4>(A, st);
-    default: return launch_append<T, 256, 4>(A, st);
-  }
+  const int most = A.w.max_tokens < A.w.page_size ? A.w.max_tokens : A.w.page_size;
+  const int units = most * (A.w.head_dim / 16);
+  if (units <= 128) return launch_append<T, 128, 1>(A, st);
+  if (units <= 256) return launch_append<T, 128, 2>(A, st);
+  if (sizeof(T) == 2) return units <= 512 ? launch_append<T, 128, 4>(A, st) : launch_append<T, 256, 4>(A, st);
+  return units <= 512 ? launch_append<T, 256, 2>(A, st) : launch_append<T, 512, 2>(A, st);
 }
 
 }  // namespace svkv
