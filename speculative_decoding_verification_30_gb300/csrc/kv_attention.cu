@@ -35,8 +35,12 @@ namespace svkv {
 
 constexpr int NWARP = 4, NTHR = 32 * NWARP;   // computing; one warp more copies
 constexpr int MAX_NT = 8;      // query rows of an item: 8 NT
-constexpr int OVERHEAD = 5;    // what an item costs besides its tokens, in units
-constexpr int MIN_SHARE = 4;   // units of a block at least: shares of a few units cost more to join than they save
+// What an item costs besides its tokens, in units: its queries, its frame, its end. 64
+// sequences of 0 to 16,000 tokens: 195 us with 5, 203 with 3, 236 with 1, 198 with 8.
+constexpr int OVERHEAD = 5;
+// Units of a block at least: smaller shares cost more to join than they save (1 sequence
+// of 2,500 tokens: 13.7 us with 4, 17.5 with 1, 15.4 with 8).
+constexpr int MIN_SHARE = 4;
 // Weights are 2^(t - m) with m = LIFT below the running maximum of the exponents t,
 // and m moves only when a weight would exceed 2^TOP: they stay within fp16 (65504)
 // and the small ones keep as much of its range as there is.
@@ -89,23 +93,19 @@ template <int D, int TOK>
 struct Stage {
   uint8_t k[TOK * D], v[TOK * D];
 };
-// Blocks on an SM, and stages so that they fit its shared memory.
+// Layout of a block. Up to 24 query rows keep the queries' fragments in registers; more
+// read them from shared memory, which units of 128 tokens do half as often (32 rows of
+// 4 sequences of 131,000 tokens: 160 us against 173 with 64; 48 and 64 rows have no
+// registers for it: prompt chunks 699 us against 650). Narrow heads take 128 tokens too, so
+// that a unit is worth its barriers. Blocks on an SM: as many as registers allow (64
+// sequences of up to 16,000 tokens, 20 rows: 197 us with three, 215 with two; 256 single
+// tokens, 6 rows: 60 us with four, 69 with three).
 template <int D, int NT>
 struct Shape {
-#ifndef MT128
-#define MT128 (NT == 4 ? 2 : 1)
-#endif
-  static constexpr int MT = D == 128 ? MT128 : 2;        // runs of 16 tokens of a warp
+  static constexpr int MT = D == 64 || NT == 4 ? 2 : 1;  // runs of 16 tokens of a warp
   static constexpr int TOK = 16 * MT * NWARP;            // cached tokens of a unit
-  #ifdef BLK
-  static constexpr int BLOCKS = BLK;
-#else
   static constexpr int BLOCKS = NT <= 2 ? 4 : NT <= 3 ? 3 : 2;
-#endif
-  #ifndef QR
-#define QR 3
-#endif
-  static constexpr bool QREG = NT <= QR;                  // query fragments in registers
+  static constexpr bool QREG = NT <= 3;                  // query fragments in registers
   static constexpr int PSTRIDE = 16 * (NT | 1);          // bytes of a token's weights: odd multiples of 16 spread the banks
   // the queries' and the weights' buffers are one where the queries move on to registers
   static constexpr int QBYTES = 8 * NT * D * 2, PBYTES = TOK * PSTRIDE, PAT = QREG ? 0 : QBYTES;
@@ -113,9 +113,9 @@ struct Shape {
   static constexpr int FIXED = 1024 /* stages lie on 1024-byte boundaries */ + BUF + 8 * NT * 4 * (1 + NWARP);
   static constexpr int ROOM = (227 * 1024) / BLOCKS - 1024 - 256 - FIXED;
   static constexpr int FIT = ROOM / (int)(sizeof(Stage<D, TOK>) + sizeof(Meta) + 8);
-  static constexpr int NS = FIT > 6 ? 6 : FIT;
+  static constexpr int NS = FIT > 6 ? 6 : FIT;           // stages
   static constexpr size_t SMEM = (sizeof(Stage<D, TOK>) + sizeof(Meta) + 8) * NS + FIXED;
-  static_assert(NS >= 2, "three stages at least");
+  static_assert(NS >= 2, "one unit on its way while one is worked on");
 };
 
 // Units of sequence b: kv_heads * row tiles * (OVERHEAD + token tiles), at least one
@@ -934,11 +934,7 @@ static int row_tiles(int max_tokens, int group) {
   const long long nt = ((long long)max_tokens * group + 7) / 8;
   return nt <= 4 ? (int)nt : nt <= 6 ? 6 : MAX_NT;
 }
-#ifdef BLK
-static int blocks_per_sm(int nt) { return BLK; }
-#else
 static int blocks_per_sm(int nt) { return nt <= 2 ? 4 : nt <= 3 ? 3 : 2; }   // Shape::BLOCKS
-#endif
 
 static int sm_count() {
   int dev = 0, n = 0;
