@@ -14,6 +14,7 @@ SOURCES = [os.path.join(CSRC, "spec_verify.cu"), os.path.join(CSRC, "spec_verify
            os.path.join(CSRC, "kv_attention.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "sv_device.cuh"), os.path.join(CSRC, "keyhist.cuh"),
                   os.path.join(CSRC, "launch_cache.h"), os.path.join(CSRC, "kv_common.cuh"),
+                  os.path.join(CSRC, "kv_wide.cuh"),
                   os.path.join(os.path.dirname(HERE), "include", "spec_kv.h"), os.path.join(CSRC, "fstream.cuh"),
                   os.path.join(os.path.dirname(HERE), "include", "spec_verify.h"),
                   os.path.join(os.path.dirname(HERE), "include", "spec_lm_head.h"),

@@ -134,11 +134,6 @@ struct Angles {
   }
 };
 
-__device__ __forceinline__ uint32_t encode4(const float* x) {
-  const uint16_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint16_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
-  return (uint32_t)a | ((uint32_t)b << 16);
-}
 __device__ __forceinline__ uint2 encode8(const float* x) { return make_uint2(encode4(x), encode4(x + 4)); }
 
 __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float r) {

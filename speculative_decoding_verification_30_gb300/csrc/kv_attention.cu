@@ -124,9 +124,8 @@ struct Shape {
 struct Span {
   int tile0, tiles, rts;
 };
-template <int D, int NT>
-__device__ __forceinline__ Span span(const AttnArgs& A, const Seq& s) {
-  constexpr int TOK = Shape<D, NT>::TOK;
+template <int ROWS, int TOK>
+__device__ __forceinline__ Span span_of(const AttnArgs& A, const Seq& s) {
   Span p{0, 0, 0};
   if (s.count == 0) return p;
   const long long cap = (long long)A.w.max_pages * A.w.page_size;
@@ -135,12 +134,12 @@ __device__ __forceinline__ Span span(const AttnArgs& A, const Seq& s) {
   lo = min(lo, end);
   p.tile0 = (int)(lo / TOK);
   p.tiles = max((int)((end + TOK - 1) / TOK) - p.tile0, 1);
-  p.rts = (s.count * A.group + 8 * NT - 1) / (8 * NT);   // below 2^30
+  p.rts = (s.count * A.group + ROWS - 1) / ROWS;   // below 2^30
   return p;
 }
-template <int D, int NT>
+template <int ROWS, int TOK>
 __device__ __forceinline__ long long units_of(const AttnArgs& A, int b) {
-  const Span p = span<D, NT>(A, sequence(A.w, b));
+  const Span p = span_of<ROWS, TOK>(A, sequence(A.w, b));
   return (long long)A.w.kv_heads * p.rts * (p.tiles + OVERHEAD);
 }
 
@@ -150,6 +149,63 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 }
 __device__ __forceinline__ long long share_start(long long w, long long units, long long workers) {
   return quotient(w * units, workers);
+}
+
+// The block's share [u0, u1) of all units, and the sequence in which it begins with the
+// units before that (in shared memory); whether it has one. Block 0 leaves the
+// sequences' units for the join.
+template <int ROWS, int TOK, int THREADS>
+__device__ __forceinline__ bool find_share(const AttnArgs& A, long long* s_sum, int* s_b, long long* s_pre, long long& u0,
+                                           long long& u1) {
+  constexpr int WARPS = THREADS / 32;
+  const Window& w = A.w;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  long long mine = 0;
+  for (int b = tid; b < w.B; b += THREADS) mine += units_of<ROWS, TOK>(A, b);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s_sum[warp] = mine;
+  if (tid == 0) *s_b = -1;
+  __syncthreads();
+  long long units = 0;
+#pragma unroll 1
+  for (int i = 0; i < WARPS; ++i) units += s_sum[i];
+  const long long workers = min((long long)A.workers, max(units / MIN_SHARE, 1ll));
+  const long long wk = blockIdx.x;
+  u0 = share_start(wk, units, workers);
+  u1 = wk < workers ? share_start(wk + 1, units, workers) : u0;
+  long long before = 0;
+  for (int b0 = 0; b0 < w.B; b0 += THREADS) {
+    const int b = b0 + tid;
+    const long long u = b < w.B ? units_of<ROWS, TOK>(A, b) : 0;
+    long long inc = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    __syncthreads();   // the last values have been read
+    if (lane == 31) s_sum[warp] = inc;
+    __syncthreads();
+    long long pre = before;
+#pragma unroll 1
+    for (int i = 0; i < warp; ++i) pre += s_sum[i];
+#pragma unroll 1
+    for (int i = 0; i < WARPS; ++i) before += s_sum[i];
+    pre += inc - u;
+    if (u > 0 && u0 >= pre && u0 < pre + u) {
+      *s_b = b;
+      *s_pre = pre;
+    }
+    if (blockIdx.x == 0 && b < w.B) A.prefix[b] = pre;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    A.prefix[w.B] = units;
+    A.prefix[w.B + 1] = workers;
+    A.prefix[w.B + 2] = 0;
+  }
+  __syncthreads();
+  return u0 < u1 && *s_b >= 0;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -316,66 +372,25 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
   __shared__ int s_b;
   const Window& w = A.w;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const int G = A.group;
-
-  // --- shares: total units, then the sequence in which this block's share begins
-  constexpr int ALL = NTHR + 32;
-  long long mine = 0;
-  for (int b = tid; b < w.B; b += ALL) mine += units_of<D, NT>(A, b);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_sum[warp] = mine;
   if (tid == 0) {
-    s_b = -1;
     for (int i = 0; i < NS; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(full + i)) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  __syncthreads();
-  long long units = 0;
-#pragma unroll
-  for (int i = 0; i <= NWARP; ++i) units += s_sum[i];
-    const long long workers = min((long long)A.workers, max(units / MIN_SHARE, 1ll));
+  const int G = A.group;
+  constexpr int ALL = NTHR + 32;
   const long long wk = blockIdx.x;
-  const long long u0 = share_start(wk, units, workers), u1 = wk < workers ? share_start(wk + 1, units, workers) : u0;
-  long long before = 0;
-  for (int b0 = 0; b0 < w.B; b0 += ALL) {
-    const int b = b0 + tid;
-    const long long u = b < w.B ? units_of<D, NT>(A, b) : 0;
-    long long inc = u;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    __syncthreads();   // the last values have been read
-    if (lane == 31) s_sum[warp] = inc;
-    __syncthreads();
-    long long pre = before;
-    for (int i = 0; i < warp; ++i) pre += s_sum[i];
-    for (int i = 0; i <= NWARP; ++i) before += s_sum[i];
-    pre += inc - u;
-    if (u > 0 && u0 >= pre && u0 < pre + u) {
-      s_b = b;
-      s_pre = pre;
-    }
-    if (blockIdx.x == 0 && b < w.B) A.prefix[b] = pre;
-  }
-  if (blockIdx.x == 0 && tid == 0) {
-    A.prefix[w.B] = units;
-    A.prefix[w.B + 1] = workers;
-    A.prefix[w.B + 2] = 0;
-  }
-  __syncthreads();
+  long long u0, u1;
+  const bool some = find_share<ROWS, TOK, ALL>(A, s_sum, &s_b, &s_pre, u0, u1);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (u0 >= u1 || s_b < 0) return;
+  if (!some) return;
 
   if (warp == NWARP) {
     // --- the copying warp. Unit `cu` is number `ct` of item (cb, ch, cr)
     int cb = s_b;
     long long cu = u0;
     Seq cs = sequence(w, cb);
-    Span cp = span<D, NT>(A, cs);
+    Span cp = span_of<ROWS, TOK>(A, cs);
     int ct, ch, cr;
     {
       const long long x = u0 - s_pre;
@@ -468,7 +483,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
               if (cu < u1) {
                 do {
                   cs = sequence(w, ++cb);
-                  cp = span<D, NT>(A, cs);
+                  cp = span_of<ROWS, TOK>(A, cs);
                 } while (cp.rts == 0 && cb + 1 < w.B);
               }
             }
@@ -823,6 +838,10 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
   }
 }
 
+}  // namespace svkv
+#include "kv_wide.cuh"
+namespace svkv {
+
 // Joins the shares of the items that several blocks worked on. At most one item is cut
 // at the start of each share: block (k, n) looks whether share k is the second of its
 // item, and if so takes rows 8 n .. 8 n + 7 of it. Eight warps share the rows that are
@@ -929,12 +948,17 @@ __global__ void __launch_bounds__(JOIN * 32) kv_combine_kernel(const AttnArgs A)
 
 static sv::LaunchCache g_attn_cache;
 
-// Tiles of 8 rows of an item: just enough for the window, at most MAX_NT.
-static int row_tiles(int max_tokens, int group) {
+// Rows of a window from which the wide kernel takes over (head_dim 128).
+constexpr int WIDE_ROWS = 129;
+
+// Tiles of 8 rows of an item: just enough for the window, at most MAX_NT, or those of
+// the wide kernel.
+static int row_tiles(int max_tokens, int group, int head_dim) {
   const long long nt = ((long long)max_tokens * group + 7) / 8;
+  if (head_dim == wide::D && nt * 8 >= WIDE_ROWS) return wide::NT;
   return nt <= 4 ? (int)nt : nt <= 6 ? 6 : MAX_NT;
 }
-static int blocks_per_sm(int nt) { return nt <= 2 ? 4 : nt <= 3 ? 3 : 2; }   // Shape::BLOCKS
+static int blocks_per_sm(int nt) { return nt <= 2 ? 4 : nt <= 3 ? 3 : nt <= MAX_NT ? 2 : 1; }   // Shape::BLOCKS
 
 static int sm_count() {
   int dev = 0, n = 0;
@@ -979,21 +1003,18 @@ static bool code_map(CUtensorMap* map, const void* codes, const Window& w, int T
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NT>
-static sv_status launch_attention(AttnArgs& A, cudaStream_t st) {
-  constexpr size_t SMEM = Shape<D, NT>::SMEM;
+// The kernel's shared-memory limit, raised once per device.
+static bool raise_smem(const void* fn, size_t bytes) {
   int dev = 0, done = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      g_attn_cache.get(dev, reinterpret_cast<const void*>(kv_attention_kernel<D, NT>), SMEM, 0, &done, [](int* v) {
-        *v = 1;
-        return cudaFuncSetAttribute(kv_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
-      }) != cudaSuccess)
-    return SV_ERR_CUDA;
-  CUtensorMap map_k, map_v;
-  if (!code_map(&map_k, A.k_codes, A.w, Shape<D, NT>::TOK) || !code_map(&map_v, A.v_codes, A.w, Shape<D, NT>::TOK)) return SV_ERR_CUDA;
-  kv_attention_kernel<D, NT><<<A.workers, NTHR + 32, SMEM, st>>>(A, map_k, map_v);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  // launched while the first kernel still runs; waits for its results on the device
+  return cudaGetDevice(&dev) == cudaSuccess && g_attn_cache.get(dev, fn, bytes, 0, &done, [&](int* v) {
+    *v = 1;
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  }) == cudaSuccess;
+}
+
+// The join: launched while the first kernel still runs, waits for its results on the device.
+template <int D, int NT>
+static sv_status launch_combine(AttnArgs& A, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)A.workers, (unsigned)NT);
   cfg.blockDim = dim3(JOIN * 32);
@@ -1004,6 +1025,28 @@ static sv_status launch_attention(AttnArgs& A, cudaStream_t st) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, NT>, A) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+template <int D, int NT>
+static sv_status launch_attention(AttnArgs& A, cudaStream_t st) {
+  constexpr size_t SMEM = Shape<D, NT>::SMEM;
+  CUtensorMap map_k, map_v;
+  if (!raise_smem(reinterpret_cast<const void*>(kv_attention_kernel<D, NT>), SMEM) ||
+      !code_map(&map_k, A.k_codes, A.w, Shape<D, NT>::TOK) || !code_map(&map_v, A.v_codes, A.w, Shape<D, NT>::TOK))
+    return SV_ERR_CUDA;
+  kv_attention_kernel<D, NT><<<A.workers, NTHR + 32, SMEM, st>>>(A, map_k, map_v);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  return launch_combine<D, NT>(A, st);
+}
+
+static sv_status launch_wide(AttnArgs& A, cudaStream_t st) {
+  CUtensorMap map_k, map_v;
+  if (!raise_smem(reinterpret_cast<const void*>(wide::kv_wide_kernel), wide::SMEM) ||
+      !code_map(&map_k, A.k_codes, A.w, wide::TOK) || !code_map(&map_v, A.v_codes, A.w, wide::TOK))
+    return SV_ERR_CUDA;
+  wide::kv_wide_kernel<<<A.workers, wide::THREADS, wide::SMEM, st>>>(A, map_k, map_v);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  return launch_combine<wide::D, wide::NT>(A, st);
 }
 
 template <int D>
@@ -1025,7 +1068,7 @@ size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int
   if (B < 1 || B > 65535 || max_tokens < 1 || max_tokens > (1 << 24) || kv_heads < 1 || kv_heads > 256 ||
       q_heads < kv_heads || q_heads % kv_heads || q_heads / kv_heads > 64 || (head_dim != 64 && head_dim != 128))
     return 0;
-  const int nt = row_tiles(max_tokens, q_heads / kv_heads);
+  const int nt = row_tiles(max_tokens, q_heads / kv_heads, head_dim);
   const int workers = sm_count() * blocks_per_sm(nt);
   return prefix_bytes(B) + start_bytes(workers) + part_bytes(workers, nt, head_dim);
 }
@@ -1046,7 +1089,7 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
       !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(seq_len, 4) || !aligned(cu_tokens, 4) ||
       !aligned(page_table, 4) || !aligned(lse, 4))
     return SV_ERR_ALIGN;
-  const int nt = row_tiles(max_tokens, q_heads / kv_heads);
+  const int nt = row_tiles(max_tokens, q_heads / kv_heads, head_dim);
   const int sms = aligned(workspace, 16) ? sm_count() : 1;
   if (sms < 1) return SV_ERR_CUDA;
   const int workers = sms * blocks_per_sm(nt);
@@ -1069,5 +1112,6 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   A.group = q_heads / kv_heads;
   A.group_mul = ((1 << 16) + A.group - 1) / A.group;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (nt == wide::NT) return launch_wide(A, st);
   return head_dim == 128 ? pick_attention<128>(nt, A, st) : pick_attention<64>(nt, A, st);
 }

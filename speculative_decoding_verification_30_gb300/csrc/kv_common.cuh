@@ -2,6 +2,7 @@
 // attention kernels (definitions in include/spec_kv.h).
 #pragma once
 
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -37,6 +38,13 @@ __device__ __forceinline__ int page_of(const Window& w, int b, long long j) {
   if (j >= w.max_pages) return -1;
   const int p = w.page_table[(size_t)b * w.max_pages + j];
   return p >= 0 && p < w.num_pages ? p : -1;
+}
+
+// Four values as e4m3 codes: to nearest even, beyond 448 to 448, NaN stays NaN.
+__device__ __forceinline__ uint32_t encode4(const float* x) {
+  const uint16_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint16_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+  return (uint32_t)a | ((uint32_t)b << 16);
 }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -1,0 +1,639 @@
+// kv_wide.cuh -- attention of many query rows over the paged 8-bit cache (prompt
+// chunks): included by kv_attention.cu, whose schedule and join it shares.
+//
+// With some hundred query rows the products outweigh the cache's bytes, so they run on
+// the 5th-generation tensor cores: 4 head_dim flops for each (row, key). An item has up
+// to 256 rows, two tiles of 128 that take turns: while one is in its softmax the tensor
+// cores work for the other. Per unit of 128 tokens:
+//   S = Q K^T  on e4m3 codes as they lie in the cache: a bf16 query has 8 significant
+//              bits and is the sum of two e4m3 numbers (4 bits each, scaled so that the
+//              row's largest element is in [2^7, 2^8)), so S takes two products and no
+//              key is widened;
+//   softmax    a thread to a row: S from TMEM, weights to TMEM as fp16 over S;
+//   O += P V   weights from TMEM, values widened to fp16 (exactly) by two warps into
+//              shared memory, where head_dim runs along the rows.
+// O stays in TMEM and is scaled there when a row's frame moves.
+// Warps: 0 copies (TMA), 1 issues the products, 2-3 widen values, 4-7 and 8-11 are the
+// two tiles' rows. Every wait is bounded; one that runs out stops the block, and the
+// join makes every output NaN.
+#pragma once
+
+namespace svkv {
+namespace wide {
+
+constexpr int D = 128, TOK = 128, ROWS = 256, NT = ROWS / 8;
+constexpr int THREADS = 384, NK = 3, NV = 2, NM = 8;   // stages of keys, of values, of a unit's facts
+constexpr int TILE8 = TOK * D, TILE16 = 2 * TILE8;
+// instruction descriptors: fp32 accumulator, M = 128, N = 128; e4m3 x e4m3, and fp16 x
+// fp16 with the second operand's rows along N
+constexpr uint32_t ID_QK = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t ID_PV = ID_QK | (1u << 16);
+
+struct Item {                 // what the rows need of an item
+  int row0, count, i0, r0, h, slot, flags, pad;
+};
+struct __align__(16) Ctl {
+  Meta meta[NM];
+  Item item[NM];
+  unsigned long long kfull[NK], kempty[NK], vfull[NV], vempty[NV], wfull[NV], wempty[NV];
+  unsigned long long sfull[2], pfull[2], qfull[2], ofull[2], ready[NM], done;
+  // NaN values of units that only some rows see: (item, token, chunk of 16, mask)
+  int nan_count;
+  int4 nan[64];
+  uint32_t taddr;
+  int err;
+  long long sum[THREADS / 32], pre;
+  int start_b;
+};
+constexpr int SMEM = 1024 + 4 * TILE8 + NK * TILE8 + NV * TILE8 + NV * TILE16 + (int)sizeof(Ctl);
+static_assert(SMEM <= 227 * 1024, "one block on an SM");
+
+__device__ __forceinline__ void arrive(unsigned long long* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void expect(unsigned long long* b, int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+// Waits for a phase unless another wait of the block has run out.
+__device__ __forceinline__ bool wait(unsigned long long* b, uint32_t parity, volatile int* err) {
+  const uint32_t at = smem_u32(b);
+  if (arrived(at, parity)) return true;
+  const uint64_t t0 = now_ns();
+  while (!arrived(at, parity)) {
+    if (*err) return false;
+    if (now_ns() - t0 > WAIT_NS) {
+      *err = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_warp(unsigned long long* b, uint32_t parity, volatile int* err) {
+  return __all_sync(0xffffffffu, wait(b, parity, err));
+}
+__device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void commit(unsigned long long* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+// Shared-memory descriptor, 128-byte swizzle: groups of eight 128-byte rows 1024 bytes
+// apart; `lead` between the blocks of 64 fp16 along N (rows along N only).
+__device__ __forceinline__ uint64_t desc(uint32_t at, uint32_t lead) {
+  return (uint64_t)((at >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void mma_qk(uint32_t d, uint64_t a, uint64_t b, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(ID_QK), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(ID_PV), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ float code_value(uint32_t c) {   // one e4m3 code
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3);
+  return __low2float(__half2(h));
+}
+
+// Largest exponent of a row's logits in a unit. `s`: the row's 128 columns of TMEM.
+template <bool MASK>
+__device__ __forceinline__ float largest(const Meta& M, uint32_t s, float rs, int hi, int lo) {
+  float best = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t x[32];
+    tmem_ld32(x, s + 32 * c);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const float4 run = M.run[2 * c + half];
+      const float a = rs * run.x;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float y = fmaf(__uint_as_float(x[16 * half + k]), a, run.y);
+        const int at = 32 * c + 16 * half + k;
+        if (!MASK || (at <= hi && at > lo && run.w == 0.f)) best = fmaxf(best, y);
+      }
+    }
+  }
+  return best;
+}
+
+// A row's weights in the frame m, written over its logits as fp16 (a quarter's weights
+// cover only columns that have been read); their sum without the value scales.
+template <bool MASK>
+__device__ __forceinline__ float weights(const Meta& M, uint32_t s, float rs, float m, int hi, int lo) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t x[32], p[16];
+    tmem_ld32(x, s + 32 * c);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const float4 run = M.run[2 * c + half];
+      const float a = rs * run.x, b = run.y - m;
+      float part = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        float y[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y[e] = fmaf(__uint_as_float(x[16 * half + k + e]), a, b);
+          const int at = 32 * c + 16 * half + k + e;
+          if (MASK && (at > hi || at <= lo || run.w != 0.f)) y[e] = -INFINITY;
+          y[e] = ex2f(y[e]);
+          part += y[e];
+        }
+        p[8 * half + k / 2] = pack_h2(y[0], y[1]);
+      }
+      sum = fmaf(part, run.z, sum);
+    }
+    tmem_st16(s + 16 * c, p);
+  }
+  return sum;
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+    kv_wide_kernel(const AttnArgs A, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  unsigned char* sq = smem;                       // [tile][high, low][row][d] e4m3
+  unsigned char* sk = sq + 4 * TILE8;             // [stage][token][d]
+  unsigned char* sv = sk + NK * TILE8;            // [stage][token][d]
+  unsigned char* sw = sv + NV * TILE8;            // [stage][d / 64][token][64] fp16
+  Ctl& C = *reinterpret_cast<Ctl*>(sw + NV * TILE16);
+  volatile int* err = &C.err;
+  const Window& w = A.w;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = A.group;
+
+  if (tid == 0) {
+    const auto init = [](unsigned long long* b, int n) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
+    };
+    for (int i = 0; i < NK; ++i) init(&C.kfull[i], 1), init(&C.kempty[i], 1);
+    for (int i = 0; i < NV; ++i) init(&C.vfull[i], 1), init(&C.vempty[i], 2), init(&C.wfull[i], 2), init(&C.wempty[i], 1);
+    for (int t = 0; t < 2; ++t) init(&C.sfull[t], 1), init(&C.pfull[t], 4), init(&C.qfull[t], 4), init(&C.ofull[t], 1);
+    for (int i = 0; i < NM; ++i) init(&C.ready[i], 1);
+    init(&C.done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    C.err = 0;
+    C.nan_count = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&C.taddr)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    before_sync();
+  }
+  long long u0, u1;
+  const bool some = find_share<ROWS, TOK, THREADS>(A, C.sum, &C.start_b, &C.pre, u0, u1);
+  after_sync();
+  const uint32_t tmem = C.taddr;   // S (and P) of tile t at columns 128 t, O at 256 + 128 t
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (!some) {
+  } else if (warp == 0) {
+    // --- copies
+    int cb = C.start_b;
+    long long cu = u0;
+    Seq cs = sequence(w, cb);
+    Span cp = span_of<ROWS, TOK>(A, cs);
+    int ct, ch, cr;
+    {
+      const long long x = u0 - C.pre;
+      const int per = cp.tiles + OVERHEAD;
+      const long long item = quotient(x, per);
+      ct = (int)(x - item * per);
+      ch = (int)quotient(item, cp.rts);
+      cr = (int)(item - (long long)ch * cp.rts);
+      if (lane == 0) A.start[blockIdx.x] = Start{u0 - ct, cp.tiles, ch, cr, cs.first, cs.count, 0};
+    }
+    int entry = -1, window_b = -1, window_h = -1, window0 = 0;
+    float eks = 1.f, elv = 0.f, einv = 1.f;
+    const int P = w.page_size, shift = __ffs(P) - 1, box = min(P, TOK);
+    int j = 0, ni = 0;   // units, items
+    bool ok = true;
+    for (;; ++j) {
+      if (ct < OVERHEAD) {
+        cu += OVERHEAD - ct;
+        ct = OVERHEAD;
+      }
+      const bool on = cu < u1;
+      const int ks_ = j % NK, vs_ = j % NV;
+      Meta& M = C.meta[j % NM];
+      if (j >= NK) ok = wait_warp(&C.kempty[ks_], (uint32_t)(j / NK - 1) & 1, err);
+      if (!ok) break;
+      if (!on) {
+        if (lane == 0) {
+          M.flags = END;
+          C.item[ni % NM].flags = END;
+          arrive(&C.kfull[ks_]);
+        }
+        if (j >= NV) ok = wait_warp(&C.vempty[vs_], (uint32_t)(j / NV - 1) & 1, err);
+        if (lane == 0) {
+          arrive(&C.vfull[vs_]);
+          arrive(&C.ready[ni % NM]);
+        }
+        break;
+      }
+      const int tok0 = (cp.tile0 + ct - OVERHEAD) * TOK;
+      const int live = cs.len < 0 ? 0 : (int)min(cs.len + cs.count - tok0, (long long)TOK);
+      const int j0 = tok0 >> shift, j1 = (tok0 + TOK - 1) >> shift;
+      if (cb != window_b || j0 < window0 || j1 >= window0 + 32) {
+        window_b = cb;
+        window_h = -1;
+        window0 = j0;
+        entry = page_of(w, cb, (long long)j0 + lane);
+      }
+      if (ch != window_h) {
+        window_h = ch;
+        const size_t at = (size_t)max(entry, 0) * w.kv_heads + ch;
+        const float vs = entry < 0 ? 1.f : A.v_scale[at];
+        eks = entry < 0 ? 1.f : A.k_scale[at];
+        elv = log2f(vs);
+        einv = __frcp_rn(vs);
+      }
+      const int from = ((tok0 + (16 * lane & (TOK - 1))) >> shift) - window0;
+      const int page = __shfl_sync(0xffffffffu, entry, from);
+      const float ks = __shfl_sync(0xffffffffu, eks, from), lv = __shfl_sync(0xffffffffu, elv, from),
+                  inv = __shfl_sync(0xffffffffu, einv, from);
+      const bool gap = __any_sync(0xffffffffu, page < 0);
+      if (lane < TOK / 16) M.run[lane] = make_float4(ks, lv, inv, page < 0 ? 1.f : 0.f);
+      const int at = tok0 + (lane * box & (TOK - 1));
+      const int pg = __shfl_sync(0xffffffffu, entry, (at >> shift) - window0);
+      const bool mine = lane * box < TOK && pg >= 0 && at - tok0 < live;
+      const int bytes = __popc(__ballot_sync(0xffffffffu, mine)) * box * D;
+      if (lane == 0) {
+        const long long item0 = cu - ct, item1 = item0 + OVERHEAD + cp.tiles;
+        const bool first = ct == OVERHEAD || cu == u0;
+        const bool masked = gap || cs.len < 0 || tok0 + TOK - 1 > cs.len || (A.window && tok0 <= cs.len + cs.count - 1 - A.window);
+        M.flags = (first ? FIRST : 0) | (cu + 1 == item1 || cu + 1 == u1 ? LAST : 0) | (masked ? MASKED : 0);
+        const long long hi = cs.len < 0 ? -FAR : cs.len - tok0;
+        M.hi0 = (int)min(hi, FAR);
+        M.lo0 = A.window ? (int)max(min(hi - A.window, FAR), -FAR) : (int)-FAR;
+        M.live = live;
+        M.pad = tok0;
+        if (first) {
+          Item& I = C.item[ni % NM];
+          I.row0 = cs.first;
+          I.count = cs.count;
+          I.i0 = cr * ROWS / G;
+          I.r0 = cr * ROWS % G;
+          I.h = ch;
+          I.slot = u0 < item0 ? 1 : 0;
+          I.flags = u0 <= item0 + OVERHEAD && u1 >= item1 ? WHOLE : 0;
+          arrive(&C.ready[ni % NM]);
+        }
+        M.slot = ni + (first ? 0 : -1);
+        expect(&C.kfull[ks_], bytes);
+      }
+      ni += ct == OVERHEAD || cu == u0;
+      __syncwarp();
+      const int y = (pg * w.kv_heads + ch) * P + (at & (P - 1)), d = (at - tok0) * D;
+      if (mine) copy_box(smem_u32(sk + ks_ * TILE8) + d, &map_k, y, smem_u32(&C.kfull[ks_]));
+      if (j >= NV) ok = wait_warp(&C.vempty[vs_], (uint32_t)(j / NV - 1) & 1, err);
+      if (!ok) {
+        ++j;
+        break;
+      }
+      if (lane == 0) expect(&C.vfull[vs_], bytes);
+      __syncwarp();
+      if (mine) copy_box(smem_u32(sv + vs_ * TILE8) + d, &map_v, y, smem_u32(&C.vfull[vs_]));
+      ++cu;
+      if (++ct == cp.tiles + OVERHEAD) {
+        ct = 0;
+        if (++cr == cp.rts) {
+          cr = 0;
+          if (++ch == w.kv_heads) {
+            ch = 0;
+            if (cu < u1) {
+              do {
+                cs = sequence(w, ++cb);
+                cp = span_of<ROWS, TOK>(A, cs);
+              } while (cp.rts == 0 && cb + 1 < w.B);
+            }
+          }
+        }
+      }
+    }
+    if (*err) {   // let the copies land that were asked for (each wait bounded)
+      __syncwarp();
+      if (lane == 0) {
+        A.prefix[w.B + 2] = 1;
+        int never = 0;
+        for (int i = max(0, j - NK); i < j; ++i) wait(&C.kfull[i % NK], (uint32_t)(i / NK) & 1, &never);
+        for (int i = max(0, j - NV); i < j; ++i) wait(&C.vfull[i % NV], (uint32_t)(i / NV) & 1, &never);
+      }
+    }
+  } else if (warp == 1) {
+    // --- products, issued by one thread
+    if (lane == 0) {
+      int items = 0;
+      const auto qk = [&](int t, int j) {
+        const uint32_t q0 = smem_u32(sq + 2 * t * TILE8), k0 = smem_u32(sk + (j % NK) * TILE8);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            mma_qk(tmem + 128 * t, desc(q0 + part * TILE8 + 32 * k, 0), desc(k0 + 32 * k, 0), part | k);
+        commit(&C.sfull[t]);
+      };
+      // unit j's first product for tile t needs the keys, and new queries if an item begins
+      const auto begin = [&](int j) {
+        if (!wait(&C.kfull[j % NK], (uint32_t)(j / NK) & 1, err)) return -1;
+        return C.meta[j % NM].flags;
+      };
+      int flags = begin(0);
+      if (flags >= 0 && !(flags & END)) {
+        bool ok = true;
+        for (int t = 0; t < 2 && ok; ++t) {
+          ok = wait(&C.qfull[t], 0, err);
+          after_sync();
+          if (ok) qk(t, 0);
+        }
+        if (ok) commit(&C.kempty[0]);
+        ++items;
+        for (int j = 0; ok; ++j) {
+          const int now = flags;
+          flags = begin(j + 1);
+          if (flags < 0) break;
+          const bool more = !(flags & END), fresh = flags & FIRST;
+          ok = wait(&C.wfull[j % NV], (uint32_t)(j / NV) & 1, err);
+          if (!ok) break;
+          const uint32_t v0 = smem_u32(sw + (j % NV) * TILE16);
+          for (int t = 0; t < 2 && ok; ++t) {
+            ok = wait(&C.pfull[t], (uint32_t)j & 1, err);
+            if (!ok) break;
+            after_sync();
+#pragma unroll
+            for (int k = 0; k < TOK / 16; ++k)
+              mma_pv(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, desc(v0 + 16 * 128 * k, TOK * 128),
+                     (uint32_t)(k != 0 || !(now & FIRST)));
+            if (t == 1) commit(&C.wempty[j % NV]);
+            if (now & LAST) commit(&C.ofull[t]);
+            if (more && !fresh) qk(t, j + 1);
+          }
+          if (!ok || !more) break;
+          if (fresh) {
+            for (int t = 0; t < 2 && ok; ++t) {
+              ok = wait(&C.qfull[t], (uint32_t)items & 1, err);
+              after_sync();
+              if (ok) qk(t, j + 1);
+            }
+            ++items;
+          }
+          if (ok) commit(&C.kempty[(j + 1) % NK]);
+        }
+      }
+      // wake the rows for the END
+      commit(&C.done);
+      int never = 0;
+      wait(&C.done, 0, &never);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // --- values to fp16: 1024 chunks of 16 codes a unit
+    const int me = tid - 64;
+    for (int j = 0;; ++j) {
+      if (!wait_warp(&C.vfull[j % NV], (uint32_t)(j / NV) & 1, err)) break;
+      const Meta& M = C.meta[j % NM];
+      const int flags = M.flags;
+      if (flags & END) break;
+      if (j >= NV && !wait_warp(&C.wempty[j % NV], (uint32_t)(j / NV - 1) & 1, err)) break;
+      const unsigned char* src = sv + (j % NV) * TILE8;
+      unsigned char* dst = sw + (j % NV) * TILE16;
+#pragma unroll 4
+      for (int i = 0; i < TOK * 8 / 64; ++i) {
+        const int x = i * 64 + me, t = x >> 3, c = x & 7;   // token, chunk of 16
+        uint4 v = *reinterpret_cast<const uint4*>(src + t * 128 + ((c ^ (t & 7)) << 4));
+        if (flags & MASKED) {
+          if (t >= M.live || M.run[t >> 4].w != 0.f) v = make_uint4(0u, 0u, 0u, 0u);   // what is not there reads as zero
+          uint32_t q[4] = {v.x, v.y, v.z, v.w};
+          uint32_t nan = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t hit = ((q[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            if (hit) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                if (hit >> (8 * b) & 0x80u) {
+                  nan |= 1u << (4 * k + b);
+                  q[k] &= ~(0xFFu << (8 * b));
+                }
+            }
+          }
+          if (nan) {   // kept aside: only rows that see the token get it
+            const int n = atomicAdd(&C.nan_count, 1);
+            if (n < 64) C.nan[n] = make_int4(M.slot, M.pad + t, c, (int)nan);
+            v = make_uint4(q[0], q[1], q[2], q[3]);
+          }
+        }
+        uint32_t o[8];
+        widen(v.x, o[0], o[1]);
+        widen(v.y, o[2], o[3]);
+        widen(v.z, o[4], o[5]);
+        widen(v.w, o[6], o[7]);
+        unsigned char* row = dst + (c >> 2) * (TOK * 128) + t * 128;
+        const int k = 2 * (c & 3);
+        *reinterpret_cast<uint4*>(row + ((k ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(row + (((k + 1) ^ (t & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        arrive(&C.vempty[j % NV]);
+        arrive(&C.wfull[j % NV]);
+      }
+    }
+  } else {
+    // --- rows: thread `r` of tile `t`
+    const int t = (warp - 4) >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
+    int j = 0;
+    for (int it = 0;; ++it) {
+      if (!wait_warp(&C.ready[it % NM], (uint32_t)(it / NM) & 1, err)) break;
+      const Item& I = C.item[it % NM];
+      if (I.flags & END) break;
+      const int x = I.r0 + 128 * t + r, i = I.i0 + x / G, hd = I.h * G + x % G;
+      const bool there = i < I.count;
+      float rs;
+      {
+        uint32_t q[64];
+        if (there) {
+          const uint4* p = reinterpret_cast<const uint4*>(A.q + (size_t)(I.row0 + i) * (size_t)A.q_stride + (size_t)hd * D);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint4 v = p[k];
+            q[4 * k] = v.x, q[4 * k + 1] = v.y, q[4 * k + 2] = v.z, q[4 * k + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) q[k] = 0u;
+        }
+        uint32_t top = 0u;
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          const uint32_t a = (q[k] << 16) & 0x7FFFFFFFu, b = q[k] & 0x7FFF0000u;
+          if (a < 0x7F800000u) top = max(top, a);
+          if (b < 0x7F800000u) top = max(top, b);
+        }
+        const int e = top ? min(max((int)(top >> 23) - 127 - 7, -100), 119) : 0;
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        rs = __uint_as_float((uint32_t)(127 + e) << 23) * A.scale;
+        unsigned char* hi = sq + 2 * t * TILE8 + r * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t h[4], l[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float f[4], b[4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t u = q[8 * c + 2 * k + y];
+              f[2 * y] = __uint_as_float(u << 16) * down;
+              f[2 * y + 1] = __uint_as_float(u & 0xFFFF0000u) * down;
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (isinf(f[y])) f[y] = NAN;   // e4m3 has no infinity
+            h[k] = encode4(f);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) b[y] = f[y] - code_value(h[k] >> (8 * y) & 0xFFu);
+            l[k] = encode4(b);
+          }
+          *reinterpret_cast<uint4*>(hi + ((c ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(hi + TILE8 + ((c ^ (r & 7)) << 4)) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive(&C.qfull[t]);
+
+      float m = NO_FRAME, l = 0.f;
+      int flags = 0;
+      bool ok = true;
+      for (;; ++j) {
+        ok = wait_warp(&C.sfull[t], (uint32_t)j & 1, err);
+        if (!ok) break;
+        after_sync();
+        const Meta& M = C.meta[j % NM];
+        flags = M.flags;
+        const int hi = M.hi0 + i, lo = M.lo0 + i;
+        // the unit's largest exponent; loops over its quarters stay rolled (code that is
+        // long is fetched again by every warp)
+        float best = flags & MASKED ? largest<true>(M, ts, rs, hi, lo) : largest<false>(M, ts, rs, hi, lo);
+        if (__any_sync(0xffffffffu, best > m + TOP)) {
+          // some weight would leave its range: move the frames to the rows' maxima
+          const float m2 = fmaxf(m, best - LIFT), f = ex2f(m - m2);   // f: 0 the first time
+          if (!(flags & FIRST)) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t y[32];
+              tmem_ld32(y, to + 32 * c);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+              tmem_st32(to + 32 * c, y);
+            }
+          }
+          l *= f;
+          m = m2;
+        }
+        l += flags & MASKED ? weights<true>(M, ts, rs, m, hi, lo) : weights<false>(M, ts, rs, m, hi, lo);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(&C.pfull[t]);
+        if (flags & LAST) {
+          ++j;
+          break;
+        }
+      }
+      if (!ok) break;
+      if (!wait_warp(&C.ofull[t], (uint32_t)it & 1, err)) break;
+      after_sync();
+      const size_t at = (size_t)(I.row0 + i) * w.q_heads + hd;
+      const bool whole = I.flags & WHOLE;
+      const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      const int last_tok = C.meta[(j - 1) % NM].pad, hi = C.meta[(j - 1) % NM].hi0 + i, lo = C.meta[(j - 1) % NM].lo0 + i;
+      float* slot = A.part + ((size_t)blockIdx.x * 2 + I.slot) * ROWS * (D + 2);
+      const int row = 128 * t + r, nans = min(C.nan_count, 64);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t y[32];
+        tmem_ld32(y, to + 32 * c);
+        if (!there) continue;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+        for (int n = 0; n < nans; ++n) {
+          const int4 e = C.nan[n];
+          const int p = e.y - last_tok;
+          if (e.x == it && e.z >> 1 == c && p <= hi && p > lo)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (k >> 4 == (e.z & 1) && e.w >> (k & 15) & 1) y[k] = 0x7FC00000u;
+        }
+        if (whole) {
+          uint4* o = reinterpret_cast<uint4*>(A.out + at * D + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t z[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(y[8 * k + 2 * b]), __uint_as_float(y[8 * k + 2 * b + 1]));
+              z[b] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            o[k] = make_uint4(z[0], z[1], z[2], z[3]);
+          }
+        } else {
+          float4* o = reinterpret_cast<float4*>(slot + 2 * ROWS + row * D + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            o[k] = make_float4(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1]), __uint_as_float(y[4 * k + 2]),
+                               __uint_as_float(y[4 * k + 3]));
+        }
+      }
+      if (there) {
+        if (whole) {
+          if (A.lse) A.lse[at] = LN2F * (m + log2f(l));
+        } else {
+          slot[2 * row] = m;
+          slot[2 * row + 1] = l;
+        }
+      }
+      before_sync();
+      __syncwarp();
+    }
+  }
+  before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+}  // namespace wide
+}  // namespace svkv

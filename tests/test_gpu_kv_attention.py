@@ -244,3 +244,67 @@ def test_attention_refusals():
                 lambda: sv.spec_kv_attention(q, cache, *win, out=q.float()), lambda: sv.spec_kv_attention(q, cache, *win, lse=q)):
         with pytest.raises(sv.SpecVerifyError):
             bad()
+
+
+# --- many query rows (new tokens x query heads of a kv head, head_dim 128): the wide kernel
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("heads,kv_heads,new", [(4, 1, 64), (8, 1, 130), (7, 1, 37), (2, 2, 257), (64, 1, 4)])
+def test_many_rows(heads, kv_heads, new, page):
+    check([0, 1, 127, 128, 300], [new] * 5, heads, kv_heads, 128, page, seed=heads + page, seqs=(0, 2, 4))
+
+
+def test_many_rows_ragged_and_empty_places():
+    check([0, 1500, -1, 5, 64, 700], [90, 1, 3, 0, 200, 33], 8, 2, 128, 32, seed=30)
+    check([12000, 40], [70, 50], 4, 1, 128, 64, seed=31)            # items cut between blocks
+
+
+@pytest.mark.parametrize("window", [1, 50, 128, 1000])
+def test_many_rows_in_sliding_windows(window):
+    check([0, 500, 2000], [100, 60, 128], 4, 1, 128, 16, window=window, seed=window)
+
+
+def test_many_rows_unmapped_pages_and_scales():
+    def edit(c, t):
+        t[0, 2:5] = -1
+        t[1, :] = -1
+        t[2, 0] = 1 << 20
+        t[2, 9] = -7
+        r = np.random.default_rng(1)
+        for k in (1, 3):
+            c[k][:] = np.exp(r.normal(size=c[k].shape) * (2 if k == 1 else 6) - 4).astype(np.float32)
+    check([200, 60, 97], [70, 64, 80], 4, 1, 128, 16, seed=32, edit=edit, garbage=False)
+
+
+@pytest.mark.parametrize("gain,spread", [(1e-20, 1.0), (60.0, 1.0), (1.0, 2.0 ** 40), (1.0, 2.0 ** -40)])
+def test_many_rows_magnitudes(gain, spread):
+    check([40, 300], [100, 90], 4, 2, 128, 32, seed=33, gain=gain, spread=spread,
+          scale=0.09 if gain != 1.0 else 0.09 / (gain * spread))
+    check([400], [100], 2, 1, 128, 16, seed=34, scale=0.0)
+
+
+def test_many_rows_nan_stays_where_it_is_seen():
+    nan = float("nan")
+
+    def edit(c, t):                # tokens 52, 75 and 100 of sequence 0 are new: query i sees up to 50 + i
+        c[2][t[0][52 // 16], 0, 52 % 16, 9] = 0x7F
+        c[2][t[0][75 // 16], 1, 75 % 16, 120] = 0xFF
+        c[0][t[0][100 // 16], 1, 100 % 16, 3] = 0x7F
+        c[2][t[1][3 // 16], 0, 3, 77] = 0x7F          # seen by every query of sequence 1
+
+    def q_edit(q):
+        q[70, 1, 5] = nan
+    check([50, 200], [60, 50], 8, 2, 128, 16, seed=35, edit=edit, q_edit=q_edit, nan_ok=True)
+
+
+def test_many_rows_repeat_and_streams():
+    g, cache, sl, cu, table = make([1000, 300], [128, 65], 4, 1, 128, 64, 36)
+    q = torch.randn(193, 4, 128, generator=g).to(torch.bfloat16).to(DEV)
+    kvc, win = to_cache(cache), (_i32(sl.tolist()), _i32(cu.tolist()), _i32(table.tolist()), 128)
+    ref = sv.spec_kv_attention(q, kvc, *win)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        got = sv.spec_kv_attention(q, kvc, *win, stream=side)
+        side.synchronize()
+        assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
