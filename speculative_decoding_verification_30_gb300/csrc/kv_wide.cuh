@@ -424,41 +424,52 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (j >= NV && !wait_warp(&C.wempty[j % NV], (uint32_t)(j / NV - 1) & 1, err)) break;
       const unsigned char* src = sv + (j % NV) * TILE8;
       unsigned char* dst = sw + (j % NV) * TILE16;
-#pragma unroll 4
-      for (int i = 0; i < TOK * 8 / 64; ++i) {
-        const int x = i * 64 + me, t = x >> 3, c = x & 7;   // token, chunk of 16
-        uint4 v = *reinterpret_cast<const uint4*>(src + t * 128 + ((c ^ (t & 7)) << 4));
-        if (flags & MASKED) {
-          if (t >= M.live || M.run[t >> 4].w != 0.f) v = make_uint4(0u, 0u, 0u, 0u);   // what is not there reads as zero
-          uint32_t q[4] = {v.x, v.y, v.z, v.w};
-          uint32_t nan = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t hit = ((q[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-            if (hit) {
-#pragma unroll
-              for (int b = 0; b < 4; ++b)
-                if (hit >> (8 * b) & 0x80u) {
-                  nan |= 1u << (4 * k + b);
-                  q[k] &= ~(0xFFu << (8 * b));
-                }
-            }
-          }
-          if (nan) {   // kept aside: only rows that see the token get it
-            const int n = atomicAdd(&C.nan_count, 1);
-            if (n < 64) C.nan[n] = make_int4(M.slot, M.pad + t, c, (int)nan);
-            v = make_uint4(q[0], q[1], q[2], q[3]);
-          }
-        }
+      const auto chunk = [&](int x, const uint4& v) {
+        const int t = x >> 3, c = x & 7, k = 2 * (c & 3);   // token, chunk of 16
         uint32_t o[8];
         widen(v.x, o[0], o[1]);
         widen(v.y, o[2], o[3]);
         widen(v.z, o[4], o[5]);
         widen(v.w, o[6], o[7]);
         unsigned char* row = dst + (c >> 2) * (TOK * 128) + t * 128;
-        const int k = 2 * (c & 3);
         *reinterpret_cast<uint4*>(row + ((k ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(row + (((k + 1) ^ (t & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      };
+      const auto codes = [&](int x) {
+        return *reinterpret_cast<const uint4*>(src + (x >> 3) * 128 + (((x & 7) ^ (x >> 3 & 7)) << 4));
+      };
+      if (!(flags & MASKED)) {
+#pragma unroll 1
+        for (int i = me; i < TOK * 8; i += 256) {
+          uint4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = codes(i + 64 * k);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) chunk(i + 64 * k, v[k]);
+        }
+      } else {
+#pragma unroll 1
+        for (int x = me; x < TOK * 8; x += 64) {
+          const int t = x >> 3, c = x & 7;
+          uint4 v = codes(x);
+          if (t >= M.live || M.run[t >> 4].w != 0.f) v = make_uint4(0u, 0u, 0u, 0u);   // what is not there reads as zero
+          uint32_t q[4] = {v.x, v.y, v.z, v.w}, nan = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t hit = ((q[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            while (hit) {
+              const int b = (__ffs(hit) - 1) >> 3;
+              hit &= hit - 1;
+              nan |= 1u << (4 * k + b);
+              q[k] &= ~(0xFFu << (8 * b));
+            }
+          }
+          if (nan) {   // kept aside: only rows that see the token get it
+            const int n = atomicAdd(&C.nan_count, 1);
+            if (n < 64) C.nan[n] = make_int4(M.slot, M.pad + t, c, (int)nan);
+          }
+          chunk(x, make_uint4(q[0], q[1], q[2], q[3]));
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
