@@ -27,8 +27,9 @@
  *
  * Limits: 1 <= B <= 65535, 1 <= N <= 2^24, 1 <= max_tokens <= N, page_size 16, 32,
  * 64 or 128, head_dim 64 or 128, kv_heads 1..256, q_heads a multiple of kv_heads,
- * at most 64 kv_heads, 1 <= max_pages <= 2^20, num_pages * kv_heads < 2^31 /
- * page_size. Pointers are device pointers, owned by the caller; nothing is
+ * at most 64 kv_heads, B * max_tokens * kv_heads < 2^31, 1 <= max_pages <= 2^20,
+ * num_pages * kv_heads < 2^31 / page_size. spec_kv_append also refuses windows that
+ * would take 2^31 blocks (about B * max_tokens * (q_heads + kv_heads) * head_dim / 2^12). Pointers are device pointers, owned by the caller; nothing is
  * allocated, the calls are asynchronous on `stream` (a cudaStream_t) and read the
  * lengths on the device, so they can be captured in a graph and replayed.
  */

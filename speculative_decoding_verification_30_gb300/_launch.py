@@ -11,16 +11,19 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def ptr(t: torch.Tensor, name: str, dtype, device) -> int:
-    """Device address of a contiguous tensor of this type on this device."""
+    """Device address of a contiguous tensor of this type on this CUDA device."""
+    try:
+        if t.dtype is dtype and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise SpecVerifyError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise SpecVerifyError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise SpecVerifyError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise SpecVerifyError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise SpecVerifyError(f"{name} must be contiguous")
 
 
 class _Here:

@@ -357,6 +357,7 @@ sv_status spec_kv_append(const void* k, long long k_stride, const void* v, long 
                  num_pages, page_size, q_heads,  kv_heads, head_dim};
   if (bad_window(w) || rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 || (rot_dim && max_pos < 1))
     return SV_ERR_SHAPE;
+  if ((long long)B * max_tokens * kv_heads > 2147483647ll) return SV_ERR_SHAPE;
   const long long kw = (long long)kv_heads * head_dim, qw = (long long)q_heads * head_dim;
   if (k_stride < kw || v_stride < kw || (q && q_stride < qw) || (q && q == q_out && q_stride != qw))
     return SV_ERR_SHAPE;

@@ -1085,6 +1085,7 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   const Window w{seq_len, cu_tokens, page_table, B,       N,        max_tokens, max_pages,
                  num_pages, page_size, q_heads,  kv_heads, head_dim};
   if (bad_window(w) || q_stride < (long long)q_heads * head_dim || window < 0 || !isfinite(scale)) return SV_ERR_SHAPE;
+  if ((long long)B * max_tokens * kv_heads > 2147483647ll) return SV_ERR_SHAPE;
   if (!aligned(q, 16) || (q_stride * 2) % 16 || !aligned(out, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) ||
       !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(seq_len, 4) || !aligned(cu_tokens, 4) ||
       !aligned(page_table, 4) || !aligned(lse, 4))

@@ -2,7 +2,6 @@
 window of tokens, and the attention of the window over it (include/spec_kv.h)."""
 from __future__ import annotations
 
-import math
 from typing import NamedTuple
 
 import torch
@@ -36,36 +35,49 @@ def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"
     return a.cos().float(), a.sin().float()
 
 
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
 def _cache(kv: KVCache, device):
     """Pointers and [num_pages, kv_heads, page_size, head_dim] of a cache."""
-    k, v = kv.k_codes, kv.v_codes
-    if not isinstance(k, torch.Tensor) or k.dim() != 4 or k.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    k, ks, v, vs = kv
+    shape = getattr(k, "shape", ())
+    if len(shape) != 4 or k.dtype not in _CODES:
         raise SpecVerifyError("the codes must be [num_pages, kv_heads, page_size, head_dim] float8_e4m3fn or uint8")
-    if v.shape != k.shape or kv.k_scale.shape != k.shape[:2] or kv.v_scale.shape != k.shape[:2]:
+    if v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
         raise SpecVerifyError("keys and values must have one shape, the scales [num_pages, kv_heads]")
-    return (ptr(k, "k_codes", k.dtype, device), ptr(kv.k_scale, "k_scale", torch.float32, device),
-            ptr(v, "v_codes", k.dtype, device), ptr(kv.v_scale, "v_scale", torch.float32, device)), k.shape
+    ty = k.dtype
+    return (ptr(k, "k_codes", ty, device), ptr(ks, "k_scale", torch.float32, device), ptr(v, "v_codes", ty, device),
+            ptr(vs, "v_scale", torch.float32, device)), shape
 
 
 def _window(seq_len, cu_tokens, page_table, device):
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise SpecVerifyError("page_table must be [B, max_pages]")
-    B = page_table.shape[0]
+    """Pointers, B and max_pages of a window's tables."""
+    i32 = torch.int32
+    try:
+        B, max_pages = page_table.shape
+    except (AttributeError, ValueError):
+        raise SpecVerifyError("page_table must be [B, max_pages]") from None
     if seq_len.shape != (B,) or cu_tokens.shape != (B + 1,):
         raise SpecVerifyError("seq_len must be [B] and cu_tokens [B + 1]")
-    return (ptr(seq_len, "seq_len", torch.int32, device), ptr(cu_tokens, "cu_tokens", torch.int32, device),
-            ptr(page_table, "page_table", torch.int32, device)), B, page_table.shape[1]
+    return (ptr(seq_len, "seq_len", i32, device), ptr(cu_tokens, "cu_tokens", i32, device),
+            ptr(page_table, "page_table", i32, device)), B, max_pages
 
 
 def _heads(x, name, dtype, device, dim):
-    """(address, token stride, heads) of [N, heads, dim] with adjacent heads."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.device != device:
+    """(address, token stride, N, heads) of [N, heads, dim] with adjacent heads."""
+    try:
+        n, heads, d = x.shape
+        ts, hs, ds = x.stride()
+    except (AttributeError, ValueError):
+        raise SpecVerifyError(f"{name} must be [N, heads, {dim}] {dtype}") from None
+    if x.device != device:
         raise SpecVerifyError(f"{name} must be a CUDA tensor on {device}")
-    if x.dim() != 3 or x.shape[2] != dim or x.dtype != dtype:
+    if d != dim or x.dtype != dtype:
         raise SpecVerifyError(f"{name} must be [N, heads, {dim}] {dtype}")
-    if x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != dim):
+    if ds != 1 or (heads > 1 and hs != dim):
         raise SpecVerifyError(f"{name}: the heads of a token must be adjacent")
-    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1] * dim, x.shape[1]
+    return x.data_ptr(), ts if n > 1 else heads * dim, n, heads
 
 
 def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_tokens: torch.Tensor,
@@ -82,13 +94,13 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
     becomes 1 when a token could not be stored."""
     if not isinstance(k, torch.Tensor) or not k.is_cuda:
         raise SpecVerifyError("k must be a CUDA tensor")
-    dev, dt = k.device, _dtype_code(k)
+    dev, ty = k.device, k.dtype
+    dt = _dtype_code(k)
     cache, (pages, heads, page, dim) = _cache(kv, dev)
     win, B, max_pages = _window(seq_len, cu_tokens, page_table, dev)
-    kp, ks, kh = _heads(k, "k", k.dtype, dev, dim)
-    vp, vs, vh = _heads(v, "v", k.dtype, dev, dim)
-    N = k.shape[0]
-    if kh != heads or vh != heads or v.shape[0] != N:
+    kp, ks, N, kh = _heads(k, "k", ty, dev, dim)
+    vp, vs, vn, vh = _heads(v, "v", ty, dev, dim)
+    if kh != heads or vh != heads or vn != N:
         raise SpecVerifyError("k and v must be [N, kv_heads, head_dim] of the cache")
     rot = max_pos = 0
     cp = sp = None
@@ -97,26 +109,30 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
     if cos is not None:
         if cos.dim() != 2 or cos.shape != sin.shape:
             raise SpecVerifyError("cos and sin must be [max_pos, rot_dim / 2]")
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        max_pos, rot = cos.shape
+        rot *= 2
         cp, sp = ptr(cos, "cos", torch.float32, dev), ptr(sin, "sin", torch.float32, dev)
     fp = None if flag is None else ptr(flag, "flag", torch.int32, dev)
     with on_device(dev, stream, k, v, *kv, seq_len, cu_tokens, page_table, q, cos, sin, q_out, flag) as st:
         qp = op = None
         qs, qh = 0, heads
         if q is not None:
-            qp, qs, qh = _heads(q, "q", k.dtype, dev, dim)
-            if q.shape[0] != N:
+            qp, qs, qn, qh = _heads(q, "q", ty, dev, dim)
+            if qn != N:
                 raise SpecVerifyError("q must have the rows of k")
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+                q_out = torch.empty((N, qh, dim), dtype=ty, device=dev)
+                op = q_out.data_ptr()
             elif q_out.shape != q.shape:
                 raise SpecVerifyError("q_out must have q's shape")
-            op = ptr(q_out, "q_out", q.dtype, dev)
+            else:
+                op = ptr(q_out, "q_out", ty, dev)
         elif q_out is not None:
             raise SpecVerifyError("q_out without q")
         rc = load().spec_kv_append(kp, ks, vp, vs, qp, qs, op, dt, cp, sp, rot, max_pos, int(interleaved), *win, B, N,
                                    max_tokens, max_pages, pages, page, qh, heads, dim, *cache, fp, st)
-    _check(rc, "spec_kv_append")
+    if rc:
+        _check(rc, "spec_kv_append")
     return q_out
 
 
@@ -141,25 +157,33 @@ def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_to
     dev = q.device
     cache, (pages, heads, page, dim) = _cache(kv, dev)
     win, B, max_pages = _window(seq_len, cu_tokens, page_table, dev)
-    qp, qs, qh = _heads(q, "q", torch.bfloat16, dev, dim)
-    N = q.shape[0]
+    qp, qs, N, qh = _heads(q, "q", torch.bfloat16, dev, dim)
     if scale is None:
-        scale = 1.0 / math.sqrt(dim)
+        scale = dim ** -0.5
+    lib = load()
     with on_device(dev, stream, q, *kv, seq_len, cu_tokens, page_table, out, lse, workspace) as st:
-        need = spec_kv_attention_workspace_bytes(B, max_tokens, qh, heads, dim)
         if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            size = lib.spec_kv_attention_workspace_bytes(B, max_tokens, qh, heads, dim) or 16
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            wp = workspace.data_ptr()
+        else:
+            size, wp = workspace.numel(), ptr(workspace, "workspace", torch.uint8, dev)
         if out is None:
-            out = torch.empty(N, qh, dim, dtype=torch.bfloat16, device=dev)
+            out = torch.empty((N, qh, dim), dtype=torch.bfloat16, device=dev)
+            op = out.data_ptr()
         elif out.shape != (N, qh, dim):
             raise SpecVerifyError("out must be [N, q_heads, head_dim]")
+        else:
+            op = ptr(out, "out", torch.bfloat16, dev)
         if lse is None:
-            lse = torch.empty(N, qh, dtype=torch.float32, device=dev)
+            lse = torch.empty((N, qh), dtype=torch.float32, device=dev)
+            lp = lse.data_ptr()
         elif lse.shape != (N, qh):
             raise SpecVerifyError("lse must be [N, q_heads]")
-        rc = load().spec_kv_attention(qp, qs, *cache, *win, B, N, max_tokens, max_pages, pages, page, qh, heads, dim,
-                                      float(scale), window, ptr(out, "out", torch.bfloat16, dev),
-                                      ptr(lse, "lse", torch.float32, dev),
-                                      ptr(workspace, "workspace", torch.uint8, dev), workspace.numel(), st)
-    _check(rc, "spec_kv_attention")
+        else:
+            lp = ptr(lse, "lse", torch.float32, dev)
+        rc = lib.spec_kv_attention(qp, qs, *cache, *win, B, N, max_tokens, max_pages, pages, page, qh, heads, dim, scale,
+                                   window, op, lp, wp, size, st)
+    if rc:
+        _check(rc, "spec_kv_attention")
     return out, lse

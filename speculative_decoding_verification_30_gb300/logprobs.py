@@ -52,14 +52,17 @@ def _forward(logits, tokens, temperature, top_n, stream):
     tok = _per_row(tokens, "tokens", torch.int32, R, dev)
     temp = _per_row(temperature, "temperature", torch.float32, R, dev)
     with on_device(dev, stream, logits, tokens, temperature) as st:
-        logprob, entropy, lse = (torch.empty(lead, dtype=torch.float32, device=dev) for _ in range(3))
+        logprob = torch.empty(lead, dtype=torch.float32, device=dev)
+        entropy = torch.empty(lead, dtype=torch.float32, device=dev)
+        lse = torch.empty(lead, dtype=torch.float32, device=dev)
         rank = torch.empty(lead, dtype=torch.int32, device=dev)
         ids = torch.empty((*lead, top_n), dtype=torch.int32, device=dev)
         lps = torch.empty((*lead, top_n), dtype=torch.float32, device=dev)
         rc = load().spec_token_logprobs(logits.data_ptr(), _dtype_code(logits), R, V, ld, tok, temp, top_n,
                                         logprob.data_ptr(), rank.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
                                         ids.data_ptr(), lps.data_ptr(), st)
-    _check(rc, "spec_token_logprobs")
+    if rc:
+        _check(rc, "spec_token_logprobs")
     return TokenLogprobs(logprob, rank, entropy, lse, ids, lps)
 
 
@@ -136,5 +139,6 @@ def spec_token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse
         gld = _rows(out, "out")[2]
         rc = load().spec_token_logprobs_backward(logits.data_ptr(), _dtype_code(logits), R, V, ld, *args, n, ids, gt,
                                                  out.data_ptr(), gld, st)
-    _check(rc, "spec_token_logprobs_backward")
+    if rc:
+        _check(rc, "spec_token_logprobs_backward")
     return out
