@@ -587,10 +587,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
       m = wm;
       acc.move<T>(m, c);
     }
-    if (m > -INFINITY) {       // else nothing but -inf so far
+    if (fmaf(wm, c, -acc.M) > -160.f) {   // else every weight is 0 in fp32 (or nothing but -inf so far)
 #pragma unroll
       for (int u = 0; u < UNR; ++u) acc.add<T>(v[u]);
     }
+    if (wm < xt) continue;     // nothing here comes before the token
     // padding would count beside a -inf token, so a wave that holds it goes id by id
     const int id0 = r.a0 + (v0 - lane) * EPV;
     if (whole && (unsigned)(tok - id0) >= (unsigned)(UNR * 32 * EPV))
