@@ -29,9 +29,10 @@
  * 64 or 128, head_dim 64 or 128, kv_heads 1..256, q_heads a multiple of kv_heads,
  * at most 64 kv_heads, B * max_tokens * kv_heads < 2^31, 1 <= max_pages <= 2^20,
  * num_pages * kv_heads < 2^31 / page_size. spec_kv_append also refuses windows that
- * would take 2^31 blocks (about B * max_tokens * (q_heads + kv_heads) * head_dim / 2^12). Pointers are device pointers, owned by the caller; nothing is
- * allocated, the calls are asynchronous on `stream` (a cudaStream_t) and read the
- * lengths on the device, so they can be captured in a graph and replayed.
+ * would take 2^31 blocks (about B * max_tokens * (q_heads + kv_heads) * head_dim /
+ * 2^12). Pointers are device pointers, owned by the caller; nothing is allocated, the
+ * calls are asynchronous on `stream` (a cudaStream_t) and read the lengths on the
+ * device, so they can be captured in a graph and replayed.
  */
 #ifndef SPEC_KV_H
 #define SPEC_KV_H
@@ -74,7 +75,7 @@ sv_status spec_kv_append(const void* k, long long k_stride, const void* v, long 
                          void* k_codes, float* k_scale, void* v_codes, float* v_scale, int32_t* flag, void* stream);
 
 /* Bytes of device workspace that spec_kv_attention needs for these arguments on the
- * current device; 0 for arguments outside the limits. The workspace need not be
+ * current device; 0 for arguments outside the limits or without a device. The workspace need not be
  * cleared and holds nothing between calls; calls that may run at the same time must
  * not share one. */
 size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int kv_heads, int head_dim);
@@ -92,9 +93,13 @@ size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int
  *   lse    [N][q_heads] float (written) or NULL
  *   scale  a finite factor, usually head_dim^-1/2; window >= 0 (0: no limit)
  *   workspace: 16-byte aligned, spec_kv_attention_workspace_bytes() bytes
- * Products are formed from queries and weights in fp16 (queries scaled by a power of
- * two for each row, so their 8 significant bits are kept; weights to 11 bits) and
- * codes as they are, all sums in fp32. Repeated calls give the same bits.
+ * Products are formed from the codes as they are, from weights rounded to fp16 (11
+ * bits) and from queries scaled by a power of two for each row, all sums in fp32. With
+ * up to 128 query rows for a kv head (max_tokens * q_heads / kv_heads), or head_dim 64,
+ * queries are fp16: their 8 significant bits are kept. With more, a query element is
+ * the sum of two e4m3 numbers: it keeps its 8 bits down to 2^-9 of its row's largest
+ * element, smaller ones are off by at most 2^-17 of that, and an infinite one counts as
+ * NaN. Repeated calls give the same bits.
  * Every wait for a copy is bounded (0.2 s); if one runs out, all outputs are NaN.
  * Returns SV_ERR_NULL, SV_ERR_SHAPE, SV_ERR_ALIGN or SV_ERR_WORKSPACE before
  * launching, SV_ERR_CUDA when the tensor-map encoder or a launch fails. */

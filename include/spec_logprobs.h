@@ -17,8 +17,8 @@
  * token) is skipped: it is not read, its outputs are 0 (rank and ids -1) and its
  * gradient is 0. A data error in a row (a NaN or +inf logit, a row that is -inf
  * everywhere, a token >= V, a temperature that is negative, NaN or +inf, or so
- * small that a finite logit over it overflows) is reported in band: NaN outputs
- * with rank and ids -1.
+ * small that 1 / T or lse leaves fp32) is reported in band: NaN outputs with rank and
+ * ids -1. The lowest finite value of the type is a logit like any other.
  *
  * Pointers are device pointers, owned by the caller; the calls allocate nothing,
  * keep no state and are asynchronous on `stream` (a cudaStream_t).

@@ -960,7 +960,7 @@ static int row_tiles(int max_tokens, int group, int head_dim) {
 }
 static int blocks_per_sm(int nt) { return nt <= 2 ? 4 : nt <= 3 ? 3 : nt <= MAX_NT ? 2 : 1; }   // Shape::BLOCKS
 
-static int sm_count() {
+static int sm_count() try {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (g_attn_cache.get(dev, reinterpret_cast<const void*>(&sm_count), 0, 0, &n, [&](int* v) {
@@ -968,6 +968,8 @@ static int sm_count() {
       }) != cudaSuccess)
     return 0;
   return n;
+} catch (...) {   // no exception passes the C entry points
+  return 0;
 }
 
 static size_t prefix_bytes(int B) { return ((size_t)(B + 3) * sizeof(long long) + 127) & ~(size_t)127; }
@@ -1004,12 +1006,14 @@ static bool code_map(CUtensorMap* map, const void* codes, const Window& w, int T
 }
 
 // The kernel's shared-memory limit, raised once per device.
-static bool raise_smem(const void* fn, size_t bytes) {
+static bool raise_smem(const void* fn, size_t bytes) try {
   int dev = 0, done = 0;
   return cudaGetDevice(&dev) == cudaSuccess && g_attn_cache.get(dev, fn, bytes, 0, &done, [&](int* v) {
     *v = 1;
     return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   }) == cudaSuccess;
+} catch (...) {
+  return false;
 }
 
 // The join: launched while the first kernel still runs, waits for its results on the device.
@@ -1070,7 +1074,7 @@ size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int
     return 0;
   const int nt = row_tiles(max_tokens, q_heads / kv_heads, head_dim);
   const int workers = sm_count() * blocks_per_sm(nt);
-  return prefix_bytes(B) + start_bytes(workers) + part_bytes(workers, nt, head_dim);
+  return workers < 1 ? 0 : prefix_bytes(B) + start_bytes(workers) + part_bytes(workers, nt, head_dim);
 }
 
 sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_codes, const float* k_scale,

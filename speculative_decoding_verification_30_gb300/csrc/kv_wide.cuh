@@ -8,7 +8,8 @@
 //   S = Q K^T  on e4m3 codes as they lie in the cache: a bf16 query has 8 significant
 //              bits and is the sum of two e4m3 numbers (4 bits each, scaled so that the
 //              row's largest element is in [2^7, 2^8)), so S takes two products and no
-//              key is widened;
+//              key is widened; exact for elements down to 2^-9 of the row's largest,
+//              smaller ones end at the codes' spacing, 2^-17 of that;
 //   softmax    a thread to a row: S from TMEM, weights to TMEM as fp16 over S;
 //   O += P V   weights from TMEM, values widened to fp16 (exactly) by two warps into
 //              shared memory, where head_dim runs along the rows.
@@ -37,9 +38,10 @@ struct __align__(16) Ctl {
   Item item[NM];
   unsigned long long kfull[NK], kempty[NK], vfull[NV], vempty[NV], wfull[NV], wempty[NV];
   unsigned long long sfull[2], pfull[2], qfull[2], ofull[2], ready[NM], done;
-  // NaN values of units that only some rows see: (item, token, chunk of 16, mask)
-  int nan_count;
-  int4 nan[64];
+  // NaN values of units that only some rows see: a bit for each element of a token, and
+  // the unit (+ 1) that last had any
+  uint4 nan[NV][TOK];
+  int nan_unit[NV];
   uint32_t taddr;
   int err;
   long long sum[THREADS / 32], pre;
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     C.err = 0;
-    C.nan_count = 0;
+    for (int i = 0; i < NV; ++i) C.nan_unit[i] = 0;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&C.taddr)) : "memory");
@@ -294,7 +296,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         M.hi0 = (int)min(hi, FAR);
         M.lo0 = A.window ? (int)max(min(hi - A.window, FAR), -FAR) : (int)-FAR;
         M.live = live;
-        M.pad = tok0;
         if (first) {
           Item& I = C.item[ni % NM];
           I.row0 = cs.first;
@@ -306,7 +307,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           I.flags = u0 <= item0 + OVERHEAD && u1 >= item1 ? WHOLE : 0;
           arrive(&C.ready[ni % NM]);
         }
-        M.slot = ni + (first ? 0 : -1);
         expect(&C.kfull[ks_], bytes);
       }
       ni += ct == OVERHEAD || cu == u0;
@@ -464,10 +464,9 @@ __global__ void __launch_bounds__(THREADS, 1)
               q[k] &= ~(0xFFu << (8 * b));
             }
           }
-          if (nan) {   // kept aside: only rows that see the token get it
-            const int n = atomicAdd(&C.nan_count, 1);
-            if (n < 64) C.nan[n] = make_int4(M.slot, M.pad + t, c, (int)nan);
-          }
+          // kept aside: only rows that see the token get it
+          reinterpret_cast<unsigned short*>(&C.nan[j % NV][t])[c] = (unsigned short)nan;
+          if (nan) *reinterpret_cast<volatile int*>(&C.nan_unit[j % NV]) = j + 1;
           chunk(x, make_uint4(q[0], q[1], q[2], q[3]));
         }
       }
@@ -544,6 +543,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane == 0) arrive(&C.qfull[t]);
 
       float m = NO_FRAME, l = 0.f;
+      uint32_t bad[4] = {0u, 0u, 0u, 0u};   // elements of O that a NaN value reaches
       int flags = 0;
       bool ok = true;
       for (;; ++j) {
@@ -573,6 +573,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           m = m2;
         }
         l += flags & MASKED ? weights<true>(M, ts, rs, m, hi, lo) : weights<false>(M, ts, rs, m, hi, lo);
+        if (flags & MASKED) {
+          // the stage holds unit j until both tiles' weights are there
+          ok = wait_warp(&C.wfull[j % NV], (uint32_t)(j / NV) & 1, err);
+          if (!ok) break;
+          if (*reinterpret_cast<volatile int*>(&C.nan_unit[j % NV]) == j + 1)
+            for (int p = max(lo + 1, 0); p <= min(hi, TOK - 1); ++p) {
+              const uint4 b = C.nan[j % NV][p];
+              bad[0] |= b.x, bad[1] |= b.y, bad[2] |= b.z, bad[3] |= b.w;
+            }
+        }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         before_sync();
         __syncwarp();
@@ -588,9 +598,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const size_t at = (size_t)(I.row0 + i) * w.q_heads + hd;
       const bool whole = I.flags & WHOLE;
       const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      const int last_tok = C.meta[(j - 1) % NM].pad, hi = C.meta[(j - 1) % NM].hi0 + i, lo = C.meta[(j - 1) % NM].lo0 + i;
       float* slot = A.part + ((size_t)blockIdx.x * 2 + I.slot) * ROWS * (D + 2);
-      const int row = 128 * t + r, nans = min(C.nan_count, 64);
+      const int row = 128 * t + r;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t y[32];
@@ -598,14 +607,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!there) continue;
 #pragma unroll
         for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-        for (int n = 0; n < nans; ++n) {
-          const int4 e = C.nan[n];
-          const int p = e.y - last_tok;
-          if (e.x == it && e.z >> 1 == c && p <= hi && p > lo)
+        const uint32_t b = c == 0 ? bad[0] : c == 1 ? bad[1] : c == 2 ? bad[2] : bad[3];
+        if (b)
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (k >> 4 == (e.z & 1) && e.w >> (k & 15) & 1) y[k] = 0x7FC00000u;
-        }
+          for (int k = 0; k < 32; ++k)
+            if (b >> k & 1) y[k] = 0x7FC00000u;
         if (whole) {
           uint4* o = reinterpret_cast<uint4*>(A.out + at * D + 32 * c);
 #pragma unroll

@@ -38,13 +38,17 @@ def rope_tables(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda"
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
+def _shape(t):
+    return getattr(t, "shape", None)
+
+
 def _cache(kv: KVCache, device):
     """Pointers and [num_pages, kv_heads, page_size, head_dim] of a cache."""
     k, ks, v, vs = kv
     shape = getattr(k, "shape", ())
     if len(shape) != 4 or k.dtype not in _CODES:
         raise SpecVerifyError("the codes must be [num_pages, kv_heads, page_size, head_dim] float8_e4m3fn or uint8")
-    if v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
+    if _shape(v) != shape or _shape(ks) != shape[:2] or _shape(vs) != shape[:2]:
         raise SpecVerifyError("keys and values must have one shape, the scales [num_pages, kv_heads]")
     ty = k.dtype
     return (ptr(k, "k_codes", ty, device), ptr(ks, "k_scale", torch.float32, device), ptr(v, "v_codes", ty, device),
@@ -58,7 +62,7 @@ def _window(seq_len, cu_tokens, page_table, device):
         B, max_pages = page_table.shape
     except (AttributeError, ValueError):
         raise SpecVerifyError("page_table must be [B, max_pages]") from None
-    if seq_len.shape != (B,) or cu_tokens.shape != (B + 1,):
+    if _shape(seq_len) != (B,) or _shape(cu_tokens) != (B + 1,):
         raise SpecVerifyError("seq_len must be [B] and cu_tokens [B + 1]")
     return (ptr(seq_len, "seq_len", i32, device), ptr(cu_tokens, "cu_tokens", i32, device),
             ptr(page_table, "page_table", i32, device)), B, max_pages
@@ -107,7 +111,7 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
     if (cos is None) != (sin is None):
         raise SpecVerifyError("cos and sin come together")
     if cos is not None:
-        if cos.dim() != 2 or cos.shape != sin.shape:
+        if len(_shape(cos) or ()) != 2 or cos.shape != _shape(sin):
             raise SpecVerifyError("cos and sin must be [max_pos, rot_dim / 2]")
         max_pos, rot = cos.shape
         rot *= 2

@@ -297,6 +297,20 @@ def test_many_rows_nan_stays_where_it_is_seen():
     check([50, 200], [60, 50], 8, 2, 128, 16, seed=35, edit=edit, q_edit=q_edit, nan_ok=True)
 
 
+@pytest.mark.parametrize("window", [0, 40])
+def test_many_rows_many_nan(window):
+    def edit(c, t):                # a NaN in every element of four in five of the new tokens, some in all
+        for p in range(50, 110):
+            for h in range(2):
+                if p % 5:
+                    c[2][t[0][p // 16], h, p % 16, (p * 7 + h) % 128] = 0x7F
+                if p == 100 + h:
+                    c[2][t[0][p // 16], h, p % 16] = 0xFF
+        for p in range(240, 250):
+            c[2][t[1][p // 16], 1, p % 16, ::p % 4 + 2] = 0x7F
+    check([50, 200], [60, 50], 8, 2, 128, 16, seed=36, edit=edit, window=window, nan_ok=True)
+
+
 def test_many_rows_repeat_and_streams():
     g, cache, sl, cu, table = make([1000, 300], [128, 65], 4, 1, 128, 64, 36)
     q = torch.randn(193, 4, 128, generator=g).to(torch.bfloat16).to(DEV)
