@@ -120,7 +120,23 @@ __device__ __forceinline__ float code_value(uint32_t c) {   // one e4m3 code
   return __low2float(__half2(h));
 }
 
-// Largest exponent of a row's logits in a unit. `s`: the row's 128 columns of TMEM.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Two floats in one 64-bit register, for the packed instructions.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+
+// Largest exponent of a row's logits in a unit. `s`: the row's 128 columns of TMEM; rs >= 0,
+// so within a run of 16 tokens, whose scales are the same, the largest product has it.
 template <bool MASK>
 __device__ __forceinline__ float largest(const Meta& M, uint32_t s, float rs, int hi, int lo) {
   float best = -INFINITY;
@@ -131,13 +147,19 @@ __device__ __forceinline__ float largest(const Meta& M, uint32_t s, float rs, in
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const float4 run = M.run[2 * c + half];
-      const float a = rs * run.x;
+      float top = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float y = fmaf(__uint_as_float(x[16 * half + k]), a, run.y);
-        const int at = 32 * c + 16 * half + k;
-        if (!MASK || (at <= hi && at > lo && run.w == 0.f)) best = fmaxf(best, y);
+      for (int k = 0; k < 16; k += 2) {
+        float y[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int at = 32 * c + 16 * half + k + e;
+          y[e] = __uint_as_float(x[16 * half + k + e]);
+          if (MASK && (at > hi || at <= lo || run.w != 0.f)) y[e] = -INFINITY;
+        }
+        top = max3(top, y[0], y[1]);
       }
+      if (!MASK || top > -INFINITY) best = fmaxf(best, fmaf(top, rs * run.x, run.y));
     }
   }
   return best;
@@ -156,21 +178,28 @@ __device__ __forceinline__ float weights(const Meta& M, uint32_t s, float rs, fl
     for (int half = 0; half < 2; ++half) {
       const float4 run = M.run[2 * c + half];
       const float a = rs * run.x, b = run.y - m;
-      float part = 0.f;
+      const uint64_t a2 = pair(a, a), b2 = pair(b, b);
+      uint64_t part = 0;
 #pragma unroll
       for (int k = 0; k < 16; k += 2) {
+        uint64_t y2;
         float y[2];
+        asm("fma.rn.f32x2 %0, %1, %2, %3;"
+            : "=l"(y2)
+            : "l"(pair(__uint_as_float(x[16 * half + k]), __uint_as_float(x[16 * half + k + 1]))), "l"(a2), "l"(b2));
+        unpair(y2, y[0], y[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          y[e] = fmaf(__uint_as_float(x[16 * half + k + e]), a, b);
           const int at = 32 * c + 16 * half + k + e;
           if (MASK && (at > hi || at <= lo || run.w != 0.f)) y[e] = -INFINITY;
           y[e] = ex2f(y[e]);
-          part += y[e];
         }
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(part) : "l"(part), "l"(pair(y[0], y[1])));
         p[8 * half + k / 2] = pack_h2(y[0], y[1]);
       }
-      sum = fmaf(part, run.z, sum);
+      float p0, p1;
+      unpair(part, p0, p1);
+      sum = fmaf(p0 + p1, run.z, sum);
     }
     tmem_st16(s + 16 * c, p);
   }
@@ -511,8 +540,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (b < 0x7F800000u) top = max(top, b);
         }
         const int e = top ? min(max((int)(top >> 23) - 127 - 7, -100), 119) : 0;
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        rs = __uint_as_float((uint32_t)(127 + e) << 23) * A.scale;
+        const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), A.scale);
+        rs = __uint_as_float((uint32_t)(127 + e) << 23) * fabsf(A.scale);
         unsigned char* hi = sq + 2 * t * TILE8 + r * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {

@@ -283,6 +283,10 @@ def test_many_rows_magnitudes(gain, spread):
     check([400], [100], 2, 1, 128, 16, seed=34, scale=0.0)
 
 
+def test_many_rows_negative_scale():
+    check([400, 20], [100, 70], 4, 2, 128, 16, seed=37, scale=-0.09)
+
+
 def test_many_rows_nan_stays_where_it_is_seen():
     nan = float("nan")
 
