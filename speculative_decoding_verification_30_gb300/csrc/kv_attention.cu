@@ -948,8 +948,11 @@ __global__ void __launch_bounds__(JOIN * 32) kv_combine_kernel(const AttnArgs A)
 
 static sv::LaunchCache g_attn_cache;
 
-// Rows of a window from which the wide kernel takes over (head_dim 128).
-constexpr int WIDE_ROWS = 129;
+// Rows of a window from which the wide kernel takes over (head_dim 128): where these would
+// be more than one item and read the cache again. 3 sequences of up to 12,000 tokens, 32
+// heads on 8, this kernel and the wide one: 64 rows 48 and 50 us, 96 rows 71 and 51, 128
+// rows 74 and 53; 48 of up to 2,000: 64 rows 80 and 99, 96 rows 127 and 103.
+constexpr int WIDE_ROWS = 8 * MAX_NT + 1;
 
 // Tiles of 8 rows of an item: just enough for the window, at most MAX_NT, or those of
 // the wide kernel.
