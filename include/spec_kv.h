@@ -85,8 +85,9 @@ size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int
  * p <= seq_len[b] + i and, when window > 0, p > seq_len[b] + i - window, that lie on
  * mapped pages:
  *   lse = ln sum_p exp(a_p),  out = sum_p exp(a_p - lse) v_p
- * A query that sees nothing gets out = 0 and lse = -inf. What the cache holds past
- * a sequence's last new token is never looked at.
+ * A query that sees nothing gets out = 0 and lse = -inf; rows of a sequence past its
+ * first max_tokens are not written. What the cache holds past a sequence's last new
+ * token is never looked at.
  *   q      [N][q_heads][head_dim] bf16, token stride q_stride elements (heads
  *          adjacent; rows 16-byte aligned)
  *   out    [N][q_heads][head_dim] bf16, contiguous, 16-byte aligned (written)

