@@ -20,8 +20,8 @@
 // product and next logits, which cannot begin before the weights are there: TMEM has no
 // room for a second S. Tried: units in halves of 64 tokens, so that one half's products
 // run beside the other's softmax, 291 us (twice the products, each with N = 64 and little
-// faster than N = 128); one pass that guesses the frame and repeats, 280 against 257 us
-// for two passes.
+// faster than N = 128); weights handed over in two halves, 239; one pass that guesses the
+// frame and repeats, 280 against 257 us for two passes.
 // Warps: 0 copies (TMA), 1 issues the products, 2-3 widen values, 4-7 and 8-11 are the
 // two tiles' rows. Every wait is bounded; one that runs out stops the block, and the
 // join makes every output NaN.
