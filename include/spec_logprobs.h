@@ -36,7 +36,8 @@ extern "C" {
 
 /* Forward.
  *   logits      R rows of V elements of `dtype`, row r at logits + r * row_stride
- *               elements (row_stride >= V); any alignment of the element type
+ *               elements (row_stride >= V, or 0: one row for all tokens); any
+ *               alignment of the element type
  *   tokens      [R] int32
  *   temperature [R] float, or NULL for 1
  *   top_n       0..SV_LOGPROBS_MAX_TOP

@@ -899,7 +899,7 @@ static sv_status backward(const void* logits, int R, int V, long long ld, const 
 }
 
 static bool bad_shape(int R, int V, long long ld, int n) {
-  return R < 1 || R > (1 << 24) || V < 2 || V > 262144 || ld < V || n < 0 || n > MAX_TOP;
+  return R < 1 || R > (1 << 24) || V < 2 || V > 262144 || (ld < V && ld != 0) || n < 0 || n > MAX_TOP;
 }
 
 }  // namespace svlp

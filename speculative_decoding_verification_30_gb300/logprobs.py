@@ -90,7 +90,8 @@ class _Function(torch.autograd.Function):
 def spec_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature: torch.Tensor | None = None,
                         top_n: int = 0, stream=None) -> TokenLogprobs:
     """Log-probability, rank, entropy and the top_n alternatives (0..32) of `tokens` [...]
-    (int32) in the logit rows [..., V] (bf16 or fp32; the rows may have a stride).
+    (int32) in the logit rows [..., V] (bf16 or fp32; the rows may have a stride, or be one
+    row, expanded).
 
     `temperature` [...] (float32) divides the logits; 0 counts as 1. A row whose token
     is negative is skipped (outputs 0, rank and ids -1), so the out_tokens of

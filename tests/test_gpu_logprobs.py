@@ -244,6 +244,24 @@ def test_gradient_of_parts_and_errors():
     assert torch.isnan(d[1]).all() and not torch.isnan(d[0]).any() and not torch.isnan(d[2]).any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_one_row_for_many_tokens(dtype):
+    x, tok, temp, _ = _rows(1, 5008, dtype, 21)
+    tok = torch.arange(0, 5000, 700, dtype=torch.int32, device=DEV)
+    R = tok.numel()
+    x = x.to(DEV).requires_grad_()
+    wide = x.expand(R, -1)
+    r = sv.spec_token_logprobs(wide, tok, top_n=3)
+    ref = sv.spec_token_logprobs(x.detach().repeat(R, 1), tok, top_n=3)
+    for a, b in zip(r, ref):
+        assert torch.equal(a.detach(), b)
+    r.logprob.sum().backward()
+    d = sv.spec_token_logprobs_backward(x.detach().repeat(R, 1), tok, ref.lse, ref.entropy, grad_logprob=torch.ones(R, device=DEV))
+    assert torch.equal(x.grad, d.sum(0, keepdim=True))
+    with pytest.raises(sv.SpecVerifyError):        # the gradient's rows are each their own
+        sv.spec_token_logprobs_backward(wide.detach(), tok, ref.lse, ref.entropy, out=wide.detach())
+
+
 def test_refusals():
     x, tok = torch.zeros(4, 64, device=DEV), torch.zeros(4, dtype=torch.int32, device=DEV)
     E = sv.SpecVerifyError
