@@ -17,8 +17,9 @@
  * token) is skipped: it is not read, its outputs are 0 (rank and ids -1) and its
  * gradient is 0. A data error in a row (a NaN or +inf logit, a row that is -inf
  * everywhere, a token >= V, a temperature that is negative, NaN or +inf, or so
- * small that 1 / T or lse leaves fp32) is reported in band: NaN outputs with rank and
- * ids -1. The lowest finite value of the type is a logit like any other.
+ * small that 1 / T leaves fp32) is reported in band: NaN outputs with rank and ids -1.
+ * The lowest finite value of the type is a logit like any other: a row that holds
+ * nothing else is uniform (an output past fp32, then, is infinite).
  *
  * Pointers are device pointers, owned by the caller; the calls allocate nothing,
  * keep no state and are asynchronous on `stream` (a cudaStream_t).
@@ -58,7 +59,9 @@ sv_status spec_token_logprobs(const void* logits, sv_dtype dtype, int R, int V, 
  *   dx_j = 1/T ( g_l [j = t] + sum_i g_i [j = id_i] - p_j (g_l + sum_i g_i)
  *                - g_H p_j (ln p_j + H) )
  *   logits, dtype, R, V, row_stride, tokens, temperature: as in the forward call
- *   lse, entropy   [R] float: the forward call's outputs
+ *   lse, entropy   [R] float: the forward call's outputs. Probabilities are
+ *               exp(x / T - lse) up to |lse| = 1024; past that lse is too coarse and they
+ *               are formed from the row.
  *   grad_logprob, grad_entropy [R] float: either may be NULL (zero)
  *   top_ids [R, top_n] int32 (ids outside [0, V) count for nothing) and
  *   grad_top [R, top_n] float: NULL when top_n is 0

@@ -26,7 +26,7 @@
 // alternatives 74 us (4,100 GB/s), 2,000 rows of 50,257 fp32 of which a quarter are
 // skipped 69 us (4,310 GB/s), both bound by instruction issue (11 a logit) and each
 // CTA's start and end; 320 rows 36 us, 16 warps an SM; 2 rows 11 us, latency. Backward,
-// one read and one write: 512 rows of 151,936 bf16 49 us, 6,100 GB/s, bound by HBM.
+// one read and one write: 512 rows of 151,936 bf16 49 us, 6,040 GB/s, bound by HBM.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -276,6 +276,13 @@ struct Partial {   // of one CTA
   float m, s, w;
   int count, bad, ntop;
 };
+
+// x / T less lse, from the row's maximum m and log2 of its sum relative to it.
+__device__ __forceinline__ float log_prob(float x, float m, float temp, float l2) {
+  float d = (x - m) / temp;
+  if (d == -INFINITY && x > -INFINITY) d = x / temp - m / temp;   // the difference alone left the range
+  return fmaf(-LN2, l2, d);
+}
 
 // The lanes' partial results as one, in every lane (a butterfly: the same order always).
 __device__ __forceinline__ Partial join(Partial p, float c) {
@@ -662,12 +669,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
   if (crank != 0) return;
   // the first CTA puts the cluster together
   const Partial p = join(lane < C ? S.parts[lane] : Partial{-INFINITY, 0.f, 0.f, 0, 0, 0}, c);
-  const float l2 = log2f(p.s), all = p.m / temp + LN2 * l2;
-  const bool none = p.bad || !(p.s > 0.f) || !(fabsf(all) < INFINITY);
+  const float l2 = log2f(p.s);
+  const bool none = p.bad || !(p.s > 0.f);
   if (tid == 0) {
-    logprob[row] = none ? NAN : LN2 * fmaf(xt - p.m, c, -l2);
+    logprob[row] = none ? NAN : log_prob(xt, p.m, temp, l2);
     entropy[row] = none ? NAN : fmaxf(LN2 * (l2 - p.w / p.s), 0.f);
-    lse[row] = none ? NAN : all;
+    lse[row] = none ? NAN : p.m / temp + LN2 * l2;
     rank[row] = none ? -1 : p.count;
   }
   if (n == 0) return;
@@ -697,7 +704,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT)
     }
     if (at < n) {
       top_ids[row * n + at] = (int)~(uint32_t)k;
-      top_lp[row * n + at] = LN2 * fmaf(okey_value((uint32_t)(k >> 32)) - p.m, c, -l2);
+      top_lp[row * n + at] = log_prob(okey_value((uint32_t)(k >> 32)), p.m, temp, l2);
     }
   }
 }
@@ -723,6 +730,52 @@ __device__ __forceinline__ void grad_at(float& x0, float& x1, const Coef& f) {
   unpair(mul2(pair(ex2(a), ex2(b)), k), x0, x1);
 }
 
+// Rows whose lse is past this have their probabilities from the row itself: an lse of
+// 32 bits is known to 2^-24 of its size only, and so would they be.
+constexpr float MAX_LSE = 1024.f;
+
+// Such a row, by one CTA (rare: finite masks on every token, logits in the thousands). All
+// is read before anything is written: the gradient may take the logits' place.
+template <typename T>
+__device__ __noinline__ void grad_of_row(const T* x, T* y, int V, int tok, float temp, float gl, float gh, float H,
+                                         int n, const int32_t* ids, const float* gtop) {
+  __shared__ float part[BT / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float c = LOG2E / temp;
+  float m = -INFINITY, s = 0.f, sum = gl;
+#pragma unroll 1
+  for (int i = tid; i < V; i += BT) m = fmaxf(m, Elem<T>::get(x + i));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) part[warp] = m;
+  __syncthreads();
+#pragma unroll 1
+  for (int w = 0; w < BT / 32; ++w) m = fmaxf(m, part[w]);
+#pragma unroll 1
+  for (int i = tid; i < V; i += BT) s += ex2(fmaxf((Elem<T>::get(x + i) - m) * c, U_MIN));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  __syncthreads();
+  if (lane == 0) part[warp] = s;
+  __syncthreads();
+  s = 0.f;
+#pragma unroll 1
+  for (int w = 0; w < BT / 32; ++w) s += part[w];
+  const float l2 = log2f(s);
+#pragma unroll 1
+  for (int k = 0; k < n; ++k)
+    if (ids[k] >= 0 && ids[k] < V) sum += gtop[k];
+#pragma unroll 1
+  for (int i = tid; i < V; i += BT) {
+    const float u = fmaxf((Elem<T>::get(x + i) - m) * c, U_MIN) - l2;
+    float up = i == tok ? gl : 0.f;
+#pragma unroll 1
+    for (int k = 0; k < n; ++k)
+      if (ids[k] == i) up += gtop[k];
+    y[i] = Elem<T>::put((up - ex2(u) * (sum + gh * fmaf(LN2, u, H))) / temp);
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(BT)
     logprobs_grad_kernel(const T* logits, int V, long long ld, const int32_t* __restrict__ tokens,
@@ -737,6 +790,7 @@ __global__ void __launch_bounds__(BT)
   __shared__ int nfix;
   __shared__ Coef coef;
   __shared__ float fill;   // what a row without a gradient gets: 0, or NaN for a data error
+  __shared__ bool whole;   // the row is one CTA's
   const long long row = blockIdx.x / chunks;
   const int e0 = (int)(blockIdx.x % chunks) * CHUNK;   // the chunk's first element
   const int tid = threadIdx.x;
@@ -790,10 +844,20 @@ __global__ void __launch_bounds__(BT)
       f.k0 = -(gl + sum + gh * H) / temp;
       f.k1 = -gh * LN2 / temp;
       if (!ok) f.chi = NAN;
+      whole = tok >= 0 && tok < V && fabsf(L) > MAX_LSE;
       coef = f;
     }
   }
   __syncthreads();
+  if (whole) {
+    if (e0 == 0) {
+      float temp = temperature ? temperature[row] : 1.f;
+      if (temp == 0.f) temp = 1.f;
+      grad_of_row<T>(x, y, V, tok, temp, grad_lp ? grad_lp[row] : 0.f, grad_h ? grad_h[row] : 0.f, entropy[row], n,
+                     top_ids + row * n, grad_top + row * n);
+    }
+    return;
+  }
   const int nf = nfix;
   const Coef f = coef;
   const bool none = f.chi != f.chi;

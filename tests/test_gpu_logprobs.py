@@ -245,6 +245,62 @@ def test_gradient_of_parts_and_errors():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [0.5, 1.3, 2.0])
+def test_lowest_values_at_temperatures(T, dtype):
+    V, low = 9001, torch.finfo(TYPES[dtype]).min
+    g = torch.Generator().manual_seed(8)
+    x = (torch.randn(5, V, generator=g) * 2)
+    x[0] = low
+    x[1][torch.rand(V, generator=g) < 0.9] = low
+    x[1, 17] = low
+    x[2, 5:] = low
+    x[3] = low
+    x[3, 40] = -1e30
+    x = x.to(TYPES[dtype])
+    _check(x.to(DEV), torch.tensor([4, 17, 9000, 40, 3], dtype=torch.int32), torch.full((5,), T), 7)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradient_of_logits_far_from_zero(dtype, in_place):
+    # p is formed from the row: its exponents are off by 2^-23 of themselves (those that matter are
+    # below 150), the sum by V / 256 + 16 roundings
+    V, low = 40003, torch.finfo(TYPES[dtype]).min
+    g = torch.Generator().manual_seed(12)
+    x = torch.randn(6, V, generator=g) * 2
+    x[0] = low
+    x[1] += 30000.0
+    x[2] -= 30000.0
+    x[3, 2:] = low
+    x[3, :2] = 5e4
+    x[4] *= 1e30
+    x = x.to(TYPES[dtype])
+    tok = torch.tensor([3, 40002, 7, 1, int(x[4].float().argmax()), 9], dtype=torch.int32)
+    temp, n = torch.tensor([0.5, 1.0, 2.0, 1.0, 1.0, 1.0]), 3
+    glp, gh, gt = torch.randn(6, generator=g), torch.randn(6, generator=g), torch.randn(6, n, generator=g)
+    xd = x.to(DEV)
+    f = sv.spec_token_logprobs(xd, tok.to(DEV), temp.to(DEV), n)
+    d = sv.spec_token_logprobs_backward(xd, tok.to(DEV), f.lse, f.entropy, temp.to(DEV), glp.to(DEV), gh.to(DEV), f.top_ids,
+                                        gt.to(DEV), out=xd if in_place else None).cpu().double().numpy()
+    for r in range(6):
+        z, T = x[r].double().numpy(), float(temp[r])
+        _, _, H, _, ids, _ = logprobs.row(z, int(tok[r]), T, n)
+        assert f.top_ids[r].tolist() == ids
+        lp = (z - z.max()) / T
+        lp = np.maximum(lp - np.log(np.exp(lp).sum()), -700.0)
+        up = np.zeros(V)
+        up[int(tok[r])] += float(glp[r])
+        for j, v in zip(ids, gt[r].tolist()):
+            up[j] += v
+        ref = (up - np.exp(lp) * (up.sum() + float(gh[r]) * (lp + H))) / T
+        size = abs(float(glp[r])) + float(gt[r].abs().sum()) + abs(float(gh[r])) * (np.abs(lp) + H)
+        half = torch.finfo(TYPES[dtype]).eps / 2
+        tol = np.exp(lp) * size / T * (2.0 ** -20 + (V / 256 + 64 + 16 * np.abs(lp)) * U) + half * np.abs(ref) * 1.01
+        tol = tol + 8 * U * np.abs(up) / T + 8 * U * size / T * (up != 0) + 1e-37
+        assert (np.abs(d[r] - ref) <= tol).all(), (r, np.abs(d[r] - ref).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_one_row_for_many_tokens(dtype):
     x, tok, temp, _ = _rows(1, 5008, dtype, 21)
     tok = torch.arange(0, 5000, 700, dtype=torch.int32, device=DEV)
