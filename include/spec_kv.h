@@ -21,7 +21,7 @@
  * rejected token's place is simply written again by the next window). A negative
  * seq_len marks an empty place of the batch: nothing of it is read or written
  * but its rows of the outputs, which become 0 (lse -inf). max_tokens is a host
- * bound on the new tokens of any one sequence.
+ * bound on the new tokens of any one sequence; a close one chooses the better kernel.
  *
  * Layouts of heads: query head h reads kv head h / (q_heads / kv_heads).
  *
