@@ -23,7 +23,7 @@
 // exponent (weight 2^(s + log2 scale - m)) and the key scale through the logit.
 // Measured: 64 sequences of up to 16,000 tokens, 5 new ones, 32 heads on 8: 198 us, 5,440
 // GB/s, with the matrix pipe at a third and issue at 40%; 4 of 131,000 tokens, 64 heads on
-// 8: 161 us, 4,740 GB/s; 1 of 2,500 tokens 13 us, latency.
+// 8: 154 us, 4,980 GB/s; 1 of 2,500 tokens 13 us, latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -109,6 +109,11 @@ struct Shape {
   static constexpr int TOK = 16 * MT * NWARP;            // cached tokens of a unit
   static constexpr int BLOCKS = NT <= 2 ? 4 : NT <= 3 ? 3 : 2;
   static constexpr bool QREG = NT <= 3;                  // query fragments in registers
+  // Weights before it is known that the frames hold: one barrier less a unit, where a unit
+  // is 128 tokens and registers are left (32 rows of 4 sequences of 131,000 tokens 153 us
+  // against 163, 6 rows of 256 sequences 58.9 against 59.8; with units of 64 tokens 20 rows
+  // 199 against 198 and 4 rows 162 against 160; 64 rows 175 against 147).
+  static constexpr bool EARLY = MT == 2 && NT <= 4;
   static constexpr int PSTRIDE = 16 * (NT | 1);          // bytes of a token's weights: odd multiples of 16 spread the banks
   // the queries' and the weights' buffers are one where the queries move on to registers
   static constexpr int QBYTES = 8 * NT * D * 2, PBYTES = TOK * PSTRIDE, PAT = QREG ? 0 : QBYTES;
@@ -581,6 +586,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[j][n][k] = 0.f;
       }
+      if (Sh::QREG && Sh::EARLY) bar(2, NTHR);   // the weights go where the queries were
     }
 
     // --- logits of the warp's runs of 16 tokens: sc[t][n] holds tokens g and g + 8, rows 8 n + 2 q (+ 1)
@@ -673,6 +679,25 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
         for (int t = 1; t < MT; ++t) x = fmaxf(x, fmaxf(sc[t][n][e], sc[t][n][2 + e]));
         top = fmaxf(top, x - m[n][e]);
       }
+    float early[NT][2];          // this unit's sums, until the frames are known to hold
+    float (&part)[NT][2] = Sh::EARLY ? early : l;
+    const auto weigh = [&]() {
+      if (Sh::EARLY)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = 0.f;
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float p0 = ex2f(sc[t][n][2 * k] - m[n][0]), p1 = ex2f(sc[t][n][2 * k + 1] - m[n][1]);
+            part[n][0] = fmaf(p0, inv[t], part[n][0]);
+            part[n][1] = fmaf(p1, inv[t], part[n][1]);
+            *reinterpret_cast<uint32_t*>(sp + (16 * (MT * warp + t) + g + 8 * k) * PS + n * 16 + q * 4) = pack_h2(p0, p1);
+          }
+    };
+    if (Sh::EARLY) weigh();      // nearly always in the right frames
     if (bar_any(2, NTHR, top > TOP)) {
       // some weight would leave its range: move every row's frame to its maximum
 #pragma unroll
@@ -706,8 +731,12 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
             }
           }
         }
+      if (Sh::EARLY) {
+        weigh();
+        bar(2, NTHR);
+      }
     }
-    // the warp's value words, ahead of the barrier: word i of run t is of token 16 t + 2 q + {0, 1, 8, 9}
+    // the warp's value words: word i of run t is of token 16 t + 2 q + {0, 1, 8, 9}
     uint32_t v[TOK / 16][4];
 #pragma unroll
     for (int t = 0; t < TOK / 16; ++t)
@@ -719,17 +748,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
         else
           v[t][i] = *reinterpret_cast<const uint16_t*>(S.v + chunk_at<D>(tk, warp) + 2 * g);
       }
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float p0 = ex2f(sc[t][n][2 * k] - m[n][0]), p1 = ex2f(sc[t][n][2 * k + 1] - m[n][1]);
-          l[n][0] = fmaf(p0, inv[t], l[n][0]);
-          l[n][1] = fmaf(p1, inv[t], l[n][1]);
-          *reinterpret_cast<uint32_t*>(sp + (16 * (MT * warp + t) + g + 8 * k) * PS + n * 16 + q * 4) = pack_h2(p0, p1);
-        }
+    if (!Sh::EARLY) weigh();
     bool by_token = false;
     if (flags & MASKED) {
       // what is not there reads as zero
@@ -746,7 +765,10 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
         for (int i = 0; i < 4; ++i) nan |= (((v[t][i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
       by_token = __any_sync(0xffffffffu, nan);
     }
-    bar(2, NTHR);
+    if (!Sh::EARLY) bar(2, NTHR);
+    if (Sh::EARLY)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) l[n][0] += part[n][0], l[n][1] += part[n][1];
 
     // --- values: o[j][n] holds head_dim (D / 4) warp + (D / 32) g + 2 j + {0: k < 2, 1: k >= 2}
     if (__builtin_expect(!by_token, 1)) {
