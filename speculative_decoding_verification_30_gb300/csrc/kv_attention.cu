@@ -98,8 +98,8 @@ struct Stage {
 };
 // Layout of a block. Up to 24 query rows keep the queries' fragments in registers; more
 // read them from shared memory, which units of 128 tokens do half as often (32 rows of
-// 4 sequences of 131,000 tokens: 160 us against 173 with 64; 48 and 64 rows have no
-// registers for it: prompt chunks 699 us against 650). Narrow heads take 128 tokens too, so
+// 4 sequences of 131,000 tokens: 160 us against 173 with 64, before EARLY; 48 and 64 rows
+// have no registers for it: prompt chunks in this kernel 699 us against 650). Narrow heads take 128 tokens too, so
 // that a unit is worth its barriers. Blocks on an SM: as many as registers allow (64
 // sequences of up to 16,000 tokens, 20 rows: 197 us with three, 215 with two; 256 single
 // tokens, 6 rows: 60 us with four, 69 with three).
