@@ -329,12 +329,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         elv = log2f(vs);
         einv = __frcp_rn(vs);
       }
-      const int from = ((tok0 + (16 * lane & (TOK - 1))) >> shift) - window0;
-      const int page = __shfl_sync(0xffffffffu, entry, from);
+      // a run of 16 tokens that no query sees counts as unmapped: its page may never have been
+      // written, and 0 times what its scale holds may be NaN
+      const int run = 16 * lane & (TOK - 1), from = ((tok0 + run) >> shift) - window0;
+      const int listed = __shfl_sync(0xffffffffu, entry, from);
+      const int page = run < live && (!A.window || tok0 + run + 16 > cs.len - A.window + 1) ? listed : -1;
       const float ks = __shfl_sync(0xffffffffu, eks, from), lv = __shfl_sync(0xffffffffu, elv, from),
                   inv = __shfl_sync(0xffffffffu, einv, from);
       const bool gap = __any_sync(0xffffffffu, page < 0);
-      if (lane < TOK / 16) M.run[lane] = make_float4(ks, lv, inv, page < 0 ? 1.f : 0.f);
+      if (lane < TOK / 16) M.run[lane] = page < 0 ? make_float4(1.f, 0.f, 1.f, 1.f) : make_float4(ks, lv, inv, 0.f);
       const int at = tok0 + (lane * box & (TOK - 1));
       const int pg = __shfl_sync(0xffffffffu, entry, (at >> shift) - window0);
       const bool mine = lane * box < TOK && pg >= 0 && at - tok0 < live;
