@@ -95,12 +95,9 @@ size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int
  *   scale  a finite factor, usually head_dim^-1/2; window >= 0 (0: no limit)
  *   workspace: 16-byte aligned, spec_kv_attention_workspace_bytes() bytes
  * Products are formed from the codes as they are, from weights rounded to fp16 (11
- * bits) and from queries scaled by a power of two for each row, all sums in fp32. With
- * up to 64 query rows for a kv head (max_tokens * q_heads / kv_heads), or head_dim 64,
- * queries are fp16: their 8 significant bits are kept. With more, a query element is
- * the sum of two e4m3 numbers: it keeps its 8 bits down to 2^-9 of its row's largest
- * element, smaller ones are off by at most 2^-17 of that, and an infinite one counts as
- * NaN. Repeated calls give the same bits.
+ * bits) and from queries in fp16, scaled by a power of two for each row so that they keep
+ * their 8 significant bits down to 2^-24 of the row's largest element; all sums in fp32.
+ * Repeated calls give the same bits.
  * Every wait for a copy is bounded (0.2 s); if one runs out, all outputs are NaN.
  * Returns SV_ERR_NULL, SV_ERR_SHAPE, SV_ERR_ALIGN or SV_ERR_WORKSPACE before
  * launching, SV_ERR_CUDA when the tensor-map encoder or a launch fails. */

@@ -5,25 +5,26 @@
 // the 5th-generation tensor cores: 4 head_dim flops for each (row, key). An item has up
 // to 256 rows, two tiles of 128 that take turns: while one is in its softmax the tensor
 // cores work for the other. Per unit of 128 tokens:
-//   S = Q K^T  on e4m3 codes as they lie in the cache: a bf16 query has 8 significant
-//              bits and is the sum of two e4m3 numbers (4 bits each, scaled so that the
-//              row's largest element is in [2^7, 2^8)), so S takes two products and no
-//              key is widened; exact for elements down to 2^-9 of the row's largest,
-//              smaller ones end at the codes' spacing, 2^-17 of that;
+//   S = Q K^T  in fp16: keys widened (exactly) into shared memory, queries
+//              scaled by a power of two so that the row's largest element is in [2^7, 2^8).
+//              Elements keep their 8 bits down to 2^-24 of that, as in the kernel for few
+//              rows: a query's precision does not depend on what else is in the batch;
 //   softmax    a thread to a row: S from TMEM, weights to TMEM as fp16 over S;
-//   O += P V   weights from TMEM, values widened to fp16 (exactly) by two warps into
-//              shared memory, where head_dim runs along the rows.
+//   O += P V   weights from TMEM, values widened likewise, head_dim along the rows.
 // O stays in TMEM and is scaled there when a row's frame moves.
-// Measured: 3 sequences of up to 700 new tokens on up to 12,000 cached, 32 heads on 8: 229
-// us, 862 TFLOP/s. Of a unit's 4,400 clocks a tile's rows compute 2,100 (1,500 of them the
-// weights, whose exponentials run at 16 a clock on an SM) and wait 1,700 for their second
-// product and next logits, which cannot begin before the weights are there: TMEM has no
-// room for a second S. Tried: units in halves of 64 tokens, so that one half's products
-// run beside the other's softmax, 291 us (twice the products, each with N = 64 and little
-// faster than N = 128); weights handed over in two halves, 239; one pass that guesses the
-// frame and repeats, 280 against 257 us for two passes.
-// Warps: 0 copies (TMA), 1 issues the products, 2-3 widen values, 4-7 and 8-11 are the
-// two tiles' rows. Every wait is bounded; one that runs out stops the block, and the
+// Measured: 3 sequences of up to 700 new tokens on up to 12,000 cached, 32 heads on 8: 240
+// us, 824 TFLOP/s. Bound by the chain of a tile, next logits, softmax, second product, of
+// which the softmax is the longest part: 2,100 of a unit's 4,600 clocks, 1,500 of them the
+// weights. Their exponentials need a third of that (32 a clock on an SM, measured); the rest is
+// the latency of loading, waiting for and computing a row's quarters in turn. Tried, when the
+// products ran on the codes themselves with a query as the sum of two e4m3 numbers (228 us, but
+// elements below 2^-9 of a row's largest lost bits: logits 1e-2 off beside a channel 300 times
+// the others): units in halves of 64 tokens, so that one half's products run beside the other's
+// softmax, 291 us (twice the products, each with N = 64 and little faster than N = 128); weights
+// handed over in two halves, 239; one pass that guesses the frame and repeats, 280 against 257
+// for two passes.
+// Warps: 0 copies (TMA), 1 issues the products, 2-3 widen values, 12-13 keys, 4-7 and 8-11
+// are the two tiles' rows. Every wait is bounded; one that runs out stops the block, and the
 // join makes every output NaN.
 #pragma once
 
@@ -31,10 +32,15 @@ namespace svkv {
 namespace wide {
 
 constexpr int D = 128, TOK = 128, ROWS = 256, NT = ROWS / 8;
-constexpr int THREADS = 384, NK = 3, NV = 2, NM = 8;   // stages of keys, of values, of a unit's facts
+constexpr int THREADS = 448, NM = 8;   // stages of a unit's facts
+// Stages of codes of keys and of values, and of these widened. A unit's widened values are
+// read by the second product of both tiles, and the next ones are not wanted before the
+// first tile's next softmax is through: one stage does. Keys are wanted as soon as that
+// product is issued, so they are widened a unit ahead.
+constexpr int NK = 2, NV = 1, NWK = 2, NWV = 1;
 constexpr int TILE8 = TOK * D, TILE16 = 2 * TILE8;
-// instruction descriptors: fp32 accumulator, M = 128, N = 128; e4m3 x e4m3, and fp16 x
-// fp16 with the second operand's rows along N
+// instruction descriptors: fp16 x fp16, fp32 accumulator, M = 128, N = 128; the second
+// operand's rows along K, and along N
 constexpr uint32_t ID_QK = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t ID_PV = ID_QK | (1u << 16);
 
@@ -44,18 +50,19 @@ struct Item {                 // what the rows need of an item
 struct __align__(16) Ctl {
   Meta meta[NM];
   Item item[NM];
-  unsigned long long kfull[NK], kempty[NK], vfull[NV], vempty[NV], wfull[NV], wempty[NV];
+  unsigned long long kfull[NK], kempty[NK], vfull[NV], vempty[NV];           // codes
+  unsigned long long wkfull[NWK], wkempty[NWK], wvfull[NWV], wvempty[NWV];   // widened
   unsigned long long sfull[2], pfull[2], qfull[2], ofull[2], ready[NM], done;
   // NaN values of units that only some rows see: a bit for each element of a token, and
   // the unit (+ 1) that last had any
-  uint4 nan[NV][TOK];
-  int nan_unit[NV];
+  uint4 nan[NWV][TOK];
+  int nan_unit[NWV];
   uint32_t taddr;
   int err;
   long long sum[THREADS / 32], pre;
   int start_b;
 };
-constexpr int SMEM = 1024 + 4 * TILE8 + NK * TILE8 + NV * TILE8 + NV * TILE16 + (int)sizeof(Ctl);
+constexpr int SMEM = 1024 + 2 * TILE16 + (NK + NV) * TILE8 + (NWK + NWV) * TILE16 + (int)sizeof(Ctl);
 static_assert(SMEM <= 227 * 1024, "one block on an SM");
 
 __device__ __forceinline__ void arrive(unsigned long long* b) {
@@ -95,7 +102,7 @@ __device__ __forceinline__ uint64_t desc(uint32_t at, uint32_t lead) {
 __device__ __forceinline__ void mma_qk(uint32_t d, uint64_t a, uint64_t b, uint32_t add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(ID_QK), "r"(add)
       : "memory");
 }
@@ -130,11 +137,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ float code_value(uint32_t c) {   // one e4m3 code
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3);
-  return __low2float(__half2(h));
-}
-
 // Two floats in one 64-bit register, for the packed instructions.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;
@@ -233,11 +235,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     kv_wide_kernel(const AttnArgs A, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  unsigned char* sq = smem;                       // [tile][high, low][row][d] e4m3
-  unsigned char* sk = sq + 4 * TILE8;             // [stage][token][d]
-  unsigned char* sv = sk + NK * TILE8;            // [stage][token][d]
-  unsigned char* sw = sv + NV * TILE8;            // [stage][d / 64][token][64] fp16
-  Ctl& C = *reinterpret_cast<Ctl*>(sw + NV * TILE16);
+  unsigned char* sq = smem;                       // [tile][d / 64][row][64] fp16
+  unsigned char* sk = sq + 2 * TILE16;            // [stage][token][d] codes
+  unsigned char* sv = sk + NK * TILE8;
+  unsigned char* swk = sv + NV * TILE8;           // [stage][d / 64][token][64] fp16
+  unsigned char* swv = swk + NWK * TILE16;
+  Ctl& C = *reinterpret_cast<Ctl*>(swv + NWV * TILE16);
   volatile int* err = &C.err;
   const Window& w = A.w;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = A.group;
@@ -246,15 +249,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     const auto init = [](unsigned long long* b, int n) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
     };
-    for (int i = 0; i < NK; ++i) init(&C.kfull[i], 1), init(&C.kempty[i], 1);
-    for (int i = 0; i < NV; ++i) init(&C.vfull[i], 1), init(&C.vempty[i], 2), init(&C.wfull[i], 2), init(&C.wempty[i], 1);
+    for (int i = 0; i < NK; ++i) init(&C.kfull[i], 1), init(&C.kempty[i], 2);
+    for (int i = 0; i < NV; ++i) init(&C.vfull[i], 1), init(&C.vempty[i], 2);
+    for (int i = 0; i < NWK; ++i) init(&C.wkfull[i], 2), init(&C.wkempty[i], 1);
+    for (int i = 0; i < NWV; ++i) init(&C.wvfull[i], 2), init(&C.wvempty[i], 1);
     for (int t = 0; t < 2; ++t) init(&C.sfull[t], 1), init(&C.pfull[t], 4), init(&C.qfull[t], 4), init(&C.ofull[t], 1);
     for (int i = 0; i < NM; ++i) init(&C.ready[i], 1);
     init(&C.done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     C.err = 0;
-    for (int i = 0; i < NV; ++i) C.nan_unit[i] = 0;
+    for (int i = 0; i < NWV; ++i) C.nan_unit[i] = 0;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&C.taddr)) : "memory");
@@ -304,12 +309,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           M.flags = END;
           C.item[ni % NM].flags = END;
           arrive(&C.kfull[ks_]);
-        }
-        if (j >= NV) ok = wait_warp(&C.vempty[vs_], (uint32_t)(j / NV - 1) & 1, err);
-        if (lane == 0) {
-          arrive(&C.vfull[vs_]);
           arrive(&C.ready[ni % NM]);
         }
+        if (j >= NV) ok = wait_warp(&C.vempty[vs_], (uint32_t)(j / NV - 1) & 1, err);
+        if (lane == 0) arrive(&C.vfull[vs_]);
         break;
       }
       const int tok0 = (cp.tile0 + ct - OVERHEAD) * TOK;
@@ -407,17 +410,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) {
       int items = 0;
       const auto qk = [&](int t, int j) {
-        const uint64_t q0 = desc(smem_u32(sq + 2 * t * TILE8), 0), k0 = desc(smem_u32(sk + (j % NK) * TILE8), 0);
+        const uint64_t q0 = desc(smem_u32(sq + t * TILE16), 0), k0 = desc(smem_u32(swk + (j % NWK) * TILE16), 0);
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int half = 0; half < 2; ++half)   // of head_dim
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            mma_qk(tmem + 128 * t, q0 + (part * TILE8 + 32 * k) / 16, k0 + 32 * k / 16, part | k);
+          for (int k = 0; k < 4; ++k) {
+            const int at = (half * TILE8 + 32 * k) / 16;
+            mma_qk(tmem + 128 * t, q0 + at, k0 + at, half | k);
+          }
         commit(&C.sfull[t]);
       };
       // unit j's first product for tile t needs the keys, and new queries if an item begins
       const auto begin = [&](int j) {
-        if (!wait(&C.kfull[j % NK], (uint32_t)(j / NK) & 1, err)) return -1;
+        if (!wait(&C.wkfull[j % NWK], (uint32_t)(j / NWK) & 1, err)) return -1;
         return C.meta[j % NM].flags;
       };
       int flags = begin(0);
@@ -428,16 +433,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           after_sync();
           if (ok) qk(t, 0);
         }
-        if (ok) commit(&C.kempty[0]);
+        if (ok) commit(&C.wkempty[0]);
         ++items;
         for (int j = 0; ok; ++j) {
           const int now = flags;
           flags = begin(j + 1);
           if (flags < 0) break;
           const bool more = !(flags & END), fresh = flags & FIRST;
-          ok = wait(&C.wfull[j % NV], (uint32_t)(j / NV) & 1, err);
+          ok = wait(&C.wvfull[j % NWV], (uint32_t)(j / NWV) & 1, err);
           if (!ok) break;
-          const uint64_t v0 = desc(smem_u32(sw + (j % NV) * TILE16), TOK * 128);
+          const uint64_t v0 = desc(smem_u32(swv + (j % NWV) * TILE16), TOK * 128);
           for (int t = 0; t < 2 && ok; ++t) {
             ok = wait(&C.pfull[t], (uint32_t)j & 1, err);
             if (!ok) break;
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int k = 0; k < TOK / 16; ++k)
               mma_pv(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, v0 + 16 * 128 * k / 16,
                      (uint32_t)(k != 0 || !(now & FIRST)));
-            if (t == 1) commit(&C.wempty[j % NV]);
+            if (t == 1) commit(&C.wvempty[j % NWV]);
             if (now & LAST) commit(&C.ofull[t]);
             if (more && !fresh) qk(t, j + 1);
           }
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             ++items;
           }
-          if (ok) commit(&C.kempty[(j + 1) % NK]);
+          if (ok) commit(&C.wkempty[(j + 1) % NWK]);
         }
       }
       // wake the rows for the END
@@ -468,68 +473,82 @@ __global__ void __launch_bounds__(THREADS, 1)
       wait(&C.done, 0, &never);
     }
     __syncwarp();
-  } else if (warp < 4) {
-    // --- values to fp16: 1024 chunks of 16 codes a unit
-    const int me = tid - 64;
-    for (int j = 0;; ++j) {
-      if (!wait_warp(&C.vfull[j % NV], (uint32_t)(j / NV) & 1, err)) break;
-      const Meta& M = C.meta[j % NM];
-      const int flags = M.flags;
-      if (flags & END) break;
-      if (j >= NV && !wait_warp(&C.wempty[j % NV], (uint32_t)(j / NV - 1) & 1, err)) break;
-      const unsigned char* src = sv + (j % NV) * TILE8;
-      unsigned char* dst = sw + (j % NV) * TILE16;
-      const auto chunk = [&](int x, const uint4& v) {
-        const int t = x >> 3, c = x & 7, k = 2 * (c & 3);   // token, chunk of 16
-        uint32_t o[8];
-        widen(v.x, o[0], o[1]);
-        widen(v.y, o[2], o[3]);
-        widen(v.z, o[4], o[5]);
-        widen(v.w, o[6], o[7]);
-        unsigned char* row = dst + (c >> 2) * (TOK * 128) + t * 128;
-        *reinterpret_cast<uint4*>(row + ((k ^ (t & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(row + (((k + 1) ^ (t & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-      };
-      const auto codes = [&](int x) {
-        return *reinterpret_cast<const uint4*>(src + (x >> 3) * 128 + (((x & 7) ^ (x >> 3 & 7)) << 4));
-      };
-      if (!(flags & MASKED)) {
+  } else if (warp < 4 || warp >= 12) {
+    // --- keys (warps 12 and 13) and values (2 and 3) to fp16. A thread has the chunk of 16
+    // codes c of tokens t0, t0 + 8, ...: the swizzle is the same in all of them, so each lies
+    // 1024 bytes after the last. (With two warps for both the chunks take 276 us, not 240.)
+    const int me = tid & 63, t0 = me >> 3, c = me & 7;
+    const int from = t0 * 128 + ((c ^ t0) << 4), to = (c >> 2) * TILE8 + t0 * 128 + (((2 * (c & 3)) ^ t0) << 4);
+    const auto chunk = [&](unsigned char* at, const uint4& v) {
+      uint32_t o[8];
+      widen(v.x, o[0], o[1]);
+      widen(v.y, o[2], o[3]);
+      widen(v.z, o[4], o[5]);
+      widen(v.w, o[6], o[7]);
+      *reinterpret_cast<uint4*>(at + to) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(at + (to ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+    };
+    const auto all = [&](unsigned char* dst, const unsigned char* src) {
 #pragma unroll 1
-        for (int i = me; i < TOK * 8; i += 256) {
-          uint4 v[4];
+      for (int i = 0; i < TOK * 128; i += 4096) {
+        uint4 v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = codes(i + 64 * k);
+        for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const uint4*>(src + from + i + 1024 * k);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) chunk(i + 64 * k, v[k]);
-        }
-      } else {
-#pragma unroll 1
-        for (int x = me; x < TOK * 8; x += 64) {
-          const int t = x >> 3, c = x & 7;
-          uint4 v = codes(x);
-          if (t >= M.live || M.run[t >> 4].w != 0.f) v = make_uint4(0u, 0u, 0u, 0u);   // what is not there reads as zero
-          uint32_t q[4] = {v.x, v.y, v.z, v.w}, nan = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t hit = ((q[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-            while (hit) {
-              const int b = (__ffs(hit) - 1) >> 3;
-              hit &= hit - 1;
-              nan |= 1u << (4 * k + b);
-              q[k] &= ~(0xFFu << (8 * b));
-            }
-          }
-          // kept aside: only rows that see the token get it
-          reinterpret_cast<unsigned short*>(&C.nan[j % NV][t])[c] = (unsigned short)nan;
-          if (nan) *reinterpret_cast<volatile int*>(&C.nan_unit[j % NV]) = j + 1;
-          chunk(x, make_uint4(q[0], q[1], q[2], q[3]));
-        }
+        for (int k = 0; k < 4; ++k) chunk(dst + i + 1024 * k, v[k]);
       }
+    };
+    // the warp's part of the stage is read, and written where the products read it
+    const auto hand_over = [&](unsigned long long* empty, unsigned long long* full) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        arrive(&C.vempty[j % NV]);
-        arrive(&C.wfull[j % NV]);
+        arrive(empty);
+        arrive(full);
+      }
+    };
+    if (warp >= 12) {
+      for (int j = 0;; ++j) {
+        if (!wait_warp(&C.kfull[j % NK], (uint32_t)(j / NK) & 1, err)) break;
+        if (j >= NWK && !wait_warp(&C.wkempty[j % NWK], (uint32_t)(j / NWK - 1) & 1, err)) break;
+        const bool end = C.meta[j % NM].flags & END;
+        if (!end) all(swk + (j % NWK) * TILE16, sk + (j % NK) * TILE8);
+        hand_over(&C.kempty[j % NK], &C.wkfull[j % NWK]);
+        if (end) break;
+      }
+    } else {
+      for (int j = 0;; ++j) {
+        if (!wait_warp(&C.vfull[j % NV], (uint32_t)(j / NV) & 1, err)) break;
+        const Meta& M = C.meta[j % NM];
+        if (M.flags & END) break;
+        if (j >= NWV && !wait_warp(&C.wvempty[j % NWV], (uint32_t)(j / NWV - 1) & 1, err)) break;
+        const unsigned char* src = sv + (j % NV) * TILE8;
+        unsigned char* dst = swv + (j % NWV) * TILE16;
+        if (!(M.flags & MASKED)) {
+          all(dst, src);
+        } else {
+#pragma unroll 1
+          for (int t = t0; t < TOK; t += 8) {
+            uint4 v = *reinterpret_cast<const uint4*>(src + from + 128 * (t - t0));
+            if (t >= M.live || M.run[t >> 4].w != 0.f) v = make_uint4(0u, 0u, 0u, 0u);   // what is not there reads as zero
+            uint32_t q[4] = {v.x, v.y, v.z, v.w}, nan = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t hit = ((q[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+              while (hit) {
+                const int b = (__ffs(hit) - 1) >> 3;
+                hit &= hit - 1;
+                nan |= 1u << (4 * k + b);
+                q[k] &= ~(0xFFu << (8 * b));
+              }
+            }
+            // kept aside: only rows that see the token get it
+            reinterpret_cast<unsigned short*>(&C.nan[j % NWV][t])[c] = (unsigned short)nan;
+            if (nan) *reinterpret_cast<volatile int*>(&C.nan_unit[j % NWV]) = j + 1;
+            chunk(dst + 128 * (t - t0), make_uint4(q[0], q[1], q[2], q[3]));
+          }
+        }
+        hand_over(&C.vempty[j % NV], &C.wvfull[j % NWV]);
       }
     }
   } else {
@@ -568,29 +587,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int e = top ? min(max((int)(top >> 23) - 127 - 7, -100), 119) : 0;
         const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), A.scale);
         rs = __uint_as_float((uint32_t)(127 + e) << 23) * fabsf(A.scale);
-        unsigned char* hi = sq + 2 * t * TILE8 + r * 128;
+        unsigned char* row = sq + t * TILE16 + r * 128;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t h[4], l[4];
+        for (int c = 0; c < 16; ++c) {   // chunks of 8 elements
+          uint32_t h[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float f[4], b[4];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t u = q[8 * c + 2 * k + y];
-              f[2 * y] = __uint_as_float(u << 16) * down;
-              f[2 * y + 1] = __uint_as_float(u & 0xFFFF0000u) * down;
-            }
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              if (isinf(f[y])) f[y] = NAN;   // e4m3 has no infinity
-            h[k] = encode4(f);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) b[y] = f[y] - code_value(h[k] >> (8 * y) & 0xFFu);
-            l[k] = encode4(b);
+            const uint32_t u = q[4 * c + k];
+            h[k] = pack_h2(__uint_as_float(u << 16) * down, __uint_as_float(u & 0xFFFF0000u) * down);
           }
-          *reinterpret_cast<uint4*>(hi + ((c ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(hi + TILE8 + ((c ^ (r & 7)) << 4)) = make_uint4(l[0], l[1], l[2], l[3]);
+          *reinterpret_cast<uint4*>(row + (c >> 3) * TILE8 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -630,11 +636,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         l += flags & MASKED ? weights<true>(M, ts, rs, m, hi, lo) : weights<false>(M, ts, rs, m, hi, lo);
         if (flags & MASKED) {
           // the stage holds unit j until both tiles' weights are there
-          ok = wait_warp(&C.wfull[j % NV], (uint32_t)(j / NV) & 1, err);
+          ok = wait_warp(&C.wvfull[j % NWV], (uint32_t)(j / NWV) & 1, err);
           if (!ok) break;
-          if (*reinterpret_cast<volatile int*>(&C.nan_unit[j % NV]) == j + 1)
+          if (*reinterpret_cast<volatile int*>(&C.nan_unit[j % NWV]) == j + 1)
             for (int p = max(lo + 1, 0); p <= min(hi, TOK - 1); ++p) {
-              const uint4 b = C.nan[j % NV][p];
+              const uint4 b = C.nan[j % NWV][p];
               bad[0] |= b.x, bad[1] |= b.y, bad[2] |= b.z, bad[3] |= b.w;
             }
         }
