@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int pg = __shfl_sync(0xffffffffu, entry, (at >> shift) - window0);
       const bool mine = lane * box < TOK && pg >= 0 && at - tok0 < live;
       const int bytes = __popc(__ballot_sync(0xffffffffu, mine)) * box * D;
+      __syncwarp();   // every lane's run is there before the stage is announced: without copies that completes it
       if (lane == 0) {
         const long long item0 = cu - ct, item1 = item0 + OVERHEAD + cp.tiles;
         const bool first = ct == OVERHEAD || cu == u0;

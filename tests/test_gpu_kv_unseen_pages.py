@@ -44,3 +44,15 @@ def test_pages_before_a_sliding_window(dim, heads, kv_heads, new, page, bad):
                 if (j + 1) * page <= n - window + 1:       # its last token lies before query 0's window
                     _poison(cache, table[b][j], bad)
     check(lens, [new] * 4, heads, kv_heads, dim, page, window=window, seed=page + dim, edit=edit)
+
+
+@pytest.mark.parametrize("heads,kv_heads,new", [(8, 2, 3), (4, 1, 40)])
+def test_long_gaps_of_unmapped_pages(heads, kv_heads, new):
+    """Units of which nothing is copied, between units that are: what a unit's facts say must be
+    there when it is announced, also when no copy has to be waited for."""
+    def edit(cache, table):
+        for j in range(table.shape[1]):
+            if (j // 12) % 2:                        # 192 tokens mapped, 192 not
+                table[:, j] = -1
+    for seed in range(6):
+        check([3000, 700, 2050], [new] * 3, heads, kv_heads, 128, 16, seed=seed, edit=edit, garbage=False)
