@@ -65,8 +65,9 @@ struct AttnArgs {
   int window;
   __nv_bfloat16* out;
   float* lse;
-  long long* prefix;   // workspace: units before each sequence [B + 1], the blocks in use, whether a wait ran out
+  long long* prefix;   // workspace: units before each sequence [B + 1], the blocks in use
   Start* start;        // workspace: the item in which each block's share begins
+  uint8_t* failed;     // workspace: whether a wait of each block ran out; every block writes its own
   float* part;         // workspace: 2 slots for each block
   int workers;
   int group;           // query heads of a kv head
@@ -90,7 +91,12 @@ struct Meta {                  // of a stage: a unit of item (b, h, rt)
 };
 static_assert(sizeof(Meta) % 16 == 0, "stages stay 16-byte aligned");
 
-constexpr uint64_t WAIT_NS = 200ull * 1000 * 1000;   // a copy that takes longer is given up
+// A copy or product that takes longer is given up. The limit of the last wait, for what is
+// still in flight before a block ends, is never shorter.
+constexpr uint64_t LAND_NS = 200ull * 1000 * 1000;
+#ifndef SPEC_KV_WAIT_NS   // a test makes it 0, for all blocks or for one
+#define SPEC_KV_WAIT_NS LAND_NS
+#endif
 
 template <int D, int TOK>
 struct Stage {
@@ -210,10 +216,15 @@ __device__ __forceinline__ bool find_share(const AttnArgs& A, long long* s_sum, 
   if (blockIdx.x == 0 && tid == 0) {
     A.prefix[w.B] = units;
     A.prefix[w.B + 1] = workers;
-    A.prefix[w.B + 2] = 0;
   }
   __syncthreads();
   return u0 < u1 && *s_b >= 0;
+}
+
+// Whether the block gave up, in its byte; the last block fills up the 16 bytes its own lies in.
+__device__ __forceinline__ void set_failed(const AttnArgs& A, int tid, int x) {
+  const int b = blockIdx.x, at = b + tid;
+  if (tid == 0 || (b + 1 == A.workers && (at ^ b) < 16)) A.failed[at] = tid == 0 ? x : 0;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -231,12 +242,13 @@ __device__ __forceinline__ bool arrived(uint32_t b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the copies of a stage, for at most WAIT_NS.
-__device__ __forceinline__ bool wait_copies(uint32_t b, uint32_t parity) {
+// Waits for the copies of a stage, for at most `limit` ns (0: gives up at once).
+__device__ __forceinline__ bool wait_copies(uint32_t b, uint32_t parity, uint64_t limit) {
+  if (limit == 0) return false;
   if (arrived(b, parity)) return true;
   const uint64_t t0 = now_ns();
   while (!arrived(b, parity))
-    if (now_ns() - t0 > WAIT_NS) return false;
+    if (now_ns() - t0 > limit) return false;
   return true;
 }
 // A box of rows of codes from row y; the first coordinate is 0, the second has no alignment rule.
@@ -385,6 +397,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  set_failed(A, tid, 0);
   const int G = A.group;
   constexpr int ALL = NTHR + 32;
   const long long wk = blockIdx.x;
@@ -507,17 +520,17 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
     for (int i = 0; i < NS - 1; ++i) ahead += issue(i);
     uint32_t parity = 0;
     for (int stage = 0;;) {
-      if (ahead > 0 && !__all_sync(0xffffffffu, wait_copies(smem_u32(full + stage), parity))) {
-        // given up: the others stop, the join makes every output NaN
+      if (ahead > 0 && !__all_sync(0xffffffffu, wait_copies(smem_u32(full + stage), parity, SPEC_KV_WAIT_NS))) {
+        // given up: the others stop, the join makes every output NaN; what was asked for lands
         if (lane == 0) {
           meta[stage].flags = END;
-          A.prefix[w.B + 2] = 1;
+          A.failed[wk] = 1;
         }
         __syncwarp();
         bar(1, ALL);
-        for (int i = 1; i < ahead; ++i) {
+        for (int i = 0; i < ahead; ++i) {
+          wait_copies(smem_u32(full + stage), parity, LAND_NS);
           if (++stage == NS) stage = 0, parity ^= 1;
-          wait_copies(smem_u32(full + stage), parity);
         }
         return;
       }
@@ -876,25 +889,37 @@ namespace svkv {
 // and adds their weighted values, D / 32 elements a lane. Then the warps of a row are
 // joined, in their order.
 constexpr int JOIN = 8;   // warps
+
+// Whether some block gave up, in every lane of a warp.
+__device__ __forceinline__ bool any_failed(const AttnArgs& A, int lane) {
+  uint32_t x = 0u;
+  for (int at = 16 * lane; at < A.workers; at += 16 * 32) {
+    const uint4 v = *reinterpret_cast<const uint4*>(A.failed + at);
+    x |= v.x | v.y | v.z | v.w;
+  }
+  return __any_sync(0xffffffffu, x != 0u);
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(JOIN * 32) kv_combine_kernel(const AttnArgs A) {
   constexpr int ROWS = 8 * NT, E = D / 32;
   // first of all, in every thread: this grid ends only after the one before it
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Window& w = A.w;
+  __shared__ bool failed;
   __shared__ float sm[JOIN], sl[JOIN], so[JOIN][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = A.group;
   const long long k = blockIdx.x, units = A.prefix[w.B], workers = A.prefix[w.B + 1];
-  if (A.prefix[w.B + 2] != 0) {   // a copy never came
+  if (k == 0) {   // no item is cut at the first share's start: these blocks see to copies that never came
+    if (!any_failed(A, lane)) return;
     const long long n = (long long)w.N * w.q_heads;
-    for (long long x = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * (JOIN * 32) + threadIdx.x; x < n * D;
-         x += (long long)gridDim.x * gridDim.y * (JOIN * 32)) {
+    for (long long x = (long long)blockIdx.y * (JOIN * 32) + threadIdx.x; x < n * D; x += (long long)gridDim.y * (JOIN * 32)) {
       A.out[x] = __float2bfloat16_rn(NAN);
       if (A.lse && x < n) A.lse[x] = NAN;
     }
     return;
   }
-  if (k == 0 || k >= workers) return;
+  if (k >= workers) return;
   const Start item = A.start[k];
   const long long i0 = item.unit0;
   // the shares that hold its first and its last unit with tokens
@@ -951,7 +976,12 @@ __global__ void __launch_bounds__(JOIN * 32) kv_combine_kernel(const AttnArgs A)
   if (lane == 0) sm[warp] = m, sl[warp] = l;
 #pragma unroll
   for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+  if (warp == JOIN - 1) {   // one warp looks, here: earlier, or in all warps, it costs 0.7 to 4 us a call
+    const bool x = any_failed(A, lane);
+    if (lane == 0) failed = x;
+  }
   __syncthreads();
+  if (failed) return;
   if (warp % team || mine >= rows) return;
   m = sm[warp];
   for (int x = 1; x < team; ++x) m = fmaxf(m, sm[warp + x]);
@@ -1002,9 +1032,13 @@ static int sm_count() try {
   return 0;
 }
 
-static size_t prefix_bytes(int B) { return ((size_t)(B + 3) * sizeof(long long) + 127) & ~(size_t)127; }
+static size_t prefix_bytes(int B) { return ((size_t)(B + 2) * sizeof(long long) + 127) & ~(size_t)127; }
 static size_t start_bytes(int workers) { return (size_t)workers * sizeof(Start); }
+static size_t failed_bytes(int workers) { return ((size_t)workers + 127) & ~(size_t)127; }
 static size_t part_bytes(int workers, int nt, int D) { return (size_t)workers * 2 * 8 * nt * (D + 2) * sizeof(float); }
+static size_t workspace_size(int B, int workers, int nt, int D) {
+  return prefix_bytes(B) + start_bytes(workers) + failed_bytes(workers) + part_bytes(workers, nt, D);
+}
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -1104,7 +1138,7 @@ size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int
     return 0;
   const int nt = row_tiles(max_tokens, q_heads / kv_heads, head_dim);
   const int workers = sm_count() * blocks_per_sm(nt);
-  return workers < 1 ? 0 : prefix_bytes(B) + start_bytes(workers) + part_bytes(workers, nt, head_dim);
+  return workers < 1 ? 0 : workspace_size(B, workers, nt, head_dim);
 }
 
 sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_codes, const float* k_scale,
@@ -1128,7 +1162,7 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   const int sms = aligned(workspace, 16) ? sm_count() : 1;
   if (sms < 1) return SV_ERR_CUDA;
   const int workers = sms * blocks_per_sm(nt);
-  if (!aligned(workspace, 16) || workspace_bytes < prefix_bytes(B) + start_bytes(workers) + part_bytes(workers, nt, head_dim))
+  if (!aligned(workspace, 16) || workspace_bytes < workspace_size(B, workers, nt, head_dim))
     return SV_ERR_WORKSPACE;
   AttnArgs A = {};
   A.w = w;
@@ -1142,7 +1176,8 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   A.lse = lse;
   A.prefix = static_cast<long long*>(workspace);
   A.start = reinterpret_cast<Start*>(static_cast<char*>(workspace) + prefix_bytes(B));
-  A.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + prefix_bytes(B) + start_bytes(workers));
+  A.failed = static_cast<uint8_t*>(workspace) + prefix_bytes(B) + start_bytes(workers);
+  A.part = reinterpret_cast<float*>(A.failed + failed_bytes(workers));
   A.workers = workers;
   A.group = q_heads / kv_heads;
   A.group_mul = ((1 << 16) + A.group - 1) / A.group;

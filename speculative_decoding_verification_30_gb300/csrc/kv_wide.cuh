@@ -71,14 +71,19 @@ __device__ __forceinline__ void arrive(unsigned long long* b) {
 __device__ __forceinline__ void expect(unsigned long long* b, int bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
 }
-// Waits for a phase unless another wait of the block has run out.
-__device__ __forceinline__ bool wait(unsigned long long* b, uint32_t parity, volatile int* err) {
+// Waits for a phase, for at most `limit` ns, unless another wait of the block has run out.
+__device__ __forceinline__ bool wait(unsigned long long* b, uint32_t parity, volatile int* err,
+                                     uint64_t limit = SPEC_KV_WAIT_NS) {
   const uint32_t at = smem_u32(b);
+  if (limit == 0) {   // a test's
+    *err = 1;
+    return false;
+  }
   if (arrived(at, parity)) return true;
   const uint64_t t0 = now_ns();
   while (!arrived(at, parity)) {
     if (*err) return false;
-    if (now_ns() - t0 > WAIT_NS) {
+    if (now_ns() - t0 > limit) {
       *err = 1;
       return false;
     }
@@ -293,7 +298,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     float eks = 1.f, elv = 0.f, einv = 1.f;
     const int P = w.page_size, shift = __ffs(P) - 1, box = min(P, TOK);
     int j = 0, ni = 0;   // units, items
-    bool ok = true;
+    int nk = 0, nv = 0;  // units whose keys and values were asked for
+    bool ok = true, kend = false, vend = false;
     for (;; ++j) {
       if (ct < OVERHEAD) {
         cu += OVERHEAD - ct;
@@ -311,8 +317,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           arrive(&C.kfull[ks_]);
           arrive(&C.ready[ni % NM]);
         }
+        kend = true;
         if (j >= NV) ok = wait_warp(&C.vempty[vs_], (uint32_t)(j / NV - 1) & 1, err);
+        if (!ok) break;
         if (lane == 0) arrive(&C.vfull[vs_]);
+        vend = true;
         break;
       }
       const int tok0 = (cp.tile0 + ct - OVERHEAD) * TOK;
@@ -372,14 +381,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
       const int y = (pg * w.kv_heads + ch) * P + (at & (P - 1)), d = (at - tok0) * D;
       if (mine) copy_box(smem_u32(sk + ks_ * TILE8) + d, &map_k, y, smem_u32(&C.kfull[ks_]));
+      ++nk;
       if (j >= NV) ok = wait_warp(&C.vempty[vs_], (uint32_t)(j / NV - 1) & 1, err);
-      if (!ok) {
-        ++j;
-        break;
-      }
+      if (!ok) break;
       if (lane == 0) expect(&C.vfull[vs_], bytes);
       __syncwarp();
       if (mine) copy_box(smem_u32(sv + vs_ * TILE8) + d, &map_v, y, smem_u32(&C.vfull[vs_]));
+      ++nv;
       ++cu;
       if (++ct == cp.tiles + OVERHEAD) {
         ct = 0;
@@ -397,15 +405,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-    if (*err) {   // let the copies land that were asked for (each wait bounded)
-      __syncwarp();
-      if (lane == 0) {
-        A.prefix[w.B + 2] = 1;
-        int never = 0;
-        for (int i = max(0, j - NK); i < j; ++i) wait(&C.kfull[i % NK], (uint32_t)(i / NK) & 1, &never);
-        for (int i = max(0, j - NV); i < j; ++i) wait(&C.vfull[i % NV], (uint32_t)(i / NV) & 1, &never);
-      }
+    // What was asked for lands before the block ends, also when the others have stopped. (The
+    // END went to stages that were empty.)
+    if (lane == 0) {
+      int never = 0;
+      for (int i = max(0, nk - NK); i < nk; ++i)
+        if (!(kend && i % NK == j % NK)) wait(&C.kfull[i % NK], (uint32_t)(i / NK) & 1, &never, LAND_NS);
+      for (int i = max(0, nv - NV); i < nv; ++i)
+        if (!(vend && i % NV == j % NV)) wait(&C.vfull[i % NV], (uint32_t)(i / NV) & 1, &never, LAND_NS);
     }
+    __syncwarp();
   } else if (warp == 1) {
     // --- products, issued by one thread
     if (lane == 0) {
@@ -471,7 +480,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // wake the rows for the END
       commit(&C.done);
       int never = 0;
-      wait(&C.done, 0, &never);
+      wait(&C.done, 0, &never, LAND_NS);
     }
     __syncwarp();
   } else if (warp < 4 || warp >= 12) {
@@ -706,8 +715,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
     }
   }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");   // of rows that have stopped
   before_sync();
   __syncthreads();
+  set_failed(A, tid, C.err);
   if (warp == 1) {
     after_sync();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
