@@ -60,8 +60,8 @@ sv_status spec_token_logprobs(const void* logits, sv_dtype dtype, int R, int V, 
  *                - g_H p_j (ln p_j + H) )
  *   logits, dtype, R, V, row_stride, tokens, temperature: as in the forward call
  *   lse, entropy   [R] float: the forward call's outputs. Probabilities are
- *               exp(x / T - lse) up to |lse| = 1024; past that lse is too coarse and they
- *               are formed from the row.
+ *               exp(x / T - lse) up to |lse| = 64, where the rounding of lse is 2^-19 at
+ *               most; past that they are formed from the row's own maximum and sum.
  *   grad_logprob, grad_entropy [R] float: either may be NULL (zero)
  *   top_ids [R, top_n] int32 (ids outside [0, V) count for nothing) and
  *   grad_top [R, top_n] float: NULL when top_n is 0

@@ -730,59 +730,131 @@ __device__ __forceinline__ void grad_at(float& x0, float& x1, const Coef& f) {
   unpair(mul2(pair(ex2(a), ex2(b)), k), x0, x1);
 }
 
-// Rows whose lse is past this have their probabilities from the row itself: an lse of
-// 32 bits is known to 2^-24 of its size only, and so would they be.
-constexpr float MAX_LSE = 1024.f;
+// An lse of 32 bits is known to 2^-25 of its size at best, and so would every probability
+// be that is formed from it. Up to here that is 2^-19, about what the forward's sum is good to;
+// rows past it (low temperatures, logits far from zero) find their maximum and sum again.
+constexpr float FAR_LSE = 64.f;
+// CTAs that such rows are spread over, at least one a row and at most as many as it has chunks: more
+// read each row more often, fewer leave SMs idle (rows of 151,936 bf16, all past FAR_LSE: 2 rows 19
+// us, 130 rows 62, 512 rows 154, against 49 if none is; with 1,216 CTAs 130 rows a quarter longer).
+constexpr int FAR_CTAS = 608;
 
-// Such a row, by one CTA (rare: finite masks on every token, logits in the thousands). All
-// is read before anything is written: the gradient may take the logits' place.
+// f(logit) for the elements [e0, e1) of a row, four 16-byte loads of a thread on their way.
+// Elements of vectors that are not there are -inf.
+template <typename T, typename F>
+__device__ __forceinline__ void over_row(const T* x, int e0, int e1, F&& f) {
+  constexpr int EPV = Elem<T>::EPV, U = 4;
+  const int tid = threadIdx.x;
+  const int a0 = min((int)(((16 - (reinterpret_cast<uintptr_t>(x + e0) & 15)) & 15) / sizeof(T)), e1 - e0);
+  const int nvec = (e1 - e0 - a0) / EPV, loose = e1 - e0 - nvec * EPV;
+#pragma unroll 1
+  for (int i = tid; i < nvec; i += U * BT) {
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      v[u] = i + u * BT < nvec ? *reinterpret_cast<const uint4*>(x + e0 + a0 + (i + u * BT) * EPV) : none_vec<T>();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float z[EPV];
+      unpack<T>(v[u], z);
+#pragma unroll
+      for (int j = 0; j < EPV; ++j) f(z[j]);
+    }
+  }
+  if (tid < loose) f(Elem<T>::get(x + e0 + (tid < a0 ? tid : nvec * EPV + tid)));
+}
+
+// A row past FAR_LSE: each of `parts` CTAs reads all of it and writes its part. A gradient that
+// takes the logits' place has one part: all is read before anything is written.
 template <typename T>
-__device__ __noinline__ void grad_of_row(const T* x, T* y, int V, int tok, float temp, float gl, float gh, float H,
-                                         int n, const int32_t* ids, const float* gtop) {
-  __shared__ float part[BT / 32];
+__device__ __noinline__ void far_part(const T* x, T* y, int V, int part, int parts, int tok, float temp, float gl,
+                                      float gh, float H, int n, const int32_t* ids, const float* gtop) {
+  constexpr int EPV = Elem<T>::EPV;
+  __shared__ float warps[BT / 32];
+  __shared__ int fix_id[MAX_FIX];
+  __shared__ float fix_g[MAX_FIX];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float c = LOG2E / temp;
-  float m = -INFINITY, s = 0.f, sum = gl;
-#pragma unroll 1
-  for (int i = tid; i < V; i += BT) m = fmaxf(m, Elem<T>::get(x + i));
+  if (tid <= n) {
+    fix_id[tid] = tid < n ? ids[tid] : tok;
+    fix_g[tid] = tid < n ? gtop[tid] : gl;
+  }
+  float m = -INFINITY, s = 0.f, sum = 0.f;
+  over_row<T>(x, 0, V, [&](float z) { m = fmaxf(m, z); });
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) part[warp] = m;
+  if (lane == 0) warps[warp] = m;
   __syncthreads();
 #pragma unroll 1
-  for (int w = 0; w < BT / 32; ++w) m = fmaxf(m, part[w]);
-#pragma unroll 1
-  for (int i = tid; i < V; i += BT) s += ex2(fmaxf((Elem<T>::get(x + i) - m) * c, U_MIN));
+  for (int w = 0; w < BT / 32; ++w) m = fmaxf(m, warps[w]);
+  over_row<T>(x, 0, V, [&](float z) { s += ex2(fmaxf((z - m) * c, U_MIN)); });
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   __syncthreads();
-  if (lane == 0) part[warp] = s;
+  if (lane == 0) warps[warp] = s;
+  // the logits of the token and the alternatives, before they may be written over
+  const int id = tid <= n ? fix_id[tid] : -1;
+  const float xs = id >= 0 && id < V ? Elem<T>::get(x + id) : 0.f;
   __syncthreads();
   s = 0.f;
 #pragma unroll 1
-  for (int w = 0; w < BT / 32; ++w) s += part[w];
+  for (int w = 0; w < BT / 32; ++w) s += warps[w];
   const float l2 = log2f(s);
 #pragma unroll 1
-  for (int k = 0; k < n; ++k)
-    if (ids[k] >= 0 && ids[k] < V) sum += gtop[k];
+  for (int k = 0; k <= n; ++k)
+    if (fix_id[k] >= 0 && fix_id[k] < V) sum += fix_g[k];
+  const float k0 = sum + gh * H, k1 = gh * LN2;
+  const auto at = [&](float z, float up) {
+    const float u = fmaxf((z - m) * c, U_MIN) - l2;
+    return (up - ex2(u) * fmaf(k1, u, k0)) / temp;
+  };
+  const int b0 = (int)((long long)V * part / parts) & ~63, b1 = part + 1 == parts ? V : (int)((long long)V * (part + 1) / parts) & ~63;
+  const uintptr_t xa = reinterpret_cast<uintptr_t>(x + b0), ya = reinterpret_cast<uintptr_t>(y + b0);
+  const int a0 = min((int)(((16 - (xa & 15)) & 15) / sizeof(T)), b1 - b0);
+  const int nvec = ((xa ^ ya) & 15) == 0 ? (b1 - b0 - a0) / EPV : 0, loose = b1 - b0 - nvec * EPV;
 #pragma unroll 1
-  for (int i = tid; i < V; i += BT) {
-    const float u = fmaxf((Elem<T>::get(x + i) - m) * c, U_MIN) - l2;
-    float up = i == tok ? gl : 0.f;
+  for (int i = tid; i < nvec; i += BT) {
+    float z[EPV];
+    unpack<T>(*reinterpret_cast<const uint4*>(x + b0 + a0 + i * EPV), z);
+#pragma unroll
+    for (int j = 0; j < EPV; ++j) z[j] = at(z[j], 0.f);
+    uint4 o;
+    if (sizeof(T) == 2) {
+      __nv_bfloat162 b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = __floats2bfloat162_rn(z[2 * j % EPV], z[(2 * j + 1) % EPV]);
+      o = *reinterpret_cast<uint4*>(b);
+    } else {
+      o = make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
+    }
+    *reinterpret_cast<uint4*>(y + b0 + a0 + i * EPV) = o;
+  }
 #pragma unroll 1
-    for (int k = 0; k < n; ++k)
-      if (ids[k] == i) up += gtop[k];
-    y[i] = Elem<T>::put((up - ex2(u) * (sum + gh * fmaf(LN2, u, H))) / temp);
+  for (int i = tid; i < loose; i += BT) {
+    const int e = b0 + (i < a0 ? i : nvec * EPV + i);
+    y[e] = Elem<T>::put(at(Elem<T>::get(x + e), 0.f));
+  }
+  __syncthreads();
+  if (id >= b0 && id < b1) {   // one thread for each place that has a gradient of its own
+    float up = 0.f;
+    bool first = true;
+#pragma unroll 1
+    for (int k = 0; k <= n; ++k)
+      if (fix_id[k] == id) {
+        up += fix_g[k];
+        first &= k >= tid;
+      }
+    if (first) y[id] = Elem<T>::put(at(xs, up));
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(BT)
+__global__ void __launch_bounds__(BT, 1024 / BT)   // the rare path may not cost the other one a block on an SM
     logprobs_grad_kernel(const T* logits, int V, long long ld, const int32_t* __restrict__ tokens,
                          const float* __restrict__ temperature, const float* __restrict__ lse,
                          const float* __restrict__ entropy, const float* __restrict__ grad_lp,
                          const float* __restrict__ grad_h, int n, const int32_t* __restrict__ top_ids,
-                         const float* __restrict__ grad_top, T* grad, long long gld, int chunks) {
+                         const float* __restrict__ grad_top, T* grad, long long gld, int chunks, int far_parts) {
   constexpr int EPV = Elem<T>::EPV;
   constexpr int CHUNK = BT * BU * EPV;
   __shared__ int fix_id[MAX_FIX];
@@ -790,7 +862,7 @@ __global__ void __launch_bounds__(BT)
   __shared__ int nfix;
   __shared__ Coef coef;
   __shared__ float fill;   // what a row without a gradient gets: 0, or NaN for a data error
-  __shared__ bool whole;   // the row is one CTA's
+  __shared__ bool far;     // past FAR_LSE
   const long long row = blockIdx.x / chunks;
   const int e0 = (int)(blockIdx.x % chunks) * CHUNK;   // the chunk's first element
   const int tid = threadIdx.x;
@@ -844,17 +916,18 @@ __global__ void __launch_bounds__(BT)
       f.k0 = -(gl + sum + gh * H) / temp;
       f.k1 = -gh * LN2 / temp;
       if (!ok) f.chi = NAN;
-      whole = tok >= 0 && tok < V && fabsf(L) > MAX_LSE;
+      far = tok >= 0 && tok < V && fabsf(L) > FAR_LSE;
       coef = f;
     }
   }
   __syncthreads();
-  if (whole) {
-    if (e0 == 0) {
+  if (far) {
+    const int part = (int)(blockIdx.x % chunks);
+    if (part < far_parts) {
       float temp = temperature ? temperature[row] : 1.f;
       if (temp == 0.f) temp = 1.f;
-      grad_of_row<T>(x, y, V, tok, temp, grad_lp ? grad_lp[row] : 0.f, grad_h ? grad_h[row] : 0.f, entropy[row], n,
-                     top_ids + row * n, grad_top + row * n);
+      far_part<T>(x, y, V, part, far_parts, tok, temp, grad_lp ? grad_lp[row] : 0.f, grad_h ? grad_h[row] : 0.f,
+                  entropy[row], n, top_ids + row * n, grad_top + row * n);
     }
     return;
   }
@@ -956,9 +1029,11 @@ static sv_status backward(const void* logits, int R, int V, long long ld, const 
   const int chunks = (V + chunk - 1) / chunk;
   const long long blocks = (long long)R * chunks;
   if (blocks > 2147483647LL) return SV_ERR_SHAPE;
+  // Parts of a row past FAR_LSE: more read the row more often, fewer leave SMs idle.
+  const int far_parts = logits == grad || R >= FAR_CTAS ? 1 : FAR_CTAS / R < chunks ? FAR_CTAS / R : chunks;
   logprobs_grad_kernel<T><<<(unsigned)blocks, BT, 0, st>>>(static_cast<const T*>(logits), V, ld, tokens, temp, lse,
                                                           ent, glp, gh, n, ids, gtop, static_cast<T*>(grad), gld,
-                                                          chunks);
+                                                          chunks, far_parts);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
