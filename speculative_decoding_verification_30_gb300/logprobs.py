@@ -71,6 +71,7 @@ class _Function(torch.autograd.Function):
     def forward(ctx, logits, tokens, temperature, top_n, stream):
         r = _forward(logits, tokens, temperature, top_n, stream)
         ctx.save_for_backward(logits, tokens, temperature, r.lse, r.entropy, r.top_ids)
+        ctx.done = None if stream is None else stream.record_event()
         ctx.mark_non_differentiable(r.rank, r.lse, r.top_ids)
         ctx.set_materialize_grads(False)
         return tuple(r)
@@ -81,6 +82,14 @@ class _Function(torch.autograd.Function):
         logits, tokens, temperature, lse, entropy, ids = ctx.saved_tensors
         if g_lp is None and g_h is None and g_top is None:
             return None, None, None, None, None
+        if ctx.done is not None:
+            # The forward pass ran on a stream of its own: this one comes after it, and the
+            # allocator learns that what it left is in use here.
+            here = torch.cuda.current_stream(logits.device)
+            here.wait_event(ctx.done)
+            for t in (logits, tokens, temperature, lse, entropy, ids):
+                if t is not None:
+                    t.record_stream(here)
         g = [None if t is None else t.contiguous() for t in (g_lp, g_h, g_top)]
         d = spec_token_logprobs_backward(logits, tokens, lse, entropy, temperature, g[0], g[1],
                                          ids if g[2] is not None else None, g[2])

@@ -1,0 +1,38 @@
+"""GPU: what has a gradient, what refuses one, and a forward pass on another stream than its
+backward pass."""
+import pytest
+import torch
+
+import speculative_decoding_verification_30_gb300 as sv
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+E = sv.SpecVerifyError
+
+
+def _rows():
+    g = torch.Generator().manual_seed(1)
+    return torch.randn(4, 500, generator=g).to(DEV), torch.tensor([1, 2, -1, 499], dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("n", [0, 5])
+def test_forward_on_a_side_stream(n):
+    x, tok = _rows()
+    ref = x.clone().requires_grad_()
+    r = sv.spec_token_logprobs(ref, tok, top_n=n)
+    (r.logprob.sum() + r.entropy.sum()).backward()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        y = x.clone().requires_grad_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)                  # the side stream is some milliseconds behind
+        r = sv.spec_token_logprobs(y, tok, top_n=n, stream=side)
+        one = torch.ones(4, device=DEV)
+        d, = torch.autograd.grad([r.logprob, r.entropy], y, [one, one])
+        del r
+        # memory of the forward's outputs must not be handed out before the gradient has read it
+        with torch.cuda.stream(side):
+            junk = [torch.full((4,), float("nan"), device=DEV) for _ in range(8)]
+        assert torch.equal(d, ref.grad)
+        del junk
