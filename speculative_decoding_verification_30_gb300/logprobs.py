@@ -105,11 +105,14 @@ def spec_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature:
     `temperature` [...] (float32) divides the logits; 0 counts as 1. A row whose token
     is negative is skipped (outputs 0, rank and ids -1), so the out_tokens of
     spec_verify can be scored as they are. Data errors give NaN with rank and ids -1.
-    When logits.requires_grad, logprob, entropy and top_logprobs are differentiable."""
+    When logits.requires_grad, logprob, entropy and top_logprobs are differentiable with
+    respect to them; a temperature that requires a gradient is refused."""
     if not isinstance(tokens, torch.Tensor):
         raise SpecVerifyError("tokens must be a CUDA tensor")
     if not isinstance(top_n, int) or not 0 <= top_n <= 32:
         raise SpecVerifyError("top_n must be 0..32")
+    if torch.is_grad_enabled() and getattr(temperature, "requires_grad", False):
+        raise SpecVerifyError("the temperature has no gradient: pass it detached")
     if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():
         return TokenLogprobs(*_Function.apply(logits, tokens, temperature, top_n, stream))
     return _forward(logits, tokens, temperature, top_n, stream)

@@ -15,6 +15,18 @@ def _rows():
     return torch.randn(4, 500, generator=g).to(DEV), torch.tensor([1, 2, -1, 499], dtype=torch.int32, device=DEV)
 
 
+def test_a_temperature_that_requires_a_gradient_is_refused():
+    x, tok = _rows()
+    temp = torch.ones(4, device=DEV, requires_grad=True)
+    for logits in (x, x.clone().requires_grad_()):
+        with pytest.raises(E):
+            sv.spec_token_logprobs(logits, tok, temp)
+    with torch.no_grad():
+        r = sv.spec_token_logprobs(x, tok, temp)
+    ref = sv.spec_token_logprobs(x, tok, temp.detach())
+    assert all(torch.equal(a, b) for a, b in zip(r, ref))
+
+
 @pytest.mark.parametrize("n", [0, 5])
 def test_forward_on_a_side_stream(n):
     x, tok = _rows()
