@@ -4,6 +4,7 @@ from __future__ import annotations
 import contextlib
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import SpecVerifyError
 
@@ -24,6 +25,13 @@ def ptr(t: torch.Tensor, name: str, dtype, device) -> int:
     if t.device != device:
         raise SpecVerifyError(f"{name} must be on {device}, got {t.device}")
     raise SpecVerifyError(f"{name} must be contiguous")
+
+
+def no_tangent(call: str, *tensors):
+    """Refuses forward-mode AD: the calls would drop the tangents in silence."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and unpack_dual(t).tangent is not None:
+            raise SpecVerifyError(f"{call} carries no forward-mode tangents")
 
 
 class _Here:

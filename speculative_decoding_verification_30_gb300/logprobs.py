@@ -7,7 +7,7 @@ from typing import NamedTuple
 import torch
 
 from . import SpecVerifyError, _check, _dtype_code, load
-from ._launch import on_device, ptr
+from ._launch import no_tangent, on_device, ptr
 
 
 class TokenLogprobs(NamedTuple):
@@ -111,6 +111,7 @@ def spec_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature:
         raise SpecVerifyError("tokens must be a CUDA tensor")
     if not isinstance(top_n, int) or not 0 <= top_n <= 32:
         raise SpecVerifyError("top_n must be 0..32")
+    no_tangent("spec_token_logprobs", logits, temperature)
     if torch.is_grad_enabled() and getattr(temperature, "requires_grad", False):
         raise SpecVerifyError("the temperature has no gradient: pass it detached")
     if isinstance(logits, torch.Tensor) and logits.requires_grad and torch.is_grad_enabled():

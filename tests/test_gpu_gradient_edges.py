@@ -2,6 +2,7 @@
 backward pass."""
 import pytest
 import torch
+import torch.autograd.forward_ad as fwd
 
 import speculative_decoding_verification_30_gb300 as sv
 
@@ -25,6 +26,18 @@ def test_a_temperature_that_requires_a_gradient_is_refused():
         r = sv.spec_token_logprobs(x, tok, temp)
     ref = sv.spec_token_logprobs(x, tok, temp.detach())
     assert all(torch.equal(a, b) for a, b in zip(r, ref))
+
+
+def test_forward_mode_tangents_are_refused():
+    x, tok = _rows()
+    with fwd.dual_level():
+        dual = fwd.make_dual(x, torch.ones_like(x))
+        with pytest.raises(E):
+            sv.spec_token_logprobs(dual, tok)
+        with pytest.raises(E):
+            sv.spec_token_logprobs(x, tok, fwd.make_dual(torch.ones(4, device=DEV), torch.ones(4, device=DEV)))
+        ok = sv.spec_token_logprobs(x, tok)
+    assert torch.equal(ok.logprob, sv.spec_token_logprobs(x, tok).logprob)
 
 
 @pytest.mark.parametrize("n", [0, 5])
