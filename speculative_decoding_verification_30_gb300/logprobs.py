@@ -72,13 +72,15 @@ class _Function(torch.autograd.Function):
         r = _forward(logits, tokens, temperature, top_n, stream)
         ctx.save_for_backward(logits, tokens, temperature, r.lse, r.entropy, r.top_ids)
         ctx.done = None if stream is None else stream.record_event()
-        ctx.mark_non_differentiable(r.rank, r.lse, r.top_ids)
+        ctx.mark_non_differentiable(r.rank, r.top_ids)
         ctx.set_materialize_grads(False)
         return tuple(r)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, g_lp, _rank, g_h, _lse, _ids, g_top):
+    def backward(ctx, g_lp, _rank, g_h, g_lse, _ids, g_top):
+        if g_lse is not None:
+            raise SpecVerifyError("lse has no gradient: use it detached in a loss")
         logits, tokens, temperature, lse, entropy, ids = ctx.saved_tensors
         if g_lp is None and g_h is None and g_top is None:
             return None, None, None, None, None
@@ -106,7 +108,8 @@ def spec_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, temperature:
     is negative is skipped (outputs 0, rank and ids -1), so the out_tokens of
     spec_verify can be scored as they are. Data errors give NaN with rank and ids -1.
     When logits.requires_grad, logprob, entropy and top_logprobs are differentiable with
-    respect to them; a temperature that requires a gradient is refused."""
+    respect to them. A temperature that requires a gradient is refused, and so is a backward
+    pass through lse."""
     if not isinstance(tokens, torch.Tensor):
         raise SpecVerifyError("tokens must be a CUDA tensor")
     if not isinstance(top_n, int) or not 0 <= top_n <= 32:

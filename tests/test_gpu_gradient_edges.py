@@ -40,6 +40,17 @@ def test_forward_mode_tangents_are_refused():
     assert torch.equal(ok.logprob, sv.spec_token_logprobs(x, tok).logprob)
 
 
+def test_a_loss_on_lse_is_refused_not_lost():
+    x, tok = _rows()
+    x.requires_grad_()
+    r = sv.spec_token_logprobs(x, tok)
+    with pytest.raises(E):
+        (r.logprob.sum() + r.lse.square().sum()).backward()
+    r = sv.spec_token_logprobs(x, tok)
+    (r.logprob.sum() + r.lse.detach().square().sum()).backward()
+    assert torch.isfinite(x.grad).all()
+
+
 @pytest.mark.parametrize("n", [0, 5])
 def test_forward_on_a_side_stream(n):
     x, tok = _rows()
