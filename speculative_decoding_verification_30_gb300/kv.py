@@ -68,6 +68,15 @@ def _window(seq_len, cu_tokens, page_table, device):
             ptr(page_table, "page_table", i32, device)), B, max_pages
 
 
+_I32 = 2 ** 31
+
+
+def _whole(x, name, lo, hi):
+    """Refuses what is no whole number of lo..hi: a larger one would be cut to 32 bits."""
+    if not isinstance(x, int) or not lo <= x <= hi:
+        raise SpecVerifyError(f"{name} must be a whole number of {lo}..{hi}")
+
+
 def _heads(x, name, dtype, device, dim):
     """(address, token stride, N, heads) of [N, heads, dim] with adjacent heads."""
     try:
@@ -106,6 +115,7 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
     vp, vs, vn, vh = _heads(v, "v", ty, dev, dim)
     if kh != heads or vh != heads or vn != N:
         raise SpecVerifyError("k and v must be [N, kv_heads, head_dim] of the cache")
+    _whole(max_tokens, "max_tokens", 1, N)
     rot = max_pos = 0
     cp = sp = None
     if (cos is None) != (sin is None):
@@ -141,7 +151,9 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
 
 
 def spec_kv_attention_workspace_bytes(B: int, max_tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
-    """Bytes of workspace of spec_kv_attention on the current device."""
+    """Bytes of workspace of spec_kv_attention on the current device; 0 for arguments outside its limits."""
+    if not all(0 <= x < _I32 for x in (B, max_tokens, q_heads, kv_heads, head_dim)):
+        return 0
     return int(load().spec_kv_attention_workspace_bytes(B, max_tokens, q_heads, kv_heads, head_dim))
 
 
@@ -162,6 +174,8 @@ def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_to
     cache, (pages, heads, page, dim) = _cache(kv, dev)
     win, B, max_pages = _window(seq_len, cu_tokens, page_table, dev)
     qp, qs, N, qh = _heads(q, "q", torch.bfloat16, dev, dim)
+    _whole(max_tokens, "max_tokens", 1, N)
+    _whole(window, "window", 0, _I32 - 1)
     if scale is None:
         scale = dim ** -0.5
     lib = load()

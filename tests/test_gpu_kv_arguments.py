@@ -1,0 +1,46 @@
+"""GPU: arguments of the cache's calls that must be refused or reported, not changed in silence."""
+import pytest
+import torch
+
+import speculative_decoding_verification_30_gb300 as sv
+from tests.test_gpu_kv import _i32
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+E = sv.SpecVerifyError
+
+
+def _call():
+    g = torch.Generator().manual_seed(2)
+    cache = sv.KVCache.empty(8, 16, 2, 64, device=DEV)
+    q, k = torch.randn(4, 4, 64, generator=g).to(torch.bfloat16).to(DEV), torch.randn(4, 2, 64, generator=g).to(torch.bfloat16).to(DEV)
+    return q, k, cache, (_i32([3]), _i32([0, 4]), _i32([[0, 1]]))
+
+
+@pytest.mark.parametrize("most", [2 ** 32 + 4, -2 ** 32 + 4, 0, 5, 3.5, None, "4"])
+def test_max_tokens(most):
+    q, k, cache, win = _call()
+    with pytest.raises(E):
+        sv.spec_kv_append(k, k, cache, *win, most)
+    with pytest.raises(E):
+        sv.spec_kv_attention(q, cache, *win, most)
+
+
+@pytest.mark.parametrize("window", [2 ** 32 + 2, 2 ** 32, -2 ** 32, 2.5, None])
+def test_window(window):
+    q, k, cache, win = _call()
+    with pytest.raises(E):
+        sv.spec_kv_attention(q, cache, *win, 4, window=window)
+
+
+def test_windows_past_every_position_are_no_window():
+    q, k, cache, win = _call()
+    sv.spec_kv_append(k, k, cache, *win, 4)
+    a, b = sv.spec_kv_attention(q, cache, *win, 4), sv.spec_kv_attention(q, cache, *win, 4, window=2 ** 31 - 1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_workspace_of_arguments_outside_the_limits():
+    assert sv.spec_kv_attention_workspace_bytes(1, 4, 4, 2, 64) > 0
+    for bad in ((2 ** 32 + 1, 4, 4, 2, 64), (1, 2 ** 32 + 4, 4, 2, 64), (1, -2 ** 32 + 4, 4, 2, 64), (0, 4, 4, 2, 64)):
+        assert sv.spec_kv_attention_workspace_bytes(*bad) == 0
