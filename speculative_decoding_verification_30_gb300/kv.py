@@ -127,6 +127,8 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
         rot *= 2
         cp, sp = ptr(cos, "cos", torch.float32, dev), ptr(sin, "sin", torch.float32, dev)
     fp = None if flag is None else ptr(flag, "flag", torch.int32, dev)
+    if fp == 0:
+        raise SpecVerifyError("flag must be [1] int32")
     with on_device(dev, stream, k, v, *kv, seq_len, cu_tokens, page_table, q, cos, sin, q_out, flag) as st:
         qp = op = None
         qs, qh = 0, heads

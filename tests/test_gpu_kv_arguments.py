@@ -44,3 +44,9 @@ def test_workspace_of_arguments_outside_the_limits():
     assert sv.spec_kv_attention_workspace_bytes(1, 4, 4, 2, 64) > 0
     for bad in ((2 ** 32 + 1, 4, 4, 2, 64), (1, 2 ** 32 + 4, 4, 2, 64), (1, -2 ** 32 + 4, 4, 2, 64), (0, 4, 4, 2, 64)):
         assert sv.spec_kv_attention_workspace_bytes(*bad) == 0
+
+
+def test_a_flag_without_a_place_is_refused():
+    q, k, cache, win = _call()
+    with pytest.raises(E):
+        sv.spec_kv_append(k, k, cache, *win, 4, flag=_i32([]))
