@@ -139,7 +139,7 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
             if q_out is None:
                 q_out = torch.empty((N, qh, dim), dtype=ty, device=dev)
                 op = q_out.data_ptr()
-            elif q_out.shape != q.shape:
+            elif _shape(q_out) != q.shape:
                 raise SpecVerifyError("q_out must have q's shape")
             else:
                 op = ptr(q_out, "q_out", ty, dev)
@@ -187,18 +187,19 @@ def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_to
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
             wp = workspace.data_ptr()
         else:
-            size, wp = workspace.numel(), ptr(workspace, "workspace", torch.uint8, dev)
+            wp = ptr(workspace, "workspace", torch.uint8, dev)
+            size = workspace.numel()
         if out is None:
             out = torch.empty((N, qh, dim), dtype=torch.bfloat16, device=dev)
             op = out.data_ptr()
-        elif out.shape != (N, qh, dim):
+        elif _shape(out) != (N, qh, dim):
             raise SpecVerifyError("out must be [N, q_heads, head_dim]")
         else:
             op = ptr(out, "out", torch.bfloat16, dev)
         if lse is None:
             lse = torch.empty((N, qh), dtype=torch.float32, device=dev)
             lp = lse.data_ptr()
-        elif lse.shape != (N, qh):
+        elif _shape(lse) != (N, qh):
             raise SpecVerifyError("lse must be [N, q_heads]")
         else:
             lp = ptr(lse, "lse", torch.float32, dev)

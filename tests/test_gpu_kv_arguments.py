@@ -50,3 +50,12 @@ def test_a_flag_without_a_place_is_refused():
     q, k, cache, win = _call()
     with pytest.raises(E):
         sv.spec_kv_append(k, k, cache, *win, 4, flag=_i32([]))
+
+
+def test_outputs_that_are_no_tensors_are_refused():
+    q, k, cache, win = _call()
+    for bad in (lambda: sv.spec_kv_attention(q, cache, *win, 4, out=1), lambda: sv.spec_kv_attention(q, cache, *win, 4, lse=[0.0]),
+                lambda: sv.spec_kv_attention(q, cache, *win, 4, workspace=b"x" * 9),
+                lambda: sv.spec_kv_append(k, k, cache, *win, 4, q=q, q_out=1)):
+        with pytest.raises(E):
+            bad()
