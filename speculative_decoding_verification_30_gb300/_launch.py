@@ -34,6 +34,25 @@ def no_tangent(call: str, *tensors):
             raise SpecVerifyError(f"{call} carries no forward-mode tangents")
 
 
+class _NoGradient(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, call, n, *tensors):
+        ctx.call = call
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise SpecVerifyError(f"{ctx.call} has no gradient")
+
+
+def no_gradient(call: str, outputs: tuple, *inputs):
+    """The outputs of a call that has no gradient: where an input requires one, a backward pass
+    through them raises instead of stopping in silence."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+        return _NoGradient.apply(call, len(outputs), *outputs, *inputs)
+    return outputs
+
+
 class _Here:
     """The device's current stream on the current device: nothing to set or restore."""
     __slots__ = ("handle",)

@@ -7,7 +7,7 @@ from typing import NamedTuple
 import torch
 
 from . import SpecVerifyError, _check, _dtype_code, load
-from ._launch import on_device, ptr
+from ._launch import no_gradient, no_tangent, on_device, ptr
 
 
 class KVCache(NamedTuple):
@@ -104,9 +104,11 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
     [N, q_heads, head_dim] is given (in q_out, which may be q).
 
     seq_len is not advanced: spec_verify_step does that by the tokens it emits. flag [1] int32
-    becomes 1 when a token could not be stored."""
+    becomes 1 when a token could not be stored. The call serves: what enters the cache has no
+    gradient, and a backward pass through the rotated queries raises."""
     if not isinstance(k, torch.Tensor) or not k.is_cuda:
         raise SpecVerifyError("k must be a CUDA tensor")
+    no_tangent("spec_kv_append", k, v, q)
     dev, ty = k.device, k.dtype
     dt = _dtype_code(k)
     cache, (pages, heads, page, dim) = _cache(kv, dev)
@@ -149,7 +151,7 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
                                    max_tokens, max_pages, pages, page, qh, heads, dim, *cache, fp, st)
     if rc:
         _check(rc, "spec_kv_append")
-    return q_out
+    return q_out if q_out is None else no_gradient("spec_kv_append", (q_out,), q, k, v)[0]
 
 
 def spec_kv_attention_workspace_bytes(B: int, max_tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -168,10 +170,13 @@ def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_to
     must have been appended) and, with window > 0, only the last `window` of them. Returns
     (out [N, q_heads, head_dim] bf16, lse [N, q_heads] float32).
 
+    The call serves: a backward pass through its outputs raises.
+
     scale defaults to head_dim^-1/2. workspace: uint8, at least
     spec_kv_attention_workspace_bytes(...) bytes, not shared by calls that may overlap."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise SpecVerifyError("q must be a CUDA tensor")
+    no_tangent("spec_kv_attention", q)
     dev = q.device
     cache, (pages, heads, page, dim) = _cache(kv, dev)
     win, B, max_pages = _window(seq_len, cu_tokens, page_table, dev)
@@ -207,4 +212,4 @@ def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_to
                                    window, op, lp, wp, size, st)
     if rc:
         _check(rc, "spec_kv_attention")
-    return out, lse
+    return no_gradient("spec_kv_attention", (out, lse), q)

@@ -1,6 +1,7 @@
 """GPU: arguments of the cache's calls that must be refused or reported, not changed in silence."""
 import pytest
 import torch
+import torch.autograd.forward_ad as fwd
 
 import speculative_decoding_verification_30_gb300 as sv
 from tests.test_gpu_kv import _i32
@@ -59,3 +60,31 @@ def test_outputs_that_are_no_tensors_are_refused():
                 lambda: sv.spec_kv_append(k, k, cache, *win, 4, q=q, q_out=1)):
         with pytest.raises(E):
             bad()
+
+
+def test_a_backward_pass_through_the_cache_raises():
+    q, k, cache, win = _call()
+    ref = sv.spec_kv_attention(q, cache, *win, 4)
+    q.requires_grad_()
+    out, lse = sv.spec_kv_attention(q, cache, *win, 4)
+    assert torch.equal(out.detach(), ref[0]) and torch.equal(lse.detach(), ref[1])
+    for x in (out, lse):
+        with pytest.raises(E):
+            x.float().sum().backward()
+    cos, sin = sv.rope_tables(64, 64, device=DEV)
+    for a, b in ((q, k), (q.detach(), k.clone().requires_grad_())):
+        r = sv.spec_kv_append(b, b, cache, *win, 4, q=a, cos=cos, sin=sin)
+        with pytest.raises(E):
+            r.float().sum().backward()
+    with torch.no_grad():
+        assert not sv.spec_kv_attention(q, cache, *win, 4)[0].requires_grad
+
+
+def test_forward_mode_tangents_are_refused():
+    q, k, cache, win = _call()
+    with fwd.dual_level():
+        dual = [fwd.make_dual(x, torch.ones_like(x)) for x in (q, k)]
+        for bad in (lambda: sv.spec_kv_attention(dual[0], cache, *win, 4), lambda: sv.spec_kv_append(dual[1], k, cache, *win, 4),
+                    lambda: sv.spec_kv_append(k, dual[1], cache, *win, 4), lambda: sv.spec_kv_append(k, k, cache, *win, 4, q=dual[0])):
+            with pytest.raises(E):
+                bad()
