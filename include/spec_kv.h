@@ -8,7 +8,11 @@
  *         for values; 16-byte aligned
  *   scale [num_pages][kv_heads] float: a cached value is its code times the scale of
  *         its page and head. spec_kv_append writes powers of two; spec_kv_attention
- *         takes any positive scales.
+ *         takes any positive scales of keys under which the logits stay in fp32's range, and
+ *         scales of values of 2^-100 to 2^100 that lie within a factor of 2^96 of one another
+ *         among the keys that a query sees (a page of zeros, to which spec_kv_append
+ *         gives 2^-60, beside values up to 2^44). Past that factor, keys on the pages of the
+ *         smaller scales may be lost from lse and out.
  *   page_table [B][max_pages] int32: page_table[b][j] holds positions j page_size to
  *         (j + 1) page_size - 1 of sequence b. An entry outside [0, num_pages) is
  *         an unmapped page. Pages that a call appends to belong to one sequence;
