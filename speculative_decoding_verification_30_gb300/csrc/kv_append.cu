@@ -338,8 +338,10 @@ static sv_status pick_append(AppendArgs& A, cudaStream_t st) {
   const int units = most * (A.w.head_dim / 16);
   if (units <= 128) return launch_append<T, 128, 1>(A, st);
   if (units <= 256) return launch_append<T, 128, 2>(A, st);
-  if (sizeof(T) == 2) return units <= 512 ? launch_append<T, 128, 4>(A, st) : launch_append<T, 256, 4>(A, st);
-  return units <= 512 ? launch_append<T, 256, 2>(A, st) : launch_append<T, 512, 2>(A, st);
+  if constexpr (sizeof(T) == 2)
+    return units <= 512 ? launch_append<T, 128, 4>(A, st) : launch_append<T, 256, 4>(A, st);
+  else
+    return units <= 512 ? launch_append<T, 256, 2>(A, st) : launch_append<T, 512, 2>(A, st);
 }
 
 }  // namespace svkv
