@@ -40,6 +40,7 @@ namespace cg = cooperative_groups;
 namespace svlp {
 
 constexpr int NT = 256, NW = NT / 32;
+constexpr int SMS = 152;               // of a GB300
 constexpr int UNR = 4;                 // groups a warp loads at once
 constexpr int MAX_TOP = SV_LOGPROBS_MAX_TOP;
 constexpr int MAX_GROUPS = 2048;       // 262,144 fp32 logits in groups of 128
@@ -737,7 +738,7 @@ constexpr float FAR_LSE = 64.f;
 // CTAs that such rows are spread over, at least one a row and at most as many as it has chunks: more
 // read each row more often, fewer leave SMs idle (rows of 151,936 bf16, all past FAR_LSE: 2 rows 19
 // us, 130 rows 62, 512 rows 154, against 49 if none is; with 1,216 CTAs 130 rows a quarter longer).
-constexpr int FAR_CTAS = 608;
+constexpr int FAR_CTAS = 4 * SMS;
 
 // f(logit) for the elements [e0, e1) of a row, four 16-byte loads of a thread on their way.
 // Elements of vectors that are not there are -inf.
@@ -997,7 +998,7 @@ static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 static int cluster_size(int R, int V, int epv) {
   const int groups = (V / epv + 31) / 32;
   int c = 1;
-  while (c < MAX_CLUSTER && (long long)R * c < 304 && groups >= c * NW * UNR) c *= 2;
+  while (c < MAX_CLUSTER && (long long)R * c < 2 * SMS && groups >= c * NW * UNR) c *= 2;
   return c;
 }
 
