@@ -30,8 +30,8 @@
  * Layouts of heads: query head h reads kv head h / (q_heads / kv_heads).
  *
  * Limits: 1 <= B <= 65535, 1 <= N <= 2^24, 1 <= max_tokens <= N, page_size 16, 32,
- * 64 or 128, head_dim 64 or 128, kv_heads 1..256, q_heads a multiple of kv_heads,
- * at most 64 kv_heads, B * max_tokens * kv_heads < 2^31, 1 <= max_pages <= 2^20,
+ * 64 or 128, head_dim 64 or 128, kv_heads 1..256, q_heads a multiple of kv_heads
+ * and at most 64 times it, B * max_tokens * kv_heads < 2^31, 1 <= max_pages <= 2^20,
  * num_pages * kv_heads < 2^31 / page_size. spec_kv_append also refuses windows that
  * would take 2^31 blocks (about B * max_tokens * (q_heads + kv_heads) * head_dim /
  * 2^12). Pointers are device pointers, owned by the caller; nothing is allocated, the
@@ -68,7 +68,9 @@ extern "C" {
  *   flag   [1] int32 or NULL: set to 1 when a token could not be stored because its
  *          page is unmapped or lies past max_pages, its position is past max_pos, or a
  *          sequence has more than max_tokens; never cleared. The other tokens are
- *          stored; a query past max_pos becomes NaN.
+ *          stored; a query past max_pos becomes NaN. Of a sequence with more than
+ *          max_tokens, the first max_tokens are stored and their queries written; the
+ *          rest of its rows of q_out keep what they held.
  * Returns SV_ERR_NULL, SV_ERR_SHAPE, SV_ERR_DTYPE or SV_ERR_ALIGN before launching,
  * SV_ERR_CUDA when the launch fails. */
 sv_status spec_kv_append(const void* k, long long k_stride, const void* v, long long v_stride, const void* q,

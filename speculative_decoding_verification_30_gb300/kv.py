@@ -105,7 +105,10 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
 
     seq_len is not advanced: spec_verify_step does that by the tokens it emits. flag [1] int32
     becomes 1 when a token could not be stored. The call serves: what enters the cache has no
-    gradient, and a backward pass through the rotated queries raises."""
+    gradient, and a backward pass through the rotated queries raises.
+
+    max_tokens bounds the new tokens of a sequence. Of one with more, only the first max_tokens are
+    stored (flag becomes 1) and only their rows of the result are written."""
     if not isinstance(k, torch.Tensor) or not k.is_cuda:
         raise SpecVerifyError("k must be a CUDA tensor")
     no_tangent("spec_kv_append", k, v, q)
@@ -170,7 +173,8 @@ def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_to
     must have been appended) and, with window > 0, only the last `window` of them. Returns
     (out [N, q_heads, head_dim] bf16, lse [N, q_heads] float32).
 
-    The call serves: a backward pass through its outputs raises.
+    The call serves: a backward pass through its outputs raises. Rows of a sequence past its
+    first max_tokens are not written.
 
     scale defaults to head_dim^-1/2. workspace: uint8, at least
     spec_kv_attention_workspace_bytes(...) bytes, not shared by calls that may overlap."""

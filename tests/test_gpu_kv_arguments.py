@@ -88,3 +88,14 @@ def test_forward_mode_tangents_are_refused():
                     lambda: sv.spec_kv_append(k, dual[1], cache, *win, 4), lambda: sv.spec_kv_append(k, k, cache, *win, 4, q=dual[0])):
             with pytest.raises(E):
                 bad()
+
+
+def test_rows_past_max_tokens_keep_what_they_held():
+    q, k, cache, win = _call()
+    out, cos_sin = torch.full_like(q, 7.0), sv.rope_tables(64, 64, device=DEV)
+    flag = _i32([0])
+    sv.spec_kv_append(k, k, cache, *win, 3, q=q, cos=cos_sin[0], sin=cos_sin[1], q_out=out, flag=flag)
+    assert int(flag) == 1 and (out[3] == 7).all() and not (out[:3] == 7).any()
+    att, lse = torch.full_like(q, 7.0), torch.full((4, 4), 7.0, device=DEV)
+    sv.spec_kv_attention(q, cache, *win, 3, out=att, lse=lse)
+    assert (att[3] == 7).all() and (lse[3] == 7).all() and not (lse[:3] == 7).any()
