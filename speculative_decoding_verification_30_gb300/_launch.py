@@ -34,6 +34,14 @@ def no_tangent(call: str, *tensors):
             raise SpecVerifyError(f"{call} carries no forward-mode tangents")
 
 
+def wrote(*tensors) -> None:
+    """Tells autograd that a kernel has written over a caller's tensors: a graph that saved one of
+    them raises in its backward pass."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 class _NoGradient(torch.autograd.Function):
     @staticmethod
     def forward(ctx, call, n, *tensors):

@@ -7,7 +7,7 @@ from typing import NamedTuple
 import torch
 
 from . import SpecVerifyError, _check, _dtype_code, load
-from ._launch import no_gradient, no_tangent, on_device, ptr
+from ._launch import no_gradient, no_tangent, on_device, ptr, wrote
 
 
 class KVCache(NamedTuple):
@@ -136,7 +136,7 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
         raise SpecVerifyError("flag must be [1] int32")
     with on_device(dev, stream, k, v, *kv, seq_len, cu_tokens, page_table, q, cos, sin, q_out, flag) as st:
         qp = op = None
-        qs, qh = 0, heads
+        qs, qh, given = 0, heads, q_out
         if q is not None:
             qp, qs, qn, qh = _heads(q, "q", ty, dev, dim)
             if qn != N:
@@ -154,6 +154,7 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
                                    max_tokens, max_pages, pages, page, qh, heads, dim, *cache, fp, st)
     if rc:
         _check(rc, "spec_kv_append")
+    wrote(given)
     return q_out if q_out is None else no_gradient("spec_kv_append", (q_out,), q, k, v)[0]
 
 
@@ -191,6 +192,7 @@ def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_to
         scale = dim ** -0.5
     lib = load()
     with on_device(dev, stream, q, *kv, seq_len, cu_tokens, page_table, out, lse, workspace) as st:
+        given = (out, lse)
         if workspace is None:
             size = lib.spec_kv_attention_workspace_bytes(B, max_tokens, qh, heads, dim) or 16
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
@@ -216,4 +218,5 @@ def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_to
                                    window, op, lp, wp, size, st)
     if rc:
         _check(rc, "spec_kv_attention")
+    wrote(*given)
     return no_gradient("spec_kv_attention", (out, lse), q)

@@ -7,7 +7,7 @@ from typing import NamedTuple
 import torch
 
 from . import SpecVerifyError, _check, _dtype_code, load
-from ._launch import no_tangent, on_device, ptr
+from ._launch import no_tangent, on_device, ptr, wrote
 
 
 class TokenLogprobs(NamedTuple):
@@ -149,6 +149,7 @@ def spec_token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse
                       ptr(grad_top, "grad_top", torch.float32, dev))
     with on_device(dev, stream, logits, tokens, temperature, lse, entropy, grad_logprob, grad_entropy, top_ids,
                    grad_top, out) as st:
+        given = out
         if out is None:
             out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
         elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev:
@@ -158,4 +159,5 @@ def spec_token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse
                                                  out.data_ptr(), gld, st)
     if rc:
         _check(rc, "spec_token_logprobs_backward")
+    wrote(given)
     return out

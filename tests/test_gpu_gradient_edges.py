@@ -72,3 +72,14 @@ def test_forward_on_a_side_stream(n):
             junk = [torch.full((4,), float("nan"), device=DEV) for _ in range(8)]
         assert torch.equal(d, ref.grad)
         del junk
+
+
+def test_a_graph_that_saved_what_a_call_writes_over_raises():
+    x, tok = _rows()
+    x = (x * 1.0).requires_grad_()
+    r = sv.spec_token_logprobs(x, tok)
+    one = torch.ones(4, device=DEV)
+    d = x.detach()                                         # the same memory
+    sv.spec_token_logprobs_backward(d, tok, r.lse.detach(), r.entropy.detach(), grad_logprob=one, out=d)
+    with pytest.raises(RuntimeError, match="inplace"):
+        r.logprob.sum().backward()

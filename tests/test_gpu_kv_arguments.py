@@ -99,3 +99,15 @@ def test_rows_past_max_tokens_keep_what_they_held():
     att, lse = torch.full_like(q, 7.0), torch.full((4, 4), 7.0, device=DEV)
     sv.spec_kv_attention(q, cache, *win, 3, out=att, lse=lse)
     assert (att[3] == 7).all() and (lse[3] == 7).all() and not (lse[:3] == 7).any()
+
+
+def test_a_graph_that_saved_what_a_call_writes_over_raises():
+    q, k, cache, win = _call()
+    cos, sin = sv.rope_tables(64, 64, device=DEV)
+    out, lse = torch.ones_like(q).requires_grad_(), torch.ones(4, 4, device=DEV).requires_grad_()
+    for x, call in ((out, lambda t: sv.spec_kv_attention(q, cache, *win, 4, out=t)), (lse, lambda t: sv.spec_kv_attention(q, cache, *win, 4, lse=t)),
+                    (out, lambda t: sv.spec_kv_append(k, k, cache, *win, 4, q=t, cos=cos, sin=sin, q_out=t))):
+        y = x.square().sum()
+        call(x.detach())
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.backward()
