@@ -4,7 +4,7 @@ from __future__ import annotations
 import contextlib
 
 import torch
-from torch.autograd.forward_ad import unpack_dual
+from torch.autograd import forward_ad
 
 from . import SpecVerifyError
 
@@ -29,8 +29,10 @@ def ptr(t: torch.Tensor, name: str, dtype, device) -> int:
 
 def no_tangent(call: str, *tensors):
     """Refuses forward-mode AD: the calls would drop the tangents in silence."""
+    if getattr(forward_ad, "_current_level", 0) < 0:      # no dual level is open
+        return
     for t in tensors:
-        if isinstance(t, torch.Tensor) and unpack_dual(t).tangent is not None:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
             raise SpecVerifyError(f"{call} carries no forward-mode tangents")
 
 
@@ -38,8 +40,7 @@ def wrote(*tensors) -> None:
     """Tells autograd that a kernel has written over a caller's tensors: a graph that saved one of
     them raises in its backward pass."""
     for t in tensors:
-        if t is not None:
-            torch.autograd.graph.increment_version(t)
+        torch.autograd.graph.increment_version(t)
 
 
 class _NoGradient(torch.autograd.Function):
@@ -56,9 +57,9 @@ class _NoGradient(torch.autograd.Function):
 def no_gradient(call: str, outputs: tuple, *inputs):
     """The outputs of a call that has no gradient: where an input requires one, a backward pass
     through them raises instead of stopping in silence."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
-        return _NoGradient.apply(call, len(outputs), *outputs, *inputs)
-    return outputs
+    if not torch.is_grad_enabled():
+        return outputs
+    return _NoGradient.apply(call, len(outputs), *outputs, *inputs)
 
 
 class _Here:

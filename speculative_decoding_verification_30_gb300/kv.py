@@ -154,8 +154,11 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, kv: KVCache, seq_len: torch
                                    max_tokens, max_pages, pages, page, qh, heads, dim, *cache, fp, st)
     if rc:
         _check(rc, "spec_kv_append")
-    wrote(given)
-    return q_out if q_out is None else no_gradient("spec_kv_append", (q_out,), q, k, v)[0]
+    if given is not None:
+        wrote(given)
+    if q is not None and (q.requires_grad or k.requires_grad or v.requires_grad):
+        return no_gradient("spec_kv_append", (q_out,), q, k, v)[0]
+    return q_out
 
 
 def spec_kv_attention_workspace_bytes(B: int, max_tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -186,13 +189,14 @@ def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_to
     cache, (pages, heads, page, dim) = _cache(kv, dev)
     win, B, max_pages = _window(seq_len, cu_tokens, page_table, dev)
     qp, qs, N, qh = _heads(q, "q", torch.bfloat16, dev, dim)
-    _whole(max_tokens, "max_tokens", 1, N)
-    _whole(window, "window", 0, _I32 - 1)
+    if type(max_tokens) is not int or type(window) is not int or not (0 < max_tokens <= N and 0 <= window < _I32):
+        _whole(max_tokens, "max_tokens", 1, N)
+        _whole(window, "window", 0, _I32 - 1)
     if scale is None:
         scale = dim ** -0.5
     lib = load()
     with on_device(dev, stream, q, *kv, seq_len, cu_tokens, page_table, out, lse, workspace) as st:
-        given = (out, lse)
+        given = [t for t in (out, lse) if t is not None]
         if workspace is None:
             size = lib.spec_kv_attention_workspace_bytes(B, max_tokens, qh, heads, dim) or 16
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
@@ -218,5 +222,6 @@ def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_to
                                    window, op, lp, wp, size, st)
     if rc:
         _check(rc, "spec_kv_attention")
-    wrote(*given)
-    return no_gradient("spec_kv_attention", (out, lse), q)
+    if given:
+        wrote(*given)
+    return no_gradient("spec_kv_attention", (out, lse), q) if q.requires_grad else (out, lse)

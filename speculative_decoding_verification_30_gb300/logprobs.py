@@ -159,5 +159,6 @@ def spec_token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse
                                                  out.data_ptr(), gld, st)
     if rc:
         _check(rc, "spec_token_logprobs_backward")
-    wrote(given)
+    if given is not None:
+        wrote(given)
     return out
