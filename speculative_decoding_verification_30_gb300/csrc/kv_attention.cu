@@ -23,7 +23,7 @@
 // exponent (weight 2^(s + log2 scale - m)) and the key scale through the logit.
 // Measured: 64 sequences of up to 16,000 tokens, 5 new ones, 32 heads on 8: 198 us, 5,440
 // GB/s, with the matrix pipe at a third and issue at 40%; 4 of 131,000 tokens, 64 heads on
-// 8: 154 us, 4,980 GB/s; 1 of 2,500 tokens 13 us, latency.
+// 8: 154 us, 4,980 GB/s; 1 of 2,500 tokens 13.4 us, latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1007,8 +1007,8 @@ static sv::LaunchCache g_attn_cache;
 
 // Rows of a window from which the wide kernel takes over (head_dim 128): where these would
 // be more than one item and read the cache again. 3 sequences of up to 12,000 tokens, 32
-// heads on 8, this kernel and the wide one: 64 rows 48 and 50 us, 96 rows 71 and 51, 128
-// rows 74 and 53; 48 of up to 2,000: 64 rows 80 and 99, 96 rows 127 and 103.
+// heads on 8, this kernel and the wide one: 64 rows 48 and 51 us, 96 rows 71 and 52, 128
+// rows 74 and 54; 48 of up to 2,000: 64 rows 81 and 97, 96 rows 128 and 98.
 constexpr int WIDE_ROWS = 8 * MAX_NT + 1;
 
 // Tiles of 8 rows of an item: just enough for the window, at most MAX_NT, or those of

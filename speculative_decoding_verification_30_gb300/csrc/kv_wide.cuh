@@ -14,8 +14,8 @@
 // O stays in TMEM and is scaled there when a row's frame moves.
 // Measured: 3 sequences of up to 700 new tokens on up to 12,000 cached, 32 heads on 8: 240
 // us, 824 TFLOP/s. Bound by the chain of a tile, next logits, softmax, second product, of
-// which the softmax is the longest part: 2,100 of a unit's 4,600 clocks, 1,500 of them the
-// weights. Their exponentials need a third of that (32 a clock on an SM, measured); the rest is
+// which the softmax is the longest part: 2,100 clocks a unit (of 4,400, taken before keys were
+// widened), 1,500 of them the weights. Their exponentials need a third of that (32 a clock on an SM, measured); the rest is
 // the latency of loading, waiting for and computing a row's quarters in turn. Tried, when the
 // products ran on the codes themselves with a query as the sum of two e4m3 numbers (228 us, but
 // elements below 2^-9 of a row's largest lost bits: logits 1e-2 off beside a channel 300 times
