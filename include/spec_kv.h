@@ -114,6 +114,33 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
                             float scale, int window, void* out, float* lse, void* workspace,
                             size_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace that spec_kv_attention_shared needs for these arguments on the
+ * current device (as spec_kv_attention_workspace_bytes). */
+size_t spec_kv_attention_shared_workspace_bytes(int B, int groups, int N, int max_tokens, int q_heads, int kv_heads,
+                                                int head_dim);
+
+/* spec_kv_attention (without a sliding window) for a batch whose sequences have leading pages in
+ * common: samples of one prompt, requests behind one system prompt. The shared pages are read
+ * once for all rows of a group instead of once for each sequence; outputs are as spec_kv_attention's
+ * but for the rounding of sums.
+ *   cu_groups  [groups+1] int32, ascending from 0 to B: group g is the sequences cu_groups[g] ..
+ *              cu_groups[g+1] - 1
+ *   shared_len [groups] int32: the page table's rows of the group's sequences name pages of the
+ *              same contents for the positions below shared_len[g] (the same pages, as a rule);
+ *              0: none. seq_len counts these tokens, and every sequence's row of page_table has
+ *              its entries for them.
+ * Whole units of 128 positions below shared_len[g] and below seq_len of every sequence of the
+ * group that has new tokens are read through the first such sequence's row of the table, the rest
+ * through each sequence's own. A negative seq_len marks an empty place, as in spec_kv_attention; it
+ * limits nothing.
+ * Limits: 1 <= groups <= B; other arguments, limits, outputs and statuses as in spec_kv_attention. */
+sv_status spec_kv_attention_shared(const void* q, long long q_stride, const void* k_codes, const float* k_scale,
+                                   const void* v_codes, const float* v_scale, const int32_t* seq_len,
+                                   const int32_t* cu_tokens, const int32_t* page_table, const int32_t* cu_groups,
+                                   const int32_t* shared_len, int B, int groups, int N, int max_tokens, int max_pages,
+                                   int num_pages, int page_size, int q_heads, int kv_heads, int head_dim, float scale,
+                                   void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

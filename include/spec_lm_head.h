@@ -107,6 +107,25 @@ sv_status spec_verify_greedy_from_hidden(const void* hidden_target, const void* 
                                          int32_t* out_tokens, int32_t* out_n_accepted, void* workspace,
                                          size_t workspace_bytes, void* stream);
 
+/* logits[M][N] = hidden[M][d] . w[N][d]^T with a head held in 4 bits: w[v][j] =
+ * scale[v][j / group] * code[v][j] + bias[v][j / group], code 0..15. For a few rows (a
+ * drafted token, a verify window), which are bound by the head's bytes.
+ *   hidden  [M][d] bf16, row-major, device, 16-byte aligned
+ *   codes   [N][d / 2] uint8, device, 16-byte aligned: element j of a row in the low (j even)
+ *           or high (j odd) half of byte j / 2
+ *   scale, bias  [N][d / group] bf16, device, 4-byte aligned
+ *   logits  [M][N] fp32, row-major, device, caller-owned, 4-byte aligned
+ * Limits: 1 <= M <= 65536 (the head is read again for every 64 rows), 1 <= N <= 16,776,960,
+ * d a positive multiple of 64 and at most 65,536, group 32, 64 or 128 and a divisor of d.
+ * Codes minus 8 and their products with hidden are exact; sums are fp32: with X the sum of
+ * hidden over a group, a group adds scale * sum (code - 8) hidden + (bias + 8 scale) X.
+ * Repeated calls give the same bits. Non-finite hidden states, scales and biases give
+ * non-finite logits in their rows and columns.
+ * Returns SV_ERR_NULL, SV_ERR_SHAPE or SV_ERR_ALIGN before launching; SV_ERR_CUDA when the
+ * launch fails. */
+sv_status spec_lm_head_logits_q4(const void* hidden, const uint8_t* codes, const void* scale, const void* bias, int M,
+                                 int N, int d, int group, float* logits, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

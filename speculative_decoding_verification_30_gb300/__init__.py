@@ -20,7 +20,9 @@ __all__ = ["load", "spec_verify", "spec_verify_noalloc", "spec_verify_workspace_
            "spec_sample", "spec_philox_uniforms", "spec_lm_head_logits", "spec_verify_from_hidden",
            "spec_verify_greedy_from_hidden", "spec_token_logprobs", "spec_token_logprobs_backward",
            "TokenLogprobs", "KVCache", "rope_tables", "spec_kv_append",
-           "spec_kv_attention", "spec_kv_attention_workspace_bytes", "sv_version", "Workspace", "SV_BF16", "SV_F32", "SpecVerifyError"]
+           "spec_kv_attention", "spec_kv_attention_workspace_bytes", "spec_kv_attention_shared",
+           "spec_kv_attention_shared_workspace_bytes", "spec_prompt_attention", "spec_prompt_attention_backward",
+           "spec_prompt_attention_backward_workspace_bytes", "Q4Weight", "spec_lm_head_logits_q4", "sv_version", "Workspace", "SV_BF16", "SV_F32", "SpecVerifyError"]
 
 SV_BF16, SV_F32 = 0, 1
 _STATUS = {0: "ok", 1: "null pointer", 2: "shape", 3: "dtype", 4: "workspace", 5: "cuda",
@@ -82,6 +84,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.spec_kv_attention_workspace_bytes.restype = sz
     lib.spec_kv_attention.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, *[i32] * 9, f32, i32, vp, vp, vp, sz, vp]
     lib.spec_kv_attention.restype = i32
+    lib.spec_kv_attention_shared_workspace_bytes.argtypes = [i32] * 7
+    lib.spec_kv_attention_shared_workspace_bytes.restype = sz
+    lib.spec_kv_attention_shared.argtypes = [vp, i64, *[vp] * 9, *[i32] * 10, f32, vp, vp, vp, sz, vp]
+    lib.spec_kv_attention_shared.restype = i32
+    lib.spec_prompt_attention.argtypes = [vp, i64, vp, i64, vp, i64, vp, *[i32] * 5, f32, i32, vp, vp, vp]
+    lib.spec_prompt_attention.restype = i32
+    lib.spec_prompt_attention_backward_workspace_bytes.argtypes = [i32, i32]
+    lib.spec_prompt_attention_backward_workspace_bytes.restype = sz
+    lib.spec_prompt_attention_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, *[i32] * 5, f32, i32,
+                                                   vp, vp, vp, vp, sz, vp]
+    lib.spec_prompt_attention_backward.restype = i32
+    lib.spec_lm_head_logits_q4.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.spec_lm_head_logits_q4.restype = i32
     lib.sv_status_string.argtypes = [i32]
     lib.sv_status_string.restype = ctypes.c_char_p
     lib.sv_version.argtypes = []
@@ -376,5 +391,9 @@ def spec_verify_greedy_from_hidden(hidden_target: torch.Tensor, weight: torch.Te
 
 
 from .kv import (KVCache, rope_tables, spec_kv_append, spec_kv_attention,  # noqa: E402
+                 spec_kv_attention_shared, spec_kv_attention_shared_workspace_bytes,
                  spec_kv_attention_workspace_bytes)
 from .logprobs import TokenLogprobs, spec_token_logprobs, spec_token_logprobs_backward  # noqa: E402
+from .prompt import (spec_prompt_attention, spec_prompt_attention_backward,  # noqa: E402
+                     spec_prompt_attention_backward_workspace_bytes)
+from .q4 import Q4Weight, spec_lm_head_logits_q4  # noqa: E402

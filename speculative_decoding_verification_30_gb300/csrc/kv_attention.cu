@@ -1185,3 +1185,24 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
   if (nt == wide::NT) return launch_wide(A, st);
   return head_dim == 128 ? pick_attention<128>(nt, A, st) : pick_attention<64>(nt, A, st);
 }
+
+size_t spec_kv_attention_shared_workspace_bytes(int B, int groups, int N, int max_tokens, int q_heads, int kv_heads,
+                                                int head_dim) {
+  if (groups < 1 || groups > B || N < 1 || N > (1 << 24)) return 0;
+  return spec_kv_attention_workspace_bytes(B, max_tokens, q_heads, kv_heads, head_dim);
+}
+
+sv_status spec_kv_attention_shared(const void* q, long long q_stride, const void* k_codes, const float* k_scale,
+                                   const void* v_codes, const float* v_scale, const int32_t* seq_len,
+                                   const int32_t* cu_tokens, const int32_t* page_table, const int32_t* cu_groups,
+                                   const int32_t* shared_len, int B, int groups, int N, int max_tokens, int max_pages,
+                                   int num_pages, int page_size, int q_heads, int kv_heads, int head_dim, float scale,
+                                   void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!cu_groups || !shared_len) return SV_ERR_NULL;
+  if (groups < 1 || groups > B) return SV_ERR_SHAPE;
+  if (!svkv::aligned(cu_groups, 4) || !svkv::aligned(shared_len, 4)) return SV_ERR_ALIGN;
+  // first form: every sequence reads its own row of the table
+  return spec_kv_attention(q, q_stride, k_codes, k_scale, v_codes, v_scale, seq_len, cu_tokens, page_table, B, N, max_tokens,
+                           max_pages, num_pages, page_size, q_heads, kv_heads, head_dim, scale, 0, out, lse, workspace,
+                           workspace_bytes, stream);
+}

@@ -225,3 +225,71 @@ def spec_kv_attention(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_to
     if given:
         wrote(*given)
     return no_gradient("spec_kv_attention", (out, lse), q) if q.requires_grad else (out, lse)
+
+
+def spec_kv_attention_shared_workspace_bytes(B: int, groups: int, N: int, max_tokens: int, q_heads: int, kv_heads: int,
+                                             head_dim: int) -> int:
+    """Bytes of workspace of spec_kv_attention_shared on the current device; 0 for arguments outside its limits."""
+    if not all(0 <= x < _I32 for x in (B, groups, N, max_tokens, q_heads, kv_heads, head_dim)):
+        return 0
+    return int(load().spec_kv_attention_shared_workspace_bytes(B, groups, N, max_tokens, q_heads, kv_heads, head_dim))
+
+
+def spec_kv_attention_shared(q: torch.Tensor, kv: KVCache, seq_len: torch.Tensor, cu_tokens: torch.Tensor,
+                             page_table: torch.Tensor, max_tokens: int, cu_groups: torch.Tensor,
+                             shared_len: torch.Tensor, scale: float | None = None, out: torch.Tensor | None = None,
+                             lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """spec_kv_attention for a batch whose sequences have leading pages in common (samples of one
+    prompt, requests behind one system prompt): group g is the sequences cu_groups[g] ..
+    cu_groups[g + 1] - 1 (cu_groups [G + 1] int32, from 0 to B), whose rows of page_table name the same
+    pages for the positions below shared_len[g] (shared_len [G] int32). These are read once for all
+    rows of the group. seq_len and page_table are those of spec_kv_attention: they count and name
+    the shared tokens too. Returns (out [N, q_heads, head_dim] bf16, lse [N, q_heads] float32).
+
+    The call serves: a backward pass through its outputs raises. workspace: uint8, at least
+    spec_kv_attention_shared_workspace_bytes(...) bytes, not shared by calls that may overlap."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise SpecVerifyError("q must be a CUDA tensor")
+    no_tangent("spec_kv_attention_shared", q)
+    dev = q.device
+    cache, (pages, heads, page, dim) = _cache(kv, dev)
+    win, B, max_pages = _window(seq_len, cu_tokens, page_table, dev)
+    groups = (_shape(shared_len) or (0,))[0]
+    if _shape(shared_len) != (groups,) or groups < 1 or _shape(cu_groups) != (groups + 1,):
+        raise SpecVerifyError("shared_len must be [G] and cu_groups [G + 1]")
+    gp, sp = ptr(cu_groups, "cu_groups", torch.int32, dev), ptr(shared_len, "shared_len", torch.int32, dev)
+    qp, qs, N, qh = _heads(q, "q", torch.bfloat16, dev, dim)
+    _whole(max_tokens, "max_tokens", 1, N)
+    if scale is None:
+        scale = dim ** -0.5
+    lib = load()
+    with on_device(dev, stream, q, *kv, seq_len, cu_tokens, page_table, cu_groups, shared_len, out, lse, workspace) as st:
+        given = [t for t in (out, lse) if t is not None]
+        if workspace is None:
+            size = lib.spec_kv_attention_shared_workspace_bytes(B, groups, N, max_tokens, qh, heads, dim) or 16
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            wp = workspace.data_ptr()
+        else:
+            wp = ptr(workspace, "workspace", torch.uint8, dev)
+            size = workspace.numel()
+        if out is None:
+            out = torch.empty((N, qh, dim), dtype=torch.bfloat16, device=dev)
+            op = out.data_ptr()
+        elif _shape(out) != (N, qh, dim):
+            raise SpecVerifyError("out must be [N, q_heads, head_dim]")
+        else:
+            op = ptr(out, "out", torch.bfloat16, dev)
+        if lse is None:
+            lse = torch.empty((N, qh), dtype=torch.float32, device=dev)
+            lp = lse.data_ptr()
+        elif _shape(lse) != (N, qh):
+            raise SpecVerifyError("lse must be [N, q_heads]")
+        else:
+            lp = ptr(lse, "lse", torch.float32, dev)
+        rc = lib.spec_kv_attention_shared(qp, qs, *cache, *win, gp, sp, B, groups, N, max_tokens, max_pages, pages, page, qh,
+                                          heads, dim, scale, op, lp, wp, size, st)
+    if rc:
+        _check(rc, "spec_kv_attention_shared")
+    if given:
+        wrote(*given)
+    return no_gradient("spec_kv_attention_shared", (out, lse), q) if q.requires_grad else (out, lse)
