@@ -11,11 +11,12 @@ LIB = os.path.join(HERE, "libspec_verify.so")
 SOURCES = [os.path.join(CSRC, "spec_verify.cu"), os.path.join(CSRC, "spec_verify_noalloc.cu"),
            os.path.join(CSRC, "telemetry.cu"), os.path.join(CSRC, "lm_head.cu"),
            os.path.join(CSRC, "logprobs.cu"), os.path.join(CSRC, "kv_append.cu"),
-           os.path.join(CSRC, "kv_attention.cu"), os.path.join(CSRC, "prompt.cu"),
+           os.path.join(CSRC, "kv_attention.cu"), os.path.join(CSRC, "prompt_forward.cu"),
+           os.path.join(CSRC, "prompt_backward.cu"),
            os.path.join(CSRC, "lm_head_q4.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "sv_device.cuh"), os.path.join(CSRC, "keyhist.cuh"),
                   os.path.join(CSRC, "launch_cache.h"), os.path.join(CSRC, "kv_common.cuh"),
-                  os.path.join(CSRC, "kv_wide.cuh"),
+                  os.path.join(CSRC, "kv_wide.cuh"), os.path.join(CSRC, "prompt_common.cuh"),
                   os.path.join(os.path.dirname(HERE), "include", "spec_kv.h"), os.path.join(CSRC, "fstream.cuh"),
                   os.path.join(os.path.dirname(HERE), "include", "spec_verify.h"),
                   os.path.join(os.path.dirname(HERE), "include", "spec_lm_head.h"),

@@ -1,12 +1,7 @@
-// Causal attention over packed prompts and its gradient (C ABI and definitions in
+// The gradient of causal attention over packed prompts (C ABI and definitions in
 // include/spec_prompt.h). First form: a warp to each row, its head's elements spread over
-// the lanes; running maximum and sum.
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-#include <math.h>
-#include <stdint.h>
-
-#include "../../include/spec_prompt.h"
+// the lanes.
+#include "prompt_common.cuh"
 
 namespace svpr {
 
@@ -50,38 +45,6 @@ __device__ __forceinline__ float dot(const float (&x)[E], const float (&y)[E]) {
 #pragma unroll
   for (int e = 0; e < E; ++e) s = fmaf(x[e], y[e], s);
   return all_sum(s);
-}
-
-template <int D>
-__global__ void forward_kernel(const Args A) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (w >= (long long)A.N * A.qh) return;
-  const int r = (int)(w / A.qh), h = (int)(w % A.qh), kv = h / A.group;
-  int first, end;
-  rows_of(A, r, first, end);
-  const int lo = A.window ? max(first, r - A.window + 1) : first;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-  load(q, A.q + (size_t)r * A.qs + (size_t)h * D, lane);
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  if (first < end)
-    for (int j = lo; j <= r; ++j) {
-      float k[E], v[E];
-      load(k, A.k + (size_t)j * A.ks + (size_t)kv * D, lane);
-      load(v, A.v + (size_t)j * A.vs + (size_t)kv * D, lane);
-      const float a = dot(q, k) * A.scale, m2 = fmaxf(m, a);
-      if (m2 == -INFINITY && a == a) continue;   // NaN stays
-      const float f = expf(m - m2), p = expf(a - m2);
-      m = m2;
-      l = fmaf(l, f, p);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(p, v[e], o[e] * f);
-    }
-#pragma unroll
-  for (int e = 0; e < E; ++e) A.out[(size_t)w * D + lane * E + e] = __float2bfloat16_rn(l == 0.f ? 0.f : o[e] / l);
-  if (A.lse && lane == 0) A.lse[w] = m + logf(l);
 }
 
 template <int D>
@@ -150,14 +113,6 @@ __global__ void grad_kv_kernel(const Args A) {
   }
 }
 
-static bool bad_shape(int B, int N, int qh, int kh, int D, float scale, int window) {
-  return B < 1 || B > 65535 || N < 1 || N > (1 << 24) || kh < 1 || kh > 256 || qh < kh || qh % kh || qh / kh > 64 ||
-         (D != 64 && D != 128) || !isfinite(scale) || scale < 0.f || window < 0;
-}
-static bool bad_stride(long long s, int heads, int D) { return s < (long long)heads * D || s >= (1ll << 30); }
-static bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-static bool rows_aligned(const void* p, long long s) { return aligned(p, 16) && (s * 2) % 16 == 0; }
-
 template <int D>
 static sv_status backward(const Args& A, cudaStream_t st) {
   const unsigned nq = (unsigned)(((long long)A.N * A.qh + 3) / 4), nk = (unsigned)(((long long)A.N * A.kh + 3) / 4);
@@ -168,33 +123,6 @@ static sv_status backward(const Args& A, cudaStream_t st) {
 }
 
 }  // namespace svpr
-
-sv_status spec_prompt_attention(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
-                                long long v_stride, const int32_t* cu_tokens, int B, int N, int q_heads, int kv_heads,
-                                int head_dim, float scale, int window, void* out, float* lse, void* stream) {
-  using namespace svpr;
-  if (!q || !k || !v || !cu_tokens || !out) return SV_ERR_NULL;
-  if (bad_shape(B, N, q_heads, kv_heads, head_dim, scale, window) || bad_stride(q_stride, q_heads, head_dim) ||
-      bad_stride(k_stride, kv_heads, head_dim) || bad_stride(v_stride, kv_heads, head_dim))
-    return SV_ERR_SHAPE;
-  if (!rows_aligned(q, q_stride) || !rows_aligned(k, k_stride) || !rows_aligned(v, v_stride) || !aligned(out, 16) ||
-      !aligned(lse, 4) || !aligned(cu_tokens, 4))
-    return SV_ERR_ALIGN;
-  Args A = {};
-  A.q = static_cast<const __nv_bfloat16*>(q), A.k = static_cast<const __nv_bfloat16*>(k);
-  A.v = static_cast<const __nv_bfloat16*>(v);
-  A.qs = q_stride, A.ks = k_stride, A.vs = v_stride;
-  A.cu = cu_tokens;
-  A.B = B, A.N = N, A.qh = q_heads, A.kh = kv_heads, A.group = q_heads / kv_heads, A.window = window;
-  A.scale = scale;
-  A.out = static_cast<__nv_bfloat16*>(out);
-  A.lse = lse;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned n = (unsigned)(((long long)N * q_heads + 3) / 4);
-  if (head_dim == 128) forward_kernel<128><<<n, 128, 0, st>>>(A);
-  else forward_kernel<64><<<n, 128, 0, st>>>(A);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
-}
 
 size_t spec_prompt_attention_backward_workspace_bytes(int N, int q_heads) {
   if (N < 1 || N > (1 << 24) || q_heads < 1 || q_heads > 64 * 256) return 0;
