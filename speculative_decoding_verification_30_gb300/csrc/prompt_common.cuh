@@ -46,13 +46,13 @@ __device__ __forceinline__ Seq sequence(const Prompts& p, int b) {
   return s;
 }
 
-// The walk over pieces of work: `span` rows of a sequence for one of `slots` head slots. Blocks
-// take them from the last rows of the prompts to the first, so that pieces with the most keys
-// come first (`up`: from the first to the last, for work over the rows behind), in turn and
-// in alternating order: the sums of their lengths are nearly even without a queue. A warp
-// walks together.
+// The walk over pieces of work: `span` rows of a sequence for one of `slots` head slots. A piece
+// at level x is the one with x spans before it (`up`: behind it), whose keys (queries) it
+// goes over. Blocks take the pieces from the highest level to the lowest, in turn and in
+// alternating order: the longest come first and the sums of their lengths are nearly even,
+// without a queue. A warp walks together.
 struct Walk {
-  int level, levels, b0, span, slots, up;
+  int level, b0, span, slots, up;
   long long before;   // pieces before sequence b0 of this level
 };
 __device__ __forceinline__ Walk walk_start(const Prompts& p, int span, int slots, int up, int lane) {
@@ -60,13 +60,12 @@ __device__ __forceinline__ Walk walk_start(const Prompts& p, int span, int slots
   for (int b = lane; b < p.B; b += 32) most = max(most, sequence(p, b).len);
 #pragma unroll
   for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-  const int levels = (most + span - 1) / span;
-  return Walk{0, levels, 0, span, slots, up, 0};
+  return Walk{(most + span - 1) / span - 1, 0, span, slots, up, 0};
 }
 // Piece n (not below the last one asked for): sequence, its first row's token and the head slot.
 __device__ __forceinline__ bool walk_to(const Prompts& p, Walk& w, long long n, int lane, Seq& s, int& token, int& slot) {
-  while (w.level < w.levels) {
-    const int at = (w.up ? w.level : w.levels - 1 - w.level) * w.span;
+  while (w.level >= 0) {
+    const int at = w.level * w.span;
     const int b = w.b0 + lane;
     const Seq mine = b < p.B ? sequence(p, b) : Seq{0, 0};
     const unsigned has = __ballot_sync(0xffffffffu, mine.len > at);
@@ -75,7 +74,7 @@ __device__ __forceinline__ bool walk_to(const Prompts& p, Walk& w, long long n, 
       const int x = (int)(n - w.before), r = x / w.slots, from = __fns(has, 0, r + 1);
       s.first = __shfl_sync(0xffffffffu, mine.first, from);
       s.len = __shfl_sync(0xffffffffu, mine.len, from);
-      token = at;
+      token = w.up ? (s.len - 1) / w.span * w.span - at : at;
       slot = x - r * w.slots;
       return true;
     }
@@ -83,7 +82,7 @@ __device__ __forceinline__ bool walk_to(const Prompts& p, Walk& w, long long n, 
     w.b0 += 32;
     if (w.b0 >= p.B) {
       w.b0 = 0;
-      ++w.level;
+      --w.level;
     }
   }
   return false;
@@ -195,12 +194,14 @@ __device__ __forceinline__ void mma_dims(uint32_t d, const unsigned char* a, con
       mma_ss(d, a0 + at, b0 + at, idesc(BLK), c | k);
     }
 }
-// d [128][D] (+)= a b over the rows of the tile b; a: bf16 in TMEM.
+// d [128][D] (+)= a b over the rows of the tile b; a: bf16 in TMEM, its second half `gap` columns
+// further than behind the first.
 template <int D>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, const unsigned char* b, bool add) {
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, const unsigned char* b, bool add, int gap = 0) {
   const uint64_t b0 = desc(smem_u32(b), COL);
 #pragma unroll
-  for (int k = 0; k < BLK / 16; ++k) mma_ts(d, a + 8 * k, b0 + 16 * 128 * k / 16, idesc(D) | FLIP, (uint32_t)(k != 0 || add));
+  for (int k = 0; k < BLK / 16; ++k)
+    mma_ts(d, a + 8 * k + (k < 4 ? 0 : gap), b0 + 16 * 128 * k / 16, idesc(D) | FLIP, (uint32_t)(k != 0 || add));
 }
 
 // 32 columns of TMEM, a row to a lane; not waited for.
