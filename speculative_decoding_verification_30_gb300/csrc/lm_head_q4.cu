@@ -1,35 +1,351 @@
 // LM-head logits with weights in 4 bits and group scales (C ABI and definitions in
-// include/spec_lm_head.h). First form: a warp to each vocabulary entry and row.
+// include/spec_lm_head.h).
+//
+// For a few rows the bound is the head's bytes, d / 2 and 4 d / group for each vocabulary
+// entry. Vocabulary rows are the 16-row side of the matrix instruction, hidden states its
+// 8-column side. The contraction may take its index in any order, so a lane keeps the 16
+// neighbouring codes that one 8-byte load of a row brings (64 elements of a row for the
+// four lanes that share it) and the hidden states are laid out to match, once, in shared memory. A
+// code becomes bf16 by way of 128 + code, whose low bits are the code; less 136 that is exact. The
+// products of a group are summed by themselves, then scaled:
+//   logit += scale * sum (code - 8) h + (bias + 8 scale) * sum h.
+// Each warp streams its rows with the codes of the next 256 elements on their way in registers. Where a
+// device's warps would not get whole numbers of tiles, warps share a tile along d.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "../../include/spec_lm_head.h"
+#include "launch_cache.h"
 
 namespace svq4 {
 
-__global__ void q4_kernel(const __nv_bfloat16* hidden, const uint8_t* codes, const __nv_bfloat16* scale,
-                          const __nv_bfloat16* bias, int M, int N, int d, int group, float* logits) {
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (w >= (long long)M * N) return;
-  const int m = (int)(w / N), v = (int)(w % N), per = d / group;
-  float sum = 0.f;
-  for (int g = 0; g < per; ++g) {
-    float a = 0.f, x = 0.f;
-    for (int j = 2 * lane; j < group; j += 64) {
-      const uint8_t c = codes[(size_t)v * (d / 2) + (g * group + j) / 2];
-      const __nv_bfloat16* h = hidden + (size_t)m * d + g * group + j;
-      const float h0 = __bfloat162float(h[0]), h1 = __bfloat162float(h[1]);
-      a = fmaf((float)((c & 15) - 8), h0, fmaf((float)((c >> 4) - 8), h1, a));
-      x += h0 + h1;
-    }
-    const float s = __bfloat162float(scale[(size_t)v * per + g]), b = __bfloat162float(bias[(size_t)v * per + g]);
-    sum = fmaf(s, a, fmaf(fmaf(8.f, s, b), x, sum));
-  }
+constexpr int WARPS = 16, THREADS = 32 * WARPS;
+constexpr int STEP = 64, SUPER = 4;      // elements of a step; steps of what is on its way
+constexpr int SMEM_MAX = 220 * 1024;
+
+struct Args {
+  const __nv_bfloat16* hidden;
+  const uint8_t* codes;
+  const unsigned short *scale, *bias;
+  float* logits;
+  int M, N, d;
+  int supers;          // of a row
+  int chunk;           // supers of hidden states in shared memory at a time
+  int split;           // warps of a tile
+};
+
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint32_t* b, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(b[0]), "r"(a[1]), "r"(b[1]), "r"(b0), "r"(b1));
+}
+// Eight codes less 8 as bf16, in the order 0 4, 1 5, 2 6, 3 7.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t (&x)[4]) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) logits[w] = sum;
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t t = ((w >> (4 * k)) & 0x000F000Fu) | 0x43004300u;   // 128 + code
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(x[k]) : "r"(t), "r"(0x43084308u));
+  }
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float widen1(unsigned short x) { return __uint_as_float((uint32_t)x << 16); }
+
+// First element of the eight of (step, word) that lane q of four has.
+template <int G>
+__device__ __forceinline__ int element(int step, int word, int q) {
+  return STEP * step + (G == 32 ? 32 * word + 8 * q : 16 * q + 8 * word);
+}
+
+// Hidden states of supers c0 .. c1 - 1, as the products want them: [column tile][step][word][lane] of
+// eight elements; and the sums of each group [group][column].
+template <int G, int NT>
+__device__ __forceinline__ void lay_out(const Args& A, int m0, int c0, int c1, uint4* sh, float* sx) {
+  const int s0 = c0 * SUPER, steps = (c1 - c0) * SUPER;
+  for (int x = threadIdx.x; x < NT * steps * 64; x += THREADS) {
+    const int lane = x & 31, word = x >> 5 & 1, st = x / 64 % steps, nt = x / 64 / steps;
+    const int m = m0 + 8 * nt + (lane >> 2), k = element<G>(s0 + st, word, lane & 3);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (m < A.M && k < A.d) v = *reinterpret_cast<const uint4*>(A.hidden + (size_t)m * A.d + k);
+    // pairs 01, 23, 45, 67 to 04, 15, 26, 37
+    sh[x] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                       __byte_perm(v.y, v.w, 0x7632));
+  }
+  const int g0 = s0 * STEP / G, groups = steps * STEP / G;
+  for (int x = threadIdx.x; x < 8 * NT * groups; x += THREADS) {
+    const int m = m0 + x % (8 * NT), g = g0 + x / (8 * NT);
+    float sum = 0.f;
+    if (m < A.M && g * G < A.d) {
+      const uint4* p = reinterpret_cast<const uint4*>(A.hidden + (size_t)m * A.d + g * G);
+#pragma unroll
+      for (int i = 0; i < G / 8; ++i) {
+        const uint4 v = p[i];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+    }
+    sx[x] = sum;
+  }
+}
+
+// G: group; NT: column tiles of 8 rows; R: tiles of 16 vocabulary rows of a warp
+template <int G, int NT, int R>
+__global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
+  constexpr int PER = SUPER * STEP / G;            // groups of a super: 8, 4 or 2
+  constexpr int OWN = PER > 4 ? 2 : 1;             // of which a lane looks up so many
+  extern __shared__ uint4 smem[];
+  uint4* sh = smem;
+  float* sx = reinterpret_cast<float*>(sh + (size_t)NT * A.chunk * SUPER * 64);
+  float* red = sx + (size_t)8 * NT * A.chunk * PER;   // [warp][R NT 4][lane]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int m0 = blockIdx.y * 8 * NT, half = A.d / 2, per = A.d / G, steps = A.d / STEP;
+  const int slots = WARPS / A.split, slot = warp % slots, part = warp / slots;
+  const int tiles = (A.N + 16 * R - 1) / (16 * R), turns = (tiles + (int)gridDim.x * slots - 1) / ((int)gridDim.x * slots);
+  const int chunks = (A.supers + A.chunk - 1) / A.chunk;
+  // the supers of chunk c that are this warp's
+  const auto from = [&](int c) { return c * A.chunk + (min(A.chunk, A.supers - c * A.chunk) * part) / A.split; };
+  const auto to = [&](int c) { return c * A.chunk + (min(A.chunk, A.supers - c * A.chunk) * (part + 1)) / A.split; };
+  const auto tile_of = [&](int turn) { return (turn * slots + slot) * (int)gridDim.x + (int)blockIdx.x; };
+
+  // What is on its way: super `ls` of tile number `lt`
+  uint2 code[SUPER][2 * R];
+  unsigned short sc[2 * R][OWN], bi[2 * R][OWN];
+  int lt = 0, lc = 0, ls = from(0);
+  int row[2 * R];
+  bool on = false;
+  const auto settle = [&]() {   // on the next super that there is
+    while (lt < turns && ls >= to(lc)) {
+      if (++lc == chunks) lc = 0, ++lt;
+      if (lt < turns) ls = from(lc);
+    }
+    on = lt < turns && tile_of(lt) < tiles;
+  };
+  const auto rows = [&]() {
+#pragma unroll
+    for (int j = 0; j < 2 * R; ++j)
+      row[j] = min(tile_of(min(lt, turns - 1)) * 16 * R + 8 * j + g, A.N - 1);
+  };
+  const auto load_codes = [&](int i) {
+    const int s = ls * SUPER + i;
+#pragma unroll
+    for (int j = 0; j < 2 * R; ++j) {
+      if (!on || s >= steps) continue;
+      const uint8_t* p = A.codes + (size_t)row[j] * half + s * (STEP / 2);
+      if (G == 32)
+        code[i][j] = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(p + 4 * q)), __ldg(reinterpret_cast<const uint32_t*>(p + 16 + 4 * q)));
+      else
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(code[i][j].x), "=r"(code[i][j].y) : "l"(p + 8 * q));
+    }
+  };
+  const auto load_scales = [&]() {
+#pragma unroll
+    for (int j = 0; j < 2 * R; ++j)
+#pragma unroll
+      for (int o = 0; o < OWN; ++o) {
+        const int x = ls * PER + q * OWN + o;
+        if (!on || q * OWN >= PER || x >= per) continue;
+        const size_t at = (size_t)row[j] * per + x;
+        sc[j][o] = __ldg(A.scale + at);
+        bi[j][o] = __ldg(A.bias + at);
+      }
+  };
+  settle();
+  rows();
+#pragma unroll
+  for (int i = 0; i < SUPER; ++i) load_codes(i);
+  load_scales();
+  if (chunks == 1) {
+    lay_out<G, NT>(A, m0, 0, A.supers, sh, sx);
+    __syncthreads();
+  }
+
+  for (int turn = 0; turn < turns; ++turn) {
+    const int tile = tile_of(turn);
+    uint64_t out[R][NT][2];
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) out[t][n][0] = out[t][n][1] = 0ull;
+    for (int c = 0; c < chunks; ++c) {
+      if (chunks > 1) {
+        __syncthreads();
+        lay_out<G, NT>(A, m0, c * A.chunk, min((c + 1) * A.chunk, A.supers), sh, sx);
+        __syncthreads();
+      }
+      if (tile >= tiles) continue;
+      const int held = min(A.chunk, A.supers - c * A.chunk) * SUPER;   // steps in shared memory
+#pragma unroll 1
+      for (int s = from(c); s < to(c); ++s) {
+        float fs[2 * R][OWN], ft[2 * R][OWN];
+#pragma unroll
+        for (int j = 0; j < 2 * R; ++j)
+#pragma unroll
+          for (int o = 0; o < OWN; ++o) {
+            fs[j][o] = widen1(sc[j][o]);
+            ft[j][o] = fmaf(8.f, fs[j][o], widen1(bi[j][o]));
+          }
+        // the next super begins to come while this one is worked on
+        ++ls;
+        settle();
+        if (ls != s + 1 || lt != turn) rows();
+        load_scales();
+        float acc[R][NT][4];
+#pragma unroll
+        for (int i = 0; i < SUPER; ++i) {
+          const int st = s * SUPER + i;
+          if (st < steps) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              if (G == 32 || (w == 0 && i * STEP % G == 0))
+#pragma unroll
+                for (int t = 0; t < R; ++t)
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) acc[t][n][0] = acc[t][n][1] = acc[t][n][2] = acc[t][n][3] = 0.f;
+              uint32_t x[2 * R][4];
+#pragma unroll
+              for (int j = 0; j < 2 * R; ++j) widen(w ? code[i][j].y : code[i][j].x, x[j]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint4 b = sh[((n * held + st - c * A.chunk * SUPER) * 2 + w) * 32 + lane];
+#pragma unroll
+                for (int t = 0; t < R; ++t) {
+                  mma16816(acc[t][n], x[2 * t], x[2 * t + 1], b.x, b.y);
+                  mma16816(acc[t][n], x[2 * t] + 2, x[2 * t + 1] + 2, b.z, b.w);
+                }
+              }
+              if (G == 32 || (w == 1 && (i + 1) * STEP % G == 0)) {
+                const int gi = (i * STEP + 32 * w) / G, own = OWN == 2 ? gi >> 1 : gi;   // of the super; its lane
+                float s2[2 * R], t2[2 * R];
+#pragma unroll
+                for (int j = 0; j < 2 * R; ++j) {
+                  s2[j] = __shfl_sync(0xffffffffu, fs[j][gi & (OWN - 1)], (lane & ~3) | own);
+                  t2[j] = __shfl_sync(0xffffffffu, ft[j][gi & (OWN - 1)], (lane & ~3) | own);
+                }
+                const float* px = sx + ((s - c * A.chunk) * PER + gi) * 8 * NT + 2 * q;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  const uint64_t xs = *reinterpret_cast<const uint64_t*>(px + 8 * n);
+#pragma unroll
+                  for (int t = 0; t < R; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                      out[t][n][e] = fma2(pair(s2[2 * t + e], s2[2 * t + e]), pair(acc[t][n][2 * e], acc[t][n][2 * e + 1]),
+                                          fma2(pair(t2[2 * t + e], t2[2 * t + e]), xs, out[t][n][e]));
+                }
+              }
+            }
+          }
+          load_codes(i);
+        }
+      }
+    }
+    const auto value = [&](int t, int n, int e) {
+      float a, b;
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(out[t][n][e >> 1]));
+      return e & 1 ? b : a;
+    };
+    if (A.split > 1) {
+      // the parts of a tile, in their order
+      const int id = 1 + slot, threads = 32 * A.split;
+      asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");   // the last turn's are read
+      float* mine = red + (size_t)warp * (R * NT * 4 * 32) + lane;
+      if (part)
+#pragma unroll
+        for (int t = 0; t < R; ++t)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mine[((t * NT + n) * 4 + e) * 32] = value(t, n, e);
+      asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+      if (part) continue;
+    }
+    if (tile >= tiles) continue;
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = (tile * R + t) * 16 + g + 8 * (e >> 1), m = m0 + 8 * n + 2 * q + (e & 1);
+          float x = value(t, n, e);
+          for (int p = 1; p < A.split; ++p) x += red[(size_t)(warp + p * slots) * (R * NT * 4 * 32) + ((t * NT + n) * 4 + e) * 32 + lane];
+          if (v < A.N && m < A.M) A.logits[(size_t)m * A.N + v] = x;
+        }
+  }
+}
+
+static sv::LaunchCache g_cache;
+static int sm_count() try {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (g_cache.get(dev, reinterpret_cast<const void*>(&sm_count), 0, 0, &n, [&](int* v) {
+        return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
+      }) != cudaSuccess)
+    return 0;
+  return n;
+} catch (...) {   // no exception passes the C entry points
+  return 0;
+}
+// The kernel's shared-memory limit, raised once per device.
+static bool raise_smem(const void* fn) try {
+  int dev = 0, done = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && g_cache.get(dev, fn, SMEM_MAX, 0, &done, [&](int* v) {
+    *v = 1;
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MAX);
+  }) == cudaSuccess;
+} catch (...) {
+  return false;
+}
+
+template <int G, int NT>
+static sv_status launch(Args A, cudaStream_t st) {
+  constexpr int R = NT <= 2 ? 2 : 1;
+  const int sms = sm_count();
+  if (sms < 1 || !raise_smem(reinterpret_cast<const void*>(q4_kernel<G, NT, R>))) return SV_ERR_CUDA;
+  // warps of a tile: the fewest with which turns that are not full cost a tenth at most
+  const long long tiles = (A.N + 16 * R - 1) / (16 * R);
+  int split = 1;
+  double best = 1e9;
+  for (int s = 1; s <= 8; s *= 2) {
+    const double turns = (double)tiles * s / ((double)sms * WARPS), cost = ceil(turns) / turns;
+    if (cost < best - 0.05) best = cost, split = s;
+    if (best <= 1.1) break;
+  }
+  A.split = split;
+  A.supers = (A.d + SUPER * STEP - 1) / (SUPER * STEP);
+  const size_t each = (size_t)NT * SUPER * 64 * sizeof(uint4) + (size_t)8 * NT * (SUPER * STEP / G) * sizeof(float);
+  const size_t fixed = split > 1 ? (size_t)WARPS * R * NT * 4 * 32 * sizeof(float) : 0;
+  const size_t fit = (SMEM_MAX - fixed) / each;
+  A.chunk = (size_t)A.supers <= fit ? A.supers : (int)fit;
+  const long long blocks = (tiles * split + WARPS - 1) / WARPS;
+  const dim3 grid((unsigned)(blocks < sms ? blocks : sms), (unsigned)((A.M + 8 * NT - 1) / (8 * NT)));
+  q4_kernel<G, NT, R><<<grid, THREADS, A.chunk * each + fixed, st>>>(A);
+  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+template <int G>
+static sv_status pick(const Args& A, cudaStream_t st) {
+  switch (A.M >= 64 ? 8 : (A.M + 7) / 8) {
+    case 1: return launch<G, 1>(A, st);
+    case 2: return launch<G, 2>(A, st);
+    case 3: return launch<G, 3>(A, st);
+    case 4: return launch<G, 4>(A, st);
+    case 5: return launch<G, 5>(A, st);
+    case 6: return launch<G, 6>(A, st);
+    default: return launch<G, 8>(A, st);
+  }
 }
 
 static bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -45,10 +361,12 @@ sv_status spec_lm_head_logits_q4(const void* hidden, const uint8_t* codes, const
     return SV_ERR_SHAPE;
   if (!aligned(hidden, 16) || !aligned(codes, 16) || !aligned(scale, 4) || !aligned(bias, 4) || !aligned(logits, 4))
     return SV_ERR_ALIGN;
-  const long long blocks = ((long long)M * N + 3) / 4;
-  if (blocks > 2147483647ll) return SV_ERR_SHAPE;
-  q4_kernel<<<(unsigned)blocks, 128, 0, static_cast<cudaStream_t>(stream)>>>(
-      static_cast<const __nv_bfloat16*>(hidden), codes, static_cast<const __nv_bfloat16*>(scale),
-      static_cast<const __nv_bfloat16*>(bias), M, N, d, group, logits);
-  return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  Args A = {};
+  A.hidden = static_cast<const __nv_bfloat16*>(hidden);
+  A.codes = codes;
+  A.scale = static_cast<const unsigned short*>(scale), A.bias = static_cast<const unsigned short*>(bias);
+  A.logits = logits;
+  A.M = M, A.N = N, A.d = d;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return group == 32 ? pick<32>(A, st) : group == 64 ? pick<64>(A, st) : pick<128>(A, st);
 }
