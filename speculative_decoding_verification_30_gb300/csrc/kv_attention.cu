@@ -53,7 +53,12 @@ constexpr float LN2F = 0.693147180559945309f, LOG2EF = 1.44269504088896341f;
 
 struct Start {
   long long unit0;     // its first unit
-  int tiles, h, rt, row0, count, pad;
+  int tiles, h, rt, row0, count, add;
+};
+// The shared tokens of a group: `len` of them, in the row `lead` of the page table, seen by all
+// of the group's rows, new tokens first .. first + count - 1.
+struct Group {
+  int len, lead, first, count;
 };
 struct AttnArgs {
   Window w;
@@ -69,6 +74,12 @@ struct AttnArgs {
   Start* start;        // workspace: the item in which each block's share begins
   uint8_t* failed;     // workspace: whether a wait of each block ran out; every block writes its own
   float* part;         // workspace: 2 slots for each block
+  // Of spec_kv_attention_shared, else null. Its first pass goes over the shared tokens of
+  // each group for all of the group's rows: `groups` says which, the results are kept in
+  // fp32. The second pass goes over the rest of each sequence and adds those.
+  const Group* groups;   // first pass
+  const int32_t* skip;   // second pass: tokens of each sequence that the first has gone over
+  float *kept, *kept_lse;   // [N][q_heads][head_dim], [N][q_heads]: written by the first pass, read by the second
   int workers;
   int group;           // query heads of a kv head
   int group_mul;       // 2^16 / group, rounded up
@@ -77,7 +88,7 @@ struct AttnArgs {
 __device__ __forceinline__ int over_group(const AttnArgs& A, int x) { return x * A.group_mul >> 16; }
 
 constexpr long long FAR = 1ll << 30;   // past every position of a cache
-constexpr int FIRST = 1, LAST = 2, WHOLE = 4, MASKED = 8, END = 16;
+constexpr int FIRST = 1, LAST = 2, WHOLE = 4, MASKED = 8, END = 16, ADD = 32;   // ADD: to what the first pass kept
 constexpr int MAX_RUNS = 8;    // runs of 16 tokens in a unit
 struct Meta {                  // of a stage: a unit of item (b, h, rt)
   float4 run[MAX_RUNS];               // of each 16 tokens: key scale, log2 and reciprocal of the value scale
@@ -138,22 +149,34 @@ struct Shape {
 struct Span {
   int tile0, tiles, rts;
 };
+// Sequence b, or group b in the first pass over shared tokens.
+__device__ __forceinline__ Seq rows_of(const AttnArgs& A, int b) {
+  if (!A.groups) return sequence(A.w, b);
+  const Group g = A.groups[b];
+  return Seq{g.len, g.first, g.count, g.count};
+}
 template <int ROWS, int TOK>
-__device__ __forceinline__ Span span_of(const AttnArgs& A, const Seq& s) {
+__device__ __forceinline__ Span span_of(const AttnArgs& A, int b, const Seq& s) {
   Span p{0, 0, 0};
   if (s.count == 0) return p;
   const long long cap = (long long)A.w.max_pages * A.w.page_size;
-  const long long end = s.len < 0 ? 0 : min(s.len + s.count, cap);
+  const long long end = s.len < 0 ? 0 : min(s.len + (A.groups ? 0 : s.count), cap);
   long long lo = A.window && s.len >= 0 ? max(s.len - A.window + 1, 0ll) : 0ll;
+  if (A.skip) lo = max(A.skip[b], 0);
   lo = min(lo, end);
   p.tile0 = (int)(lo / TOK);
   p.tiles = max((int)((end + TOK - 1) / TOK) - p.tile0, 1);
   p.rts = (s.count * A.group + ROWS - 1) / ROWS;   // below 2^30
   return p;
 }
+__device__ __forceinline__ int table_row(const AttnArgs& A, int b) { return A.groups ? A.groups[b].lead : b; }
+// ADD where the first pass has gone over tokens of sequence b.
+__device__ __forceinline__ int added(const AttnArgs& A, int b, const Seq& s) {
+  return A.skip && s.len >= 0 && A.skip[b] > 0 ? ADD : 0;
+}
 template <int ROWS, int TOK>
 __device__ __forceinline__ long long units_of(const AttnArgs& A, int b) {
-  const Span p = span_of<ROWS, TOK>(A, sequence(A.w, b));
+  const Span p = span_of<ROWS, TOK>(A, b, rows_of(A, b));
   return (long long)A.w.kv_heads * p.rts * (p.tiles + OVERHEAD);
 }
 
@@ -263,6 +286,15 @@ __device__ __forceinline__ float ex2f(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// A row's sum l in the frame m and what the first pass kept for it, in one frame: factors of
+// the row's weighted values and of the kept ones, and their common sum in l, m.
+__device__ __forceinline__ void add_kept(float& m, float& l, float kept_lse, float& own, float& kept) {
+  const float k = kept_lse * LOG2EF, top = fmaxf(m, fmaxf(k, NO_FRAME));   // k: -inf where nothing was seen
+  own = ex2f(m - top);
+  kept = ex2f(k - top);
+  l = fmaf(l, own, kept);
+  m = top;
 }
 // Four e4m3 codes as two pairs of fp16 (exact).
 __device__ __forceinline__ void widen(uint32_t c, uint32_t& lo, uint32_t& hi) {
@@ -410,8 +442,9 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
     // --- the copying warp. Unit `cu` is number `ct` of item (cb, ch, cr)
     int cb = s_b;
     long long cu = u0;
-    Seq cs = sequence(w, cb);
-    Span cp = span_of<ROWS, TOK>(A, cs);
+    Seq cs = rows_of(A, cb);
+    Span cp = span_of<ROWS, TOK>(A, cb, cs);
+    int add = added(A, cb, cs);
     int ct, ch, cr;
     {
       const long long x = u0 - s_pre;
@@ -420,7 +453,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
       ct = (int)(x - item * per);
       ch = (int)quotient(item, cp.rts);
       cr = (int)(item - (long long)ch * cp.rts);
-      if (lane == 0) A.start[wk] = Start{u0 - ct, cp.tiles, ch, cr, cs.first, cs.count, 0};
+      if (lane == 0) A.start[wk] = Start{u0 - ct, cp.tiles, ch, cr, cs.first, cs.count, add};
     }
     // entries window0 .. window0 + 31 of the sequence's row of the page table and those
     // pages' scales, one in each lane
@@ -446,7 +479,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
           window_b = cb;
           window_h = -1;
           window0 = j0;
-          entry = page_of(w, cb, (long long)j0 + lane);
+          entry = page_of(w, table_row(A, cb), (long long)j0 + lane);
         }
         if (ch != window_h) {
           window_h = ch;
@@ -484,7 +517,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
           const bool masked = gap || cs.len < 0 || tok0 + TOK - 1 > cs.len ||
                               (A.window && tok0 <= cs.len + cs.count - 1 - A.window);
           M.flags = (ct == OVERHEAD || cu == u0 ? FIRST : 0) | (cu + 1 == item1 || cu + 1 == u1 ? LAST : 0) |
-                      (u0 <= item0 + OVERHEAD && u1 >= item1 ? WHOLE : 0) | (masked ? MASKED : 0);
+                      (u0 <= item0 + OVERHEAD && u1 >= item1 ? WHOLE : 0) | (masked ? MASKED : 0) | add;
           M.row0 = cs.first;
           M.count = cs.count;
           const long long hi = cs.len < 0 ? -FAR : cs.len - tok0;
@@ -505,8 +538,9 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
               ch = 0;
               if (cu < u1) {
                 do {
-                  cs = sequence(w, ++cb);
-                  cp = span_of<ROWS, TOK>(A, cs);
+                  cs = rows_of(A, ++cb);
+                  cp = span_of<ROWS, TOK>(A, cb, cs);
+                  add = added(A, cb, cs);
                 } while (cp.rts == 0 && cb + 1 < w.B);
               }
             }
@@ -853,7 +887,24 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
           const int d0 = (D / 4) * warp + (D / 32) * g;
           if (flags & WHOLE) {
             const size_t at = (size_t)(M.row0 + i) * w.q_heads + M.h * G + M.r0 + r - (i - M.i0) * G;
+            if (flags & ADD) {
+              float own, kept;
+              add_kept(m[n][e], sum, A.kept_lse[at], own, kept);
+#pragma unroll
+              for (int j = 0; j < DT; ++j) {
+                const float2 y = *reinterpret_cast<const float2*>(A.kept + at * D + d0 + 2 * j);
+                o[j][n][e] = fmaf(o[j][n][e], own, y.x * kept);
+                o[j][n][2 + e] = fmaf(o[j][n][2 + e], own, y.y * kept);
+              }
+            }
             const float f = sum == 0.f ? 0.f : 1.f / sum;
+            if (A.groups) {
+#pragma unroll
+              for (int j = 0; j < DT; ++j)
+                *reinterpret_cast<float2*>(A.kept + at * D + d0 + 2 * j) = make_float2(o[j][n][e] * f, o[j][n][2 + e] * f);
+              if (warp == 0 && g == 0) A.kept_lse[at] = LN2F * (m[n][e] + log2f(sum));
+              continue;
+            }
             uint32_t y[DT];
 #pragma unroll
             for (int j = 0; j < DT; ++j) {
@@ -914,6 +965,11 @@ __global__ void __launch_bounds__(JOIN * 32) kv_combine_kernel(const AttnArgs A)
     if (!any_failed(A, lane)) return;
     const long long n = (long long)w.N * w.q_heads;
     for (long long x = (long long)blockIdx.y * (JOIN * 32) + threadIdx.x; x < n * D; x += (long long)gridDim.y * (JOIN * 32)) {
+      if (A.groups) {
+        A.kept[x] = NAN;
+        if (x < n) A.kept_lse[x] = NAN;
+        continue;
+      }
       A.out[x] = __float2bfloat16_rn(NAN);
       if (A.lse && x < n) A.lse[x] = NAN;
     }
@@ -996,7 +1052,19 @@ __global__ void __launch_bounds__(JOIN * 32) kv_combine_kernel(const AttnArgs A)
   }
   const int row = first_row + mine, i = row / G;
   const size_t at = (size_t)(item.row0 + i) * w.q_heads + item.h * G + row % G;
+  if (item.add) {
+    float own, kept;
+    add_kept(m, l, A.kept_lse[at], own, kept);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], own, A.kept[at * D + lane * E + e] * kept);
+  }
   const float f = l == 0.f ? 0.f : 1.f / l;
+  if (A.groups) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) A.kept[at * D + lane * E + e] = o[e] * f;
+    if (lane == 0) A.kept_lse[at] = LN2F * (m + log2f(l));
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<__nv_bfloat162*>(A.out + at * D + lane * E + e) = __floats2bfloat162_rn(o[e] * f, o[e + 1] * f);
@@ -1129,6 +1197,106 @@ static sv_status pick_attention(int nt, AttnArgs& A, cudaStream_t st) {
   }
 }
 
+static AttnArgs arguments(const Window& w, const void* q, long long q_stride, const void* k_codes, const float* k_scale,
+                          const void* v_codes, const float* v_scale, float scale, int window, void* out, float* lse) {
+  AttnArgs A = {};
+  A.w = w;
+  A.q = static_cast<const __nv_bfloat16*>(q);
+  A.q_stride = q_stride;
+  A.k_codes = static_cast<const uint8_t*>(k_codes), A.v_codes = static_cast<const uint8_t*>(v_codes);
+  A.k_scale = k_scale, A.v_scale = v_scale;
+  A.scale = scale * LOG2EF;
+  A.window = window;
+  A.out = static_cast<__nv_bfloat16*>(out);
+  A.lse = lse;
+  A.group = w.q_heads / w.kv_heads;
+  A.group_mul = ((1 << 16) + A.group - 1) / A.group;
+  return A;
+}
+
+// Shapes and alignments of an attention call.
+static sv_status check_attention(const Window& w, const void* q, long long q_stride, const void* k_codes, const float* k_scale,
+                                 const void* v_codes, const float* v_scale, float scale, int window, const void* out,
+                                 const float* lse) {
+  if (bad_window(w) || q_stride < (long long)w.q_heads * w.head_dim || window < 0 || !isfinite(scale)) return SV_ERR_SHAPE;
+  if ((long long)w.B * w.max_tokens * w.kv_heads > 2147483647ll) return SV_ERR_SHAPE;
+  if (!aligned(q, 16) || (q_stride * 2) % 16 || !aligned(out, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(w.seq_len, 4) || !aligned(w.cu_tokens, 4) ||
+      !aligned(w.page_table, 4) || !aligned(lse, 4))
+    return SV_ERR_ALIGN;
+  return SV_OK;
+}
+
+// The kernel for nt tiles of rows and its join, in workspace_size(A.w.B, ...) bytes.
+static sv_status launch_pass(AttnArgs& A, int nt, int workers, char* workspace, cudaStream_t st) {
+  A.prefix = reinterpret_cast<long long*>(workspace);
+  A.start = reinterpret_cast<Start*>(workspace + prefix_bytes(A.w.B));
+  A.failed = reinterpret_cast<uint8_t*>(workspace) + prefix_bytes(A.w.B) + start_bytes(workers);
+  A.part = reinterpret_cast<float*>(A.failed + failed_bytes(workers));
+  A.workers = workers;
+  if (nt == wide::NT) return launch_wide(A, st);
+  return A.w.head_dim == 128 ? pick_attention<128>(nt, A, st) : pick_attention<64>(nt, A, st);
+}
+
+// --- shared tokens: what the first pass goes over, a warp to a group. Whole units of 128 tokens
+// that every sequence with new tokens holds: no row of the group is masked there, and the second
+// pass begins at the start of a unit.
+constexpr int SHARED_UNIT = 128;
+static_assert(SHARED_UNIT % wide::TOK == 0, "units of the first pass");
+
+__global__ void __launch_bounds__(256) kv_groups_kernel(const Window w, const int32_t* cu_groups, const int32_t* shared_len,
+                                                        int groups, Group* out, int32_t* skip) {
+  const int g = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (g >= groups) return;
+  const int b0 = min(max(cu_groups[g], 0), w.B), b1 = min(max(cu_groups[g + 1], b0), w.B);
+  // sequences of no group
+  if (g == 0)
+    for (int b = lane; b < b0; b += 32) skip[b] = 0;
+  if (g == groups - 1)
+    for (int b = b1 + lane; b < w.B; b += 32) skip[b] = 0;
+  long long len = min((long long)shared_len[g], (long long)w.max_pages * w.page_size);
+  int lead = w.B;
+  for (int b = b0 + lane; b < b1; b += 32) {
+    const Seq s = sequence(w, b);
+    if (s.count > 0 && s.len >= 0) {
+      len = min(len, s.len);
+      lead = min(lead, b);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    len = min(len, __shfl_xor_sync(0xffffffffu, len, o));
+    lead = min(lead, __shfl_xor_sync(0xffffffffu, lead, o));
+  }
+  const int n = lead == w.B || len < 0 ? 0 : (int)len / SHARED_UNIT * SHARED_UNIT;
+  for (int b = b0 + lane; b < b1; b += 32) skip[b] = n;
+  if (lane == 0) {
+    const int first = min(max(w.cu_tokens[b0], 0), w.N), end = min(w.cu_tokens[b1], w.N);
+    out[g] = n ? Group{n, lead, first, max(end - first, 0)} : Group{0, 0, 0, 0};
+  }
+}
+
+// How spec_kv_attention_shared lies in its workspace.
+struct SharedPlan {
+  int nt1, nt2, workers1, workers2;
+  size_t groups, skip, kept, lse, pass, total;   // offsets
+};
+static SharedPlan shared_plan(int B, int groups, int N, int max_tokens, int group, int heads, int D, int sms) {
+  SharedPlan p;
+  p.nt1 = row_tiles((N + groups - 1) / groups, group, D);
+  p.nt2 = row_tiles(max_tokens, group, D);
+  p.workers1 = sms * blocks_per_sm(p.nt1), p.workers2 = sms * blocks_per_sm(p.nt2);
+  const auto up = [](size_t x) { return (x + 127) & ~(size_t)127; };
+  p.groups = 0;
+  p.skip = up((size_t)groups * sizeof(Group));
+  p.kept = p.skip + up((size_t)B * sizeof(int32_t));
+  p.lse = p.kept + up((size_t)N * heads * D * sizeof(float));
+  p.pass = p.lse + up((size_t)N * heads * sizeof(float));
+  const size_t a = workspace_size(groups, p.workers1, p.nt1, D), b = workspace_size(B, p.workers2, p.nt2, D);
+  p.total = p.pass + (a > b ? a : b);
+  return p;
+}
+
 }  // namespace svkv
 
 size_t spec_kv_attention_workspace_bytes(int B, int max_tokens, int q_heads, int kv_heads, int head_dim) {
@@ -1152,44 +1320,24 @@ sv_status spec_kv_attention(const void* q, long long q_stride, const void* k_cod
     return SV_ERR_NULL;
   const Window w{seq_len, cu_tokens, page_table, B,       N,        max_tokens, max_pages,
                  num_pages, page_size, q_heads,  kv_heads, head_dim};
-  if (bad_window(w) || q_stride < (long long)q_heads * head_dim || window < 0 || !isfinite(scale)) return SV_ERR_SHAPE;
-  if ((long long)B * max_tokens * kv_heads > 2147483647ll) return SV_ERR_SHAPE;
-  if (!aligned(q, 16) || (q_stride * 2) % 16 || !aligned(out, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) ||
-      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(seq_len, 4) || !aligned(cu_tokens, 4) ||
-      !aligned(page_table, 4) || !aligned(lse, 4))
-    return SV_ERR_ALIGN;
+  if (const sv_status bad = check_attention(w, q, q_stride, k_codes, k_scale, v_codes, v_scale, scale, window, out, lse)) return bad;
   const int nt = row_tiles(max_tokens, q_heads / kv_heads, head_dim);
   const int sms = aligned(workspace, 16) ? sm_count() : 1;
   if (sms < 1) return SV_ERR_CUDA;
   const int workers = sms * blocks_per_sm(nt);
   if (!aligned(workspace, 16) || workspace_bytes < workspace_size(B, workers, nt, head_dim))
     return SV_ERR_WORKSPACE;
-  AttnArgs A = {};
-  A.w = w;
-  A.q = static_cast<const __nv_bfloat16*>(q);
-  A.q_stride = q_stride;
-  A.k_codes = static_cast<const uint8_t*>(k_codes), A.v_codes = static_cast<const uint8_t*>(v_codes);
-  A.k_scale = k_scale, A.v_scale = v_scale;
-  A.scale = scale * LOG2EF;
-  A.window = window;
-  A.out = static_cast<__nv_bfloat16*>(out);
-  A.lse = lse;
-  A.prefix = static_cast<long long*>(workspace);
-  A.start = reinterpret_cast<Start*>(static_cast<char*>(workspace) + prefix_bytes(B));
-  A.failed = static_cast<uint8_t*>(workspace) + prefix_bytes(B) + start_bytes(workers);
-  A.part = reinterpret_cast<float*>(A.failed + failed_bytes(workers));
-  A.workers = workers;
-  A.group = q_heads / kv_heads;
-  A.group_mul = ((1 << 16) + A.group - 1) / A.group;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (nt == wide::NT) return launch_wide(A, st);
-  return head_dim == 128 ? pick_attention<128>(nt, A, st) : pick_attention<64>(nt, A, st);
+  AttnArgs A = arguments(w, q, q_stride, k_codes, k_scale, v_codes, v_scale, scale, window, out, lse);
+  return launch_pass(A, nt, workers, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream));
 }
 
 size_t spec_kv_attention_shared_workspace_bytes(int B, int groups, int N, int max_tokens, int q_heads, int kv_heads,
                                                 int head_dim) {
-  if (groups < 1 || groups > B || N < 1 || N > (1 << 24)) return 0;
-  return spec_kv_attention_workspace_bytes(B, max_tokens, q_heads, kv_heads, head_dim);
+  using namespace svkv;
+  if (groups < 1 || groups > B || N < 1 || N > (1 << 24) || max_tokens > N ||
+      spec_kv_attention_workspace_bytes(B, max_tokens, q_heads, kv_heads, head_dim) == 0)
+    return 0;
+  return shared_plan(B, groups, N, max_tokens, q_heads / kv_heads, q_heads, head_dim, sm_count()).total;
 }
 
 sv_status spec_kv_attention_shared(const void* q, long long q_stride, const void* k_codes, const float* k_scale,
@@ -1198,11 +1346,33 @@ sv_status spec_kv_attention_shared(const void* q, long long q_stride, const void
                                    const int32_t* shared_len, int B, int groups, int N, int max_tokens, int max_pages,
                                    int num_pages, int page_size, int q_heads, int kv_heads, int head_dim, float scale,
                                    void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!cu_groups || !shared_len) return SV_ERR_NULL;
+  using namespace svkv;
+  if (!q || !k_codes || !k_scale || !v_codes || !v_scale || !seq_len || !cu_tokens || !page_table || !cu_groups ||
+      !shared_len || !out || !workspace)
+    return SV_ERR_NULL;
+  const Window w{seq_len, cu_tokens, page_table, B,       N,        max_tokens, max_pages,
+                 num_pages, page_size, q_heads,  kv_heads, head_dim};
+  if (const sv_status bad = check_attention(w, q, q_stride, k_codes, k_scale, v_codes, v_scale, scale, 0, out, lse)) return bad;
   if (groups < 1 || groups > B) return SV_ERR_SHAPE;
-  if (!svkv::aligned(cu_groups, 4) || !svkv::aligned(shared_len, 4)) return SV_ERR_ALIGN;
-  // first form: every sequence reads its own row of the table
-  return spec_kv_attention(q, q_stride, k_codes, k_scale, v_codes, v_scale, seq_len, cu_tokens, page_table, B, N, max_tokens,
-                           max_pages, num_pages, page_size, q_heads, kv_heads, head_dim, scale, 0, out, lse, workspace,
-                           workspace_bytes, stream);
+  if (!aligned(cu_groups, 4) || !aligned(shared_len, 4)) return SV_ERR_ALIGN;
+  const int sms = aligned(workspace, 16) ? sm_count() : 1;
+  if (sms < 1) return SV_ERR_CUDA;
+  const SharedPlan p = shared_plan(B, groups, N, max_tokens, q_heads / kv_heads, q_heads, head_dim, sms);
+  if (!aligned(workspace, 16) || workspace_bytes < p.total) return SV_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  AttnArgs A = arguments(w, q, q_stride, k_codes, k_scale, v_codes, v_scale, scale, 0, out, lse);
+  A.kept = reinterpret_cast<float*>(ws + p.kept);
+  A.kept_lse = reinterpret_cast<float*>(ws + p.lse);
+  Group* g = reinterpret_cast<Group*>(ws + p.groups);
+  int32_t* skip = reinterpret_cast<int32_t*>(ws + p.skip);
+  kv_groups_kernel<<<(groups + 7) / 8, 256, 0, st>>>(w, cu_groups, shared_len, groups, g, skip);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  A.groups = g;
+  A.w.B = groups;
+  if (const sv_status bad = launch_pass(A, p.nt1, p.workers1, ws + p.pass, st)) return bad;
+  A.groups = nullptr;
+  A.w.B = B;
+  A.skip = skip;
+  return launch_pass(A, p.nt2, p.workers2, ws + p.pass, st);
 }

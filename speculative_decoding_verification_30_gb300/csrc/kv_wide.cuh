@@ -282,8 +282,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     // --- copies
     int cb = C.start_b;
     long long cu = u0;
-    Seq cs = sequence(w, cb);
-    Span cp = span_of<ROWS, TOK>(A, cs);
+    Seq cs = rows_of(A, cb);
+    Span cp = span_of<ROWS, TOK>(A, cb, cs);
+    int add = added(A, cb, cs);
     int ct, ch, cr;
     {
       const long long x = u0 - C.pre;
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       ct = (int)(x - item * per);
       ch = (int)quotient(item, cp.rts);
       cr = (int)(item - (long long)ch * cp.rts);
-      if (lane == 0) A.start[blockIdx.x] = Start{u0 - ct, cp.tiles, ch, cr, cs.first, cs.count, 0};
+      if (lane == 0) A.start[blockIdx.x] = Start{u0 - ct, cp.tiles, ch, cr, cs.first, cs.count, add};
     }
     int entry = -1, window_b = -1, window_h = -1, window0 = 0;
     float eks = 1.f, elv = 0.f, einv = 1.f;
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         window_b = cb;
         window_h = -1;
         window0 = j0;
-        entry = page_of(w, cb, (long long)j0 + lane);
+        entry = page_of(w, table_row(A, cb), (long long)j0 + lane);
       }
       if (ch != window_h) {
         window_h = ch;
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           I.r0 = cr * ROWS % G;
           I.h = ch;
           I.slot = u0 < item0 ? 1 : 0;
-          I.flags = u0 <= item0 + OVERHEAD && u1 >= item1 ? WHOLE : 0;
+          I.flags = (u0 <= item0 + OVERHEAD && u1 >= item1 ? WHOLE : 0) | add;
           arrive(&C.ready[ni % NM]);
         }
         expect(&C.kfull[ks_], bytes);
@@ -397,8 +398,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             ch = 0;
             if (cu < u1) {
               do {
-                cs = sequence(w, ++cb);
-                cp = span_of<ROWS, TOK>(A, cs);
+                cs = rows_of(A, ++cb);
+                cp = span_of<ROWS, TOK>(A, cb, cs);
+                add = added(A, cb, cs);
               } while (cp.rts == 0 && cb + 1 < w.B);
             }
           }
@@ -667,8 +669,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!wait_warp(&C.ofull[t], (uint32_t)it & 1, err)) break;
       after_sync();
       const size_t at = (size_t)(I.row0 + i) * w.q_heads + hd;
-      const bool whole = I.flags & WHOLE;
-      const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      const bool whole = I.flags & WHOLE, add = whole && there && (I.flags & ADD);
+      float own = 1.f, kept = 0.f;
+      if (add) add_kept(m, l, A.kept_lse[at], own, kept);
+      const float f = whole ? (l == 0.f ? 0.f : own / l) : 1.f;
+      kept = l == 0.f ? 0.f : kept / l;
       float* slot = A.part + ((size_t)blockIdx.x * 2 + I.slot) * ROWS * (D + 2);
       const int row = 128 * t + r;
 #pragma unroll 1
@@ -678,12 +683,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!there) continue;
 #pragma unroll
         for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+        if (add)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 z = *reinterpret_cast<const float4*>(A.kept + at * D + 32 * c + 4 * k);
+            y[4 * k] = __float_as_uint(fmaf(z.x, kept, __uint_as_float(y[4 * k])));
+            y[4 * k + 1] = __float_as_uint(fmaf(z.y, kept, __uint_as_float(y[4 * k + 1])));
+            y[4 * k + 2] = __float_as_uint(fmaf(z.z, kept, __uint_as_float(y[4 * k + 2])));
+            y[4 * k + 3] = __float_as_uint(fmaf(z.w, kept, __uint_as_float(y[4 * k + 3])));
+          }
         const uint32_t b = c == 0 ? bad[0] : c == 1 ? bad[1] : c == 2 ? bad[2] : bad[3];
         if (b)
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (b >> k & 1) y[k] = 0x7FC00000u;
-        if (whole) {
+        if (whole && !A.groups) {
           uint4* o = reinterpret_cast<uint4*>(A.out + at * D + 32 * c);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -696,7 +710,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             o[k] = make_uint4(z[0], z[1], z[2], z[3]);
           }
         } else {
-          float4* o = reinterpret_cast<float4*>(slot + 2 * ROWS + row * D + 32 * c);
+          float4* o = reinterpret_cast<float4*>((whole ? A.kept + at * D : slot + 2 * ROWS + row * D) + 32 * c);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             o[k] = make_float4(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1]), __uint_as_float(y[4 * k + 2]),
@@ -705,7 +719,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (there) {
         if (whole) {
-          if (A.lse) A.lse[at] = LN2F * (m + log2f(l));
+          float* to = A.groups ? A.kept_lse : A.lse;
+          if (to) to[at] = LN2F * (m + log2f(l));
         } else {
           slot[2 * row] = m;
           slot[2 * row + 1] = l;
