@@ -21,7 +21,7 @@
 
 namespace svq4 {
 
-constexpr int WARPS = 16, THREADS = 32 * WARPS;
+constexpr int WARPS = 16;                // of a block, at most
 constexpr int STEP = 64, SUPER = 4;      // elements of a step; steps of what is on its way
 constexpr int SMEM_MAX = 220 * 1024;
 
@@ -36,6 +36,13 @@ struct Args {
   int split;           // warps of a tile
 };
 
+__device__ __forceinline__ void mma16816_first(float* c, const uint32_t* a, const uint32_t* b, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, "
+      "%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(b[0]), "r"(a[1]), "r"(b[1]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint32_t* b, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
@@ -51,16 +58,6 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t (&x)[4]) {
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(x[k]) : "r"(t), "r"(0x43084308u));
   }
 }
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ float widen1(unsigned short x) { return __uint_as_float((uint32_t)x << 16); }
 
 // First element of the eight of (step, word) that lane q of four has.
@@ -74,7 +71,7 @@ __device__ __forceinline__ int element(int step, int word, int q) {
 template <int G, int NT>
 __device__ __forceinline__ void lay_out(const Args& A, int m0, int c0, int c1, uint4* sh, float* sx) {
   const int s0 = c0 * SUPER, steps = (c1 - c0) * SUPER;
-  for (int x = threadIdx.x; x < NT * steps * 64; x += THREADS) {
+  for (int x = threadIdx.x; x < NT * steps * 64; x += blockDim.x) {
     const int lane = x & 31, word = x >> 5 & 1, st = x / 64 % steps, nt = x / 64 / steps;
     const int m = m0 + 8 * nt + (lane >> 2), k = element<G>(s0 + st, word, lane & 3);
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -84,7 +81,7 @@ __device__ __forceinline__ void lay_out(const Args& A, int m0, int c0, int c1, u
                        __byte_perm(v.y, v.w, 0x7632));
   }
   const int g0 = s0 * STEP / G, groups = steps * STEP / G;
-  for (int x = threadIdx.x; x < 8 * NT * groups; x += THREADS) {
+  for (int x = threadIdx.x; x < 8 * NT * groups; x += blockDim.x) {
     const int m = m0 + x % (8 * NT), g = g0 + x / (8 * NT);
     float sum = 0.f;
     if (m < A.M && g * G < A.d) {
@@ -103,7 +100,7 @@ __device__ __forceinline__ void lay_out(const Args& A, int m0, int c0, int c1, u
 
 // G: group; NT: column tiles of 8 rows; R: tiles of 16 vocabulary rows of a warp
 template <int G, int NT, int R>
-__global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
+__global__ void __launch_bounds__(32 * WARPS, 1) q4_kernel(const Args A) {
   constexpr int PER = SUPER * STEP / G;            // groups of a super: 8, 4 or 2
   constexpr int OWN = PER > 4 ? 2 : 1;             // of which a lane looks up so many
   extern __shared__ uint4 smem[];
@@ -112,7 +109,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
   float* red = sx + (size_t)8 * NT * A.chunk * PER;   // [warp][R NT 4][lane]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int m0 = blockIdx.y * 8 * NT, half = A.d / 2, per = A.d / G, steps = A.d / STEP;
-  const int slots = WARPS / A.split, slot = warp % slots, part = warp / slots;
+  const int slots = (blockDim.x >> 5) / A.split, slot = warp % slots, part = warp / slots;
   const int tiles = (A.N + 16 * R - 1) / (16 * R), turns = (tiles + (int)gridDim.x * slots - 1) / ((int)gridDim.x * slots);
   const int chunks = (A.supers + A.chunk - 1) / A.chunk;
   // the supers of chunk c that are this warp's
@@ -120,50 +117,51 @@ __global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
   const auto to = [&](int c) { return c * A.chunk + (min(A.chunk, A.supers - c * A.chunk) * (part + 1)) / A.split; };
   const auto tile_of = [&](int turn) { return (turn * slots + slot) * (int)gridDim.x + (int)blockIdx.x; };
 
-  // What is on its way: super `ls` of tile number `lt`
+  // What is on its way: super `ls` of the tile of turn `lt`; `left` steps are there from its start on
   uint2 code[SUPER][2 * R];
   unsigned short sc[2 * R][OWN], bi[2 * R][OWN];
-  int lt = 0, lc = 0, ls = from(0);
-  int row[2 * R];
-  bool on = false;
+  int lt = 0, lc = 0, ls = from(0), left = 0;
+  const uint8_t* at[2 * R];
+  size_t sat[2 * R];
   const auto settle = [&]() {   // on the next super that there is
     while (lt < turns && ls >= to(lc)) {
       if (++lc == chunks) lc = 0, ++lt;
       if (lt < turns) ls = from(lc);
     }
-    on = lt < turns && tile_of(lt) < tiles;
+    left = lt < turns && tile_of(lt) < tiles ? steps - ls * SUPER : 0;
   };
-  const auto rows = [&]() {
-#pragma unroll
-    for (int j = 0; j < 2 * R; ++j)
-      row[j] = min(tile_of(min(lt, turns - 1)) * 16 * R + 8 * j + g, A.N - 1);
-  };
-  const auto load_codes = [&](int i) {
-    const int s = ls * SUPER + i;
+  const auto place = [&]() {
 #pragma unroll
     for (int j = 0; j < 2 * R; ++j) {
-      if (!on || s >= steps) continue;
-      const uint8_t* p = A.codes + (size_t)row[j] * half + s * (STEP / 2);
+      const size_t row = min(tile_of(min(lt, turns - 1)) * 16 * R + 8 * j + g, A.N - 1);
+      at[j] = A.codes + row * half + ls * (SUPER * STEP / 2) + (G == 32 ? 4 : 8) * q;
+      sat[j] = row * per + ls * PER + q * OWN;
+    }
+  };
+  const auto load_codes = [&](int i) {
+    if (i >= left) return;
+#pragma unroll
+    for (int j = 0; j < 2 * R; ++j) {
+      const uint8_t* p = at[j] + i * (STEP / 2);
       if (G == 32)
-        code[i][j] = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(p + 4 * q)), __ldg(reinterpret_cast<const uint32_t*>(p + 16 + 4 * q)));
+        code[i][j] = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(p)), __ldg(reinterpret_cast<const uint32_t*>(p + 16)));
       else
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(code[i][j].x), "=r"(code[i][j].y) : "l"(p + 8 * q));
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(code[i][j].x), "=r"(code[i][j].y) : "l"(p));
     }
   };
   const auto load_scales = [&]() {
+    const int there = left * STEP / G - q * OWN;   // groups from the lane's first one on
 #pragma unroll
-    for (int j = 0; j < 2 * R; ++j)
+    for (int o = 0; o < OWN; ++o)
+      if (o < there && (PER >= 4 || q < PER))
 #pragma unroll
-      for (int o = 0; o < OWN; ++o) {
-        const int x = ls * PER + q * OWN + o;
-        if (!on || q * OWN >= PER || x >= per) continue;
-        const size_t at = (size_t)row[j] * per + x;
-        sc[j][o] = __ldg(A.scale + at);
-        bi[j][o] = __ldg(A.bias + at);
-      }
+        for (int j = 0; j < 2 * R; ++j) {
+          sc[j][o] = __ldg(A.scale + sat[j] + o);
+          bi[j][o] = __ldg(A.bias + sat[j] + o);
+        }
   };
   settle();
-  rows();
+  place();
 #pragma unroll
   for (int i = 0; i < SUPER; ++i) load_codes(i);
   load_scales();
@@ -174,11 +172,11 @@ __global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
 
   for (int turn = 0; turn < turns; ++turn) {
     const int tile = tile_of(turn);
-    uint64_t out[R][NT][2];
+    float out[R][NT][4];
 #pragma unroll
     for (int t = 0; t < R; ++t)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) out[t][n][0] = out[t][n][1] = 0ull;
+      for (int n = 0; n < NT; ++n) out[t][n][0] = out[t][n][1] = out[t][n][2] = out[t][n][3] = 0.f;
     for (int c = 0; c < chunks; ++c) {
       if (chunks > 1) {
         __syncthreads();
@@ -199,8 +197,14 @@ __global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
           }
         // the next super begins to come while this one is worked on
         ++ls;
-        settle();
-        if (ls != s + 1 || lt != turn) rows();
+        left -= SUPER;
+        if (s + 1 < to(c)) {
+#pragma unroll
+          for (int j = 0; j < 2 * R; ++j) at[j] += SUPER * STEP / 2, sat[j] += PER;
+        } else {
+          settle();
+          place();
+        }
         load_scales();
         float acc[R][NT][4];
 #pragma unroll
@@ -209,11 +213,6 @@ __global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
           if (st < steps) {
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-              if (G == 32 || (w == 0 && i * STEP % G == 0))
-#pragma unroll
-                for (int t = 0; t < R; ++t)
-#pragma unroll
-                  for (int n = 0; n < NT; ++n) acc[t][n][0] = acc[t][n][1] = acc[t][n][2] = acc[t][n][3] = 0.f;
               uint32_t x[2 * R][4];
 #pragma unroll
               for (int j = 0; j < 2 * R; ++j) widen(w ? code[i][j].y : code[i][j].x, x[j]);
@@ -222,7 +221,10 @@ __global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
                 const uint4 b = sh[((n * held + st - c * A.chunk * SUPER) * 2 + w) * 32 + lane];
 #pragma unroll
                 for (int t = 0; t < R; ++t) {
-                  mma16816(acc[t][n], x[2 * t], x[2 * t + 1], b.x, b.y);
+                  if (G == 32 || (w == 0 && i * STEP % G == 0))
+                    mma16816_first(acc[t][n], x[2 * t], x[2 * t + 1], b.x, b.y);
+                  else
+                    mma16816(acc[t][n], x[2 * t], x[2 * t + 1], b.x, b.y);
                   mma16816(acc[t][n], x[2 * t] + 2, x[2 * t + 1] + 2, b.z, b.w);
                 }
               }
@@ -237,13 +239,13 @@ __global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
                 const float* px = sx + ((s - c * A.chunk) * PER + gi) * 8 * NT + 2 * q;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                  const uint64_t xs = *reinterpret_cast<const uint64_t*>(px + 8 * n);
+                  const float2 xs = *reinterpret_cast<const float2*>(px + 8 * n);
 #pragma unroll
                   for (int t = 0; t < R; ++t)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                      out[t][n][e] = fma2(pair(s2[2 * t + e], s2[2 * t + e]), pair(acc[t][n][2 * e], acc[t][n][2 * e + 1]),
-                                          fma2(pair(t2[2 * t + e], t2[2 * t + e]), xs, out[t][n][e]));
+                    for (int e = 0; e < 4; ++e)
+                      out[t][n][e] = fmaf(s2[2 * t + (e >> 1)], acc[t][n][e],
+                                          fmaf(t2[2 * t + (e >> 1)], e & 1 ? xs.y : xs.x, out[t][n][e]));
                 }
               }
             }
@@ -252,11 +254,6 @@ __global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
         }
       }
     }
-    const auto value = [&](int t, int n, int e) {
-      float a, b;
-      asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(out[t][n][e >> 1]));
-      return e & 1 ? b : a;
-    };
     if (A.split > 1) {
       // the parts of a tile, in their order
       const int id = 1 + slot, threads = 32 * A.split;
@@ -268,7 +265,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mine[((t * NT + n) * 4 + e) * 32] = value(t, n, e);
+            for (int e = 0; e < 4; ++e) mine[((t * NT + n) * 4 + e) * 32] = out[t][n][e];
       asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
       if (part) continue;
     }
@@ -280,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_kernel(const Args A) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int v = (tile * R + t) * 16 + g + 8 * (e >> 1), m = m0 + 8 * n + 2 * q + (e & 1);
-          float x = value(t, n, e);
+          float x = out[t][n][e];
           for (int p = 1; p < A.split; ++p) x += red[(size_t)(warp + p * slots) * (R * NT * 4 * 32) + ((t * NT + n) * 4 + e) * 32 + lane];
           if (v < A.N && m < A.M) A.logits[(size_t)m * A.N + v] = x;
         }
@@ -315,24 +312,26 @@ static sv_status launch(Args A, cudaStream_t st) {
   constexpr int R = NT <= 2 ? 2 : 1;
   const int sms = sm_count();
   if (sms < 1 || !raise_smem(reinterpret_cast<const void*>(q4_kernel<G, NT, R>))) return SV_ERR_CUDA;
-  // warps of a tile: the fewest with which turns that are not full cost a tenth at most
+  // Few tiles: as many warps to a tile as leave each SM with 16. Else as many warps in a block as make
+  // the turns come out: an SM's time goes by turns x warps.
   const long long tiles = (A.N + 16 * R - 1) / (16 * R);
-  int split = 1;
-  double best = 1e9;
-  for (int s = 1; s <= 8; s *= 2) {
-    const double turns = (double)tiles * s / ((double)sms * WARPS), cost = ceil(turns) / turns;
-    if (cost < best - 0.05) best = cost, split = s;
-    if (best <= 1.1) break;
-  }
-  A.split = split;
+  A.split = 1;
+  while (A.split < 8 && tiles * A.split * 2 <= (long long)sms * WARPS) A.split *= 2;
+  int warps = WARPS;
+  if (A.split == 1)
+    for (long long w = WARPS - 1, best = 1ll << 60; w >= WARPS / 2; --w) {
+      const auto cost = [&](long long x) { return (tiles + sms * x - 1) / (sms * x) * x; };
+      if (best == 1ll << 60) best = cost(WARPS);
+      if (cost(w) < best) best = cost(w), warps = (int)w;
+    }
   A.supers = (A.d + SUPER * STEP - 1) / (SUPER * STEP);
   const size_t each = (size_t)NT * SUPER * 64 * sizeof(uint4) + (size_t)8 * NT * (SUPER * STEP / G) * sizeof(float);
-  const size_t fixed = split > 1 ? (size_t)WARPS * R * NT * 4 * 32 * sizeof(float) : 0;
+  const size_t fixed = A.split > 1 ? (size_t)WARPS * R * NT * 4 * 32 * sizeof(float) : 0;
   const size_t fit = (SMEM_MAX - fixed) / each;
   A.chunk = (size_t)A.supers <= fit ? A.supers : (int)fit;
-  const long long blocks = (tiles * split + WARPS - 1) / WARPS;
+  const long long blocks = (tiles * A.split + warps - 1) / warps;
   const dim3 grid((unsigned)(blocks < sms ? blocks : sms), (unsigned)((A.M + 8 * NT - 1) / (8 * NT)));
-  q4_kernel<G, NT, R><<<grid, THREADS, A.chunk * each + fixed, st>>>(A);
+  q4_kernel<G, NT, R><<<grid, 32 * warps, A.chunk * each + fixed, st>>>(A);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 template <int G>
