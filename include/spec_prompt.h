@@ -43,10 +43,10 @@ sv_status spec_prompt_attention(const void* q, long long q_stride, const void* k
                                 long long v_stride, const int32_t* cu_tokens, int B, int N, int q_heads, int kv_heads,
                                 int head_dim, float scale, int window, void* out, float* lse, void* stream);
 
-/* Bytes of device workspace of spec_prompt_attention_backward; 0 for arguments outside the
- * limits. It need not be cleared and holds nothing between calls; calls that may run at the
+/* Bytes of device workspace of spec_prompt_attention_backward on the current device; 0 for
+ * arguments outside the limits or without a device. It need not be cleared and holds nothing between calls; calls that may run at the
  * same time must not share one. */
-size_t spec_prompt_attention_backward_workspace_bytes(int N, int q_heads);
+size_t spec_prompt_attention_backward_workspace_bytes(int B, int N, int q_heads, int kv_heads, int head_dim);
 
 /* The gradient with respect to q, k and v of a loss whose gradient with respect to out is
  * grad_out (token stride go_stride elements, as q). out and lse are what the forward call

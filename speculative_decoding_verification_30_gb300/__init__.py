@@ -90,7 +90,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.spec_kv_attention_shared.restype = i32
     lib.spec_prompt_attention.argtypes = [vp, i64, vp, i64, vp, i64, vp, *[i32] * 5, f32, i32, vp, vp, vp]
     lib.spec_prompt_attention.restype = i32
-    lib.spec_prompt_attention_backward_workspace_bytes.argtypes = [i32, i32]
+    lib.spec_prompt_attention_backward_workspace_bytes.argtypes = [i32] * 5
     lib.spec_prompt_attention_backward_workspace_bytes.restype = sz
     lib.spec_prompt_attention_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, *[i32] * 5, f32, i32,
                                                    vp, vp, vp, vp, sz, vp]

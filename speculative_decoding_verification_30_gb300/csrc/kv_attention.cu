@@ -287,6 +287,10 @@ __device__ __forceinline__ float ex2f(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// The second pass, which may begin before the first has ended, ends after it.
+__device__ __forceinline__ void after_first_pass(const AttnArgs& A) {
+  if (A.skip) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 // A row's sum l in the frame m and what the first pass kept for it, in one frame: factors of
 // the row's weighted values and of the kept ones, and their common sum in l, m.
 __device__ __forceinline__ void add_kept(float& m, float& l, float kept_lse, float& own, float& kept) {
@@ -429,6 +433,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  if (A.groups) asm volatile("griddepcontrol.wait;" ::: "memory");   // kv_groups_kernel's
   set_failed(A, tid, 0);
   const int G = A.group;
   constexpr int ALL = NTHR + 32;
@@ -436,7 +441,10 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
   long long u0, u1;
   const bool some = find_share<ROWS, TOK, ALL>(A, s_sum, &s_b, &s_pre, u0, u1);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (!some) return;
+  if (!some) {
+    after_first_pass(A);
+    return;
+  }
 
   if (warp == NWARP) {
     // --- the copying warp. Unit `cu` is number `ct` of item (cb, ch, cr)
@@ -566,10 +574,14 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
           wait_copies(smem_u32(full + stage), parity, LAND_NS);
           if (++stage == NS) stage = 0, parity ^= 1;
         }
+        after_first_pass(A);
         return;
       }
       bar(1, ALL);               // the unit is there, and the one before it is done with
-      if (ahead == 0) return;    // that was the END
+      if (ahead == 0) {          // that was the END
+        after_first_pass(A);
+        return;
+      }
       ahead += issue(stage == 0 ? NS - 1 : stage - 1) - 1;
       if (++stage == NS) stage = 0, parity ^= 1;
     }
@@ -888,6 +900,7 @@ __global__ void __launch_bounds__(NTHR + 32, (Shape<D, NT>::BLOCKS))
           if (flags & WHOLE) {
             const size_t at = (size_t)(M.row0 + i) * w.q_heads + M.h * G + M.r0 + r - (i - M.i0) * G;
             if (flags & ADD) {
+              after_first_pass(A);
               float own, kept;
               add_kept(m[n][e], sum, A.kept_lse[at], own, kept);
 #pragma unroll
@@ -956,6 +969,7 @@ __global__ void __launch_bounds__(JOIN * 32) kv_combine_kernel(const AttnArgs A)
   constexpr int ROWS = 8 * NT, E = D / 32;
   // first of all, in every thread: this grid ends only after the one before it
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Window& w = A.w;
   __shared__ bool failed;
   __shared__ float sm[JOIN], sl[JOIN], so[JOIN][D];
@@ -1163,6 +1177,24 @@ static sv_status launch_combine(AttnArgs& A, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kv_combine_kernel<D, NT>, A) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
+// The kernels of the passes over shared tokens begin while the kernel before them ends, and wait on
+// the device where they read its results.
+template <typename Kernel>
+static cudaError_t launch_main(Kernel kernel, const AttnArgs& A, int threads, size_t smem, const CUtensorMap& map_k,
+                               const CUtensorMap& map_v, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)A.workers);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = A.groups || A.skip ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, A, map_k, map_v);
+}
+
 template <int D, int NT>
 static sv_status launch_attention(AttnArgs& A, cudaStream_t st) {
   constexpr size_t SMEM = Shape<D, NT>::SMEM;
@@ -1170,8 +1202,7 @@ static sv_status launch_attention(AttnArgs& A, cudaStream_t st) {
   if (!raise_smem(reinterpret_cast<const void*>(kv_attention_kernel<D, NT>), SMEM) ||
       !code_map(&map_k, A.k_codes, A.w, Shape<D, NT>::TOK) || !code_map(&map_v, A.v_codes, A.w, Shape<D, NT>::TOK))
     return SV_ERR_CUDA;
-  kv_attention_kernel<D, NT><<<A.workers, NTHR + 32, SMEM, st>>>(A, map_k, map_v);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_main(kv_attention_kernel<D, NT>, A, NTHR + 32, SMEM, map_k, map_v, st) != cudaSuccess) return SV_ERR_CUDA;
   return launch_combine<D, NT>(A, st);
 }
 
@@ -1180,8 +1211,7 @@ static sv_status launch_wide(AttnArgs& A, cudaStream_t st) {
   if (!raise_smem(reinterpret_cast<const void*>(wide::kv_wide_kernel), wide::SMEM) ||
       !code_map(&map_k, A.k_codes, A.w, wide::TOK) || !code_map(&map_v, A.v_codes, A.w, wide::TOK))
     return SV_ERR_CUDA;
-  wide::kv_wide_kernel<<<A.workers, wide::THREADS, wide::SMEM, st>>>(A, map_k, map_v);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_main(wide::kv_wide_kernel, A, wide::THREADS, wide::SMEM, map_k, map_v, st) != cudaSuccess) return SV_ERR_CUDA;
   return launch_combine<wide::D, wide::NT>(A, st);
 }
 
@@ -1242,6 +1272,7 @@ static sv_status launch_pass(AttnArgs& A, int nt, int workers, char* workspace, 
 // that every sequence with new tokens holds: no row of the group is masked there, and the second
 // pass begins at the start of a unit.
 constexpr int SHARED_UNIT = 128;
+constexpr long long SHARED_BYTES = 320ll << 20;
 static_assert(SHARED_UNIT % wide::TOK == 0, "units of the first pass");
 
 __global__ void __launch_bounds__(256) kv_groups_kernel(const Window w, const int32_t* cu_groups, const int32_t* shared_len,
@@ -1276,14 +1307,24 @@ __global__ void __launch_bounds__(256) kv_groups_kernel(const Window w, const in
   }
 }
 
+// Tiles of 8 rows of an item of the first pass: the wide kernel's as in row_tiles, else those with the
+// fewest rows to spare.
+static int shared_tiles(long long rows, int D) {
+  const long long nt = (rows + 7) / 8;
+  if (D == wide::D && nt * 8 >= WIDE_ROWS) return wide::NT;
+  if (nt <= 4) return (int)nt;
+  const auto spent = [&](int t) { return (nt + t - 1) / t * t; };
+  return spent(6) <= spent(MAX_NT) ? 6 : MAX_NT;
+}
+
 // How spec_kv_attention_shared lies in its workspace.
 struct SharedPlan {
   int nt1, nt2, workers1, workers2;
-  size_t groups, skip, kept, lse, pass, total;   // offsets
+  size_t groups, skip, kept, lse, pass1, pass2, total;   // offsets
 };
 static SharedPlan shared_plan(int B, int groups, int N, int max_tokens, int group, int heads, int D, int sms) {
   SharedPlan p;
-  p.nt1 = row_tiles((N + groups - 1) / groups, group, D);
+  p.nt1 = shared_tiles((long long)((N + groups - 1) / groups) * group, D);
   p.nt2 = row_tiles(max_tokens, group, D);
   p.workers1 = sms * blocks_per_sm(p.nt1), p.workers2 = sms * blocks_per_sm(p.nt2);
   const auto up = [](size_t x) { return (x + 127) & ~(size_t)127; };
@@ -1291,9 +1332,9 @@ static SharedPlan shared_plan(int B, int groups, int N, int max_tokens, int grou
   p.skip = up((size_t)groups * sizeof(Group));
   p.kept = p.skip + up((size_t)B * sizeof(int32_t));
   p.lse = p.kept + up((size_t)N * heads * D * sizeof(float));
-  p.pass = p.lse + up((size_t)N * heads * sizeof(float));
-  const size_t a = workspace_size(groups, p.workers1, p.nt1, D), b = workspace_size(B, p.workers2, p.nt2, D);
-  p.total = p.pass + (a > b ? a : b);
+  p.pass1 = p.lse + up((size_t)N * heads * sizeof(float));
+  p.pass2 = p.pass1 + up(workspace_size(groups, p.workers1, p.nt1, D));   // the passes overlap: each has its own
+  p.total = p.pass2 + workspace_size(B, p.workers2, p.nt2, D);
   return p;
 }
 
@@ -1366,13 +1407,18 @@ sv_status spec_kv_attention_shared(const void* q, long long q_stride, const void
   A.kept_lse = reinterpret_cast<float*>(ws + p.lse);
   Group* g = reinterpret_cast<Group*>(ws + p.groups);
   int32_t* skip = reinterpret_cast<int32_t*>(ws + p.skip);
+  // What is read again at most where every sequence reads its own row of the table; below this much two passes
+  // take longer: 4 samples on 3,000 tokens, 20 MB: 27 us in one pass and 41 in two; 96 samples of 6 prompts of 5,000
+  // tokens, narrow heads, 300 MB: 51 and 58; 64 windows on 8,000 tokens, 1.1 GB: 199 and 110.
+  if ((long long)(B - groups) * max_pages * page_size * kv_heads * 2 * head_dim < SHARED_BYTES)
+    return launch_pass(A, p.nt2, p.workers2, ws + p.pass2, st);
   kv_groups_kernel<<<(groups + 7) / 8, 256, 0, st>>>(w, cu_groups, shared_len, groups, g, skip);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   A.groups = g;
   A.w.B = groups;
-  if (const sv_status bad = launch_pass(A, p.nt1, p.workers1, ws + p.pass, st)) return bad;
+  if (const sv_status bad = launch_pass(A, p.nt1, p.workers1, ws + p.pass1, st)) return bad;
   A.groups = nullptr;
   A.w.B = B;
   A.skip = skip;
-  return launch_pass(A, p.nt2, p.workers2, ws + p.pass, st);
+  return launch_pass(A, p.nt2, p.workers2, ws + p.pass2, st);
 }

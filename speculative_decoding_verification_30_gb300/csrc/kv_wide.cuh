@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     before_sync();
   }
+  if (A.groups) asm volatile("griddepcontrol.wait;" ::: "memory");   // kv_groups_kernel's
   long long u0, u1;
   const bool some = find_share<ROWS, TOK, THREADS>(A, C.sum, &C.start_b, &C.pre, u0, u1);
   after_sync();
@@ -671,6 +672,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const size_t at = (size_t)(I.row0 + i) * w.q_heads + hd;
       const bool whole = I.flags & WHOLE, add = whole && there && (I.flags & ADD);
       float own = 1.f, kept = 0.f;
+      if (I.flags & ADD) after_first_pass(A);
       if (add) add_kept(m, l, A.kept_lse[at], own, kept);
       const float f = whole ? (l == 0.f ? 0.f : own / l) : 1.f;
       kept = l == 0.f ? 0.f : kept / l;
@@ -733,6 +735,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");   // of rows that have stopped
   before_sync();
   __syncthreads();
+  after_first_pass(A);
   set_failed(A, tid, C.err);
   if (warp == 1) {
     after_sync();

@@ -27,6 +27,8 @@ struct BwdArgs {
   const float* lse;
   __nv_bfloat16 *gq, *gk, *gv;
   float *nlse, *ndelta;                  // workspace [q_heads][N]: -lse log2(e), -delta
+  int split;                             // pieces of a group's heads
+  float *part_k, *part_v;                // workspace [split][N][kv_heads][D], where split > 1
 };
 
 // --- delta and lse of each row. 16 lanes have a row of a head, 8 elements each.
@@ -82,6 +84,18 @@ __device__ __forceinline__ void store32(__nv_bfloat16* to, uint32_t from, float 
     reinterpret_cast<uint4*>(to)[k] = make_uint4(z[0], z[1], z[2], z[3]);
   }
 }
+// The same in fp32.
+__device__ __forceinline__ void keep32(float* to, uint32_t from, float f, bool there) {
+  uint32_t y[32];
+  tmem_ld32(y, from);
+  tmem_wait_ld();
+  pin<32>(y);
+  if (!there) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    reinterpret_cast<float4*>(to)[k] = make_float4(__uint_as_float(y[4 * k]) * f, __uint_as_float(y[4 * k + 1]) * f,
+                                                   __uint_as_float(y[4 * k + 2]) * f, __uint_as_float(y[4 * k + 3]) * f);
+}
 __device__ __forceinline__ void fill_rows(__nv_bfloat16* p, size_t row, int elements, int lane, int lanes, float x) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(x, x);
   for (int i = 2 * lane; i < elements; i += 2 * lanes) *reinterpret_cast<__nv_bfloat162*>(p + row * elements + i) = v;
@@ -97,6 +111,7 @@ __device__ __forceinline__ void clear_outside(const Prompts& p, __nv_bfloat16* g
 struct Item {
   int first, len, end;    // of the sequence; end: no item
   int token, head;        // the tile's first token; kv head (query head)
+  int h0, h1, part;       // query heads h0 .. h1 - 1 of the kv head, part `part` of them
   int lo, hi;             // tiles lo .. hi - 1, of each of the group's heads (of the kv head)
 };
 
@@ -122,11 +137,12 @@ constexpr int kv_smem() {
 }
 static_assert(kv_smem<128>() <= 227 * 1024, "one block on an SM");
 
-__device__ __forceinline__ Item kv_item(const Prompts& P, const Seq& s, int token, int slot) {
+__device__ __forceinline__ Item kv_item(const Prompts& P, int split, const Seq& s, int token, int slot) {
+  const int head = slot / split, part = slot - head * split, h0 = P.group * part / split, h1 = P.group * (part + 1) / split;
   const int tiles = (s.len + BLK - 1) / BLK;
   int hi = tiles;
   if (P.window) hi = (int)min((long long)tiles, ((long long)token + BLK - 1 + P.window - 1) / BLK + 1);
-  return Item{s.first, s.len, 0, token, slot, token / BLK, hi};
+  return Item{s.first, s.len, 0, token, head, head * P.group + h0, head * P.group + h1, part, token / BLK, hi};
 }
 
 template <int D>
@@ -141,7 +157,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   KvCtl<D>& C = *reinterpret_cast<KvCtl<D>*>(sg + NO * TILE);
   volatile int* err = &C.err;
   const Prompts& P = A.p;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = P.group;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < NI; ++i) bar_init(&C.ready[i], 1), bar_init(&C.taken[i], THREADS / 32 - 1);
@@ -168,14 +184,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // --- the walk, and the copies
-      Walk w = walk_start(P, BLK, P.kv_heads, 1, lane);
+      Walk w = walk_start(P, BLK, P.kv_heads * A.split, 1, lane);
       int u = 0, items = 0, asked_g = 0;
       bool ok = true;
       for (int it = 0; ok; ++it) {
         Seq s;
         int token, slot;
         const bool on = walk_to(P, w, piece_of(it), lane, s, token, slot);
-        const Item I = on ? kv_item(P, s, token, slot) : Item{0, 0, 1, 0, 0, 0, 0};
+        const Item I = on ? kv_item(P, A.split, s, token, slot) : Item{0, 0, 1, 0, 0, 0, 0, 0, 0, 0};
         if (it >= NI) ok = wait_warp(&C.taken[it % NI], (uint32_t)(it / NI - 1) & 1, err);
         if (!ok) break;
         if (lane == 0) {
@@ -191,7 +207,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           copy_tile<D>(sv, &map_v, I.head, I.first + I.token, &C.kvfull);
         }
         ++items;
-        for (int h = I.head * G; h < (I.head + 1) * G && ok; ++h)
+        for (int h = I.h0; h < I.h1 && ok; ++h)
           for (int i = I.lo; i < I.hi; ++i) {
             if (u >= NQ) ok = wait_warp(&C.qempty[u % NQ], (uint32_t)(u / NQ - 1) & 1, err);
             if (!ok) break;
@@ -241,7 +257,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!wait(&C.ready[it % NI], (uint32_t)(it / NI) & 1, err)) break;
           const Item& I = C.item[it % NI];
           if (I.end) break;
-          const int n = G * (I.hi - I.lo);
+          const int n = (I.h1 - I.h0) * (I.hi - I.lo);
           arrive(&C.taken[it % NI]);
           ok = wait(&C.kvfull, (uint32_t)it & 1, err);
           if (ok) scores(u);
@@ -282,7 +298,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         const Item& I = C.item[it % NI];
         if (I.end) break;
-        for (int h = I.head * G; h < (I.head + 1) * G && ok; ++h)
+        for (int h = I.h0; h < I.h1 && ok; ++h)
           for (int i = I.lo; i < I.hi; ++i, ++u) {
             const int live = I.len - BLK * i, x = g ? u % NO : u % NQ, y = u % NS;
             const float* from = (g ? A.ndelta : A.nlse) + (size_t)h * P.N + I.first + BLK * i;
@@ -317,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) break;
       const Item& I = C.item[it % NI];
       if (I.end) break;
-      const int n = G * (I.hi - I.lo);
+      const int n = (I.h1 - I.h0) * (I.hi - I.lo);
       int i = I.lo;
 #pragma unroll 1
       for (int x = 0; x < n; ++x, ++u) {
@@ -402,9 +418,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       after_sync();
       const bool there = I.token + r < I.len;
       const size_t at = ((size_t)(I.first + I.token + r) * P.kv_heads + I.head) * D;
+      if (A.split > 1) {
+        float* to = (half ? A.part_k : A.part_v) + (size_t)I.part * P.N * P.kv_heads * D + at;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32)
-        store32((half ? A.gk : A.gv) + at + c, (half ? tk : tv) + lanes + c, half ? A.scale : 1.f, there);
+        for (int c = 0; c < D; c += 32) keep32(to + c, (half ? tk : tv) + lanes + c, half ? A.scale : 1.f, there);
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32)
+          store32((half ? A.gk : A.gv) + at + c, (half ? tk : tv) + lanes + c, half ? A.scale : 1.f, there);
+      }
       before_sync();
       __syncwarp();
       if (lane == 0) arrive(&C.taken[it % NI]);
@@ -419,14 +441,39 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (C.err) {
     // given up: all rows of the block's pieces
-    Walk w = walk_start(P, BLK, P.kv_heads, 1, lane);
+    Walk w = walk_start(P, BLK, P.kv_heads * A.split, 1, lane);
     Seq s;
     int token, slot;
     for (int it = 0; walk_to(P, w, piece_of(it), lane, s, token, slot); ++it)
       for (int x = token + warp; x < min(token + BLK, s.len); x += THREADS / 32) {
-        fill_rows(A.gk, (size_t)(s.first + x) * P.kv_heads + slot, D, lane, 32, NAN);
-        fill_rows(A.gv, (size_t)(s.first + x) * P.kv_heads + slot, D, lane, 32, NAN);
+        const size_t row = (size_t)(s.first + x) * P.kv_heads + slot / A.split;
+        if (A.split > 1) {   // the sum of the parts becomes NaN
+          const size_t at = ((size_t)(slot % A.split) * P.N * P.kv_heads + row) * D;
+          for (int d = lane; d < D; d += 32) A.part_k[at + d] = A.part_v[at + d] = NAN;
+        } else {
+          fill_rows(A.gk, row, D, lane, 32, NAN);
+          fill_rows(A.gv, row, D, lane, 32, NAN);
+        }
       }
+  }
+}
+
+// The parts' sum, in their order; rows outside every sequence have been written.
+template <int D>
+__global__ void __launch_bounds__(256) prompt_sum_kernel(const BwdArgs A) {
+  const long long n = (long long)A.p.N * A.p.kv_heads * D / 4, x = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (x >= n) return;
+  const int r = (int)(x / (A.p.kv_heads * (D / 4)));
+  if (r < min(max(A.p.cu[0], 0), A.p.N) || r >= min(max(A.p.cu[A.p.B], 0), A.p.N)) return;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const float4* from = reinterpret_cast<const float4*>(v ? A.part_v : A.part_k) + x;
+    float4 sum = from[0];
+    for (int p = 1; p < A.split; ++p) {
+      const float4 y = from[p * n];
+      sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+    }
+    reinterpret_cast<uint2*>(v ? A.gv : A.gk)[x] = make_uint2(pack_bf2(sum.x, sum.y), pack_bf2(sum.z, sum.w));
   }
 }
 
@@ -452,7 +499,7 @@ constexpr int q_smem() {
 static_assert(q_smem<128>() <= 227 * 1024, "one block on an SM");
 
 __device__ __forceinline__ Item q_item(const Prompts& P, const Seq& s, int token, int slot) {
-  return Item{s.first, s.len, 0, token, slot, P.window ? max(token - P.window + 1, 0) / BLK : 0, token / BLK + 1};
+  return Item{s.first, s.len, 0, token, slot, slot, slot + 1, 0, P.window ? max(token - P.window + 1, 0) / BLK : 0, token / BLK + 1};
 }
 
 template <int D>
@@ -499,7 +546,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         Seq s;
         int token, slot;
         const bool on = walk_to(P, w, piece_of(it), lane, s, token, slot);
-        const Item I = on ? q_item(P, s, token, slot) : Item{0, 0, 1, 0, 0, 0, 0};
+        const Item I = on ? q_item(P, s, token, slot) : Item{0, 0, 1, 0, 0, 0, 0, 0, 0, 0};
         if (it >= NI) ok = wait_warp(&C.taken[it % NI], (uint32_t)(it / NI - 1) & 1, err);
         if (!ok) break;
         if (lane == 0) {
@@ -709,6 +756,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+static long long most_tiles(int B, int N) { return N / BLK + (B < N ? B : N); }
+// Pieces of a group's heads in prompt_grad_kv_kernel: where there are fewer tiles than SMs, as many as
+// give each SM one or two (5 texts of up to 333 tokens, 14 heads on 2 of 64: 35 us a call in 7 pieces, 53 in
+// one).
+static int split_of(int B, int N, int q_heads, int kv_heads, int sms) {
+  const long long pieces = most_tiles(B, N) * kv_heads, most = sms * 3ll / 2 / pieces;
+  return (int)(most < 1 ? 1 : most < q_heads / kv_heads ? most : q_heads / kv_heads);
+}
+static size_t rows_bytes(int N, int q_heads) { return (2 * (size_t)N * q_heads * sizeof(float) + 127) & ~(size_t)127; }
+
 template <int D>
 static sv_status launch(const BwdArgs& A, const void* q, long long qs, const void* k, long long ks, const void* v, long long vs,
                         cudaStream_t st) {
@@ -723,18 +780,25 @@ static sv_status launch(const BwdArgs& A, const void* q, long long qs, const voi
   prompt_rows_kernel<D><<<dim3((P.N + ROWS_BLOCK - 1) / ROWS_BLOCK, P.q_heads), 256, 0, st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   // no more blocks than there can be pieces
-  const long long tiles = P.N / BLK + (P.B < P.N ? P.B : P.N), nk = tiles * P.kv_heads, nq = tiles * P.q_heads;
+  const long long tiles = most_tiles(P.B, P.N), nk = tiles * P.kv_heads * A.split, nq = tiles * P.q_heads;
   prompt_grad_kv_kernel<D><<<(unsigned)(nk < sms ? nk : sms), THREADS, kv_smem<D>(), st>>>(A, mq, mk, mv, mg);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  if (A.split > 1) {
+    prompt_sum_kernel<D><<<(unsigned)(((long long)P.N * P.kv_heads * D / 4 + 255) / 256), 256, 0, st>>>(A);
+    if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  }
   prompt_grad_q_kernel<D><<<(unsigned)(nq < sms ? nq : sms), THREADS, q_smem<D>(), st>>>(A, mq, mk, mv, mg);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // namespace svpr
 
-size_t spec_prompt_attention_backward_workspace_bytes(int N, int q_heads) {
-  if (N < 1 || N > (1 << 24) || q_heads < 1 || q_heads > 64 * 256) return 0;
-  return (2 * (size_t)N * q_heads * sizeof(float) + 15) & ~(size_t)15;
+size_t spec_prompt_attention_backward_workspace_bytes(int B, int N, int q_heads, int kv_heads, int head_dim) {
+  using namespace svpr;
+  if (bad_shape(B, N, q_heads, kv_heads, head_dim, 1.f, 0)) return 0;
+  const int sms = sm_count(), split = sms < 1 ? 1 : split_of(B, N, q_heads, kv_heads, sms);
+  const size_t part = split > 1 ? (size_t)split * N * kv_heads * head_dim * sizeof(float) : 0;
+  return sms < 1 ? 0 : rows_bytes(N, q_heads) + 2 * part;
 }
 
 sv_status spec_prompt_attention_backward(const void* grad_out, long long go_stride, const void* q, long long q_stride,
@@ -754,7 +818,10 @@ sv_status spec_prompt_attention_backward(const void* grad_out, long long go_stri
       !rows_aligned(grad_out, go_stride) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(cu_tokens, 4) ||
       !aligned(grad_q, 16) || !aligned(grad_k, 16) || !aligned(grad_v, 16))
     return SV_ERR_ALIGN;
-  if (!aligned(workspace, 16) || workspace_bytes < spec_prompt_attention_backward_workspace_bytes(N, q_heads))
+  const int sms = aligned(workspace, 16) ? sm_count() : 1;
+  if (sms < 1) return SV_ERR_CUDA;
+  if (!aligned(workspace, 16) ||
+      workspace_bytes < spec_prompt_attention_backward_workspace_bytes(B, N, q_heads, kv_heads, head_dim))
     return SV_ERR_WORKSPACE;
   BwdArgs A = {};
   A.p = Prompts{cu_tokens, B, N, q_heads, kv_heads, q_heads / kv_heads, window};
@@ -767,6 +834,9 @@ sv_status spec_prompt_attention_backward(const void* grad_out, long long go_stri
   A.gv = static_cast<__nv_bfloat16*>(grad_v);
   A.nlse = static_cast<float*>(workspace);
   A.ndelta = A.nlse + (size_t)N * q_heads;
+  A.split = split_of(B, N, q_heads, kv_heads, sms);
+  A.part_k = reinterpret_cast<float*>(static_cast<char*>(workspace) + rows_bytes(N, q_heads));
+  A.part_v = A.part_k + (size_t)A.split * N * kv_heads * head_dim;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return head_dim == 128 ? launch<128>(A, q, q_stride, k, k_stride, v, v_stride, st)
                          : launch<64>(A, q, q_stride, k, k_stride, v, v_stride, st);

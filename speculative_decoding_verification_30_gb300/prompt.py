@@ -126,8 +126,8 @@ def spec_prompt_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: t
     op, lp = ptr(out, "out", _BF16, dev), ptr(lse, "lse", torch.float32, dev)
     with on_device(dev, stream, grad_out, q, k, v, out, lse, cu_tokens, workspace) as st:
         if workspace is None:
-            workspace = torch.empty(max(spec_prompt_attention_backward_workspace_bytes(*shape[:2]), 16), dtype=torch.uint8,
-                                    device=dev)
+            size = load().spec_prompt_attention_backward_workspace_bytes(*rest[1:6])
+            workspace = torch.empty(size or 16, dtype=torch.uint8, device=dev)
         wp, size = ptr(workspace, "workspace", torch.uint8, dev), workspace.numel()
         grads = [torch.empty(t.shape, dtype=_BF16, device=dev) for t in (q, k, v)]
         rc = load().spec_prompt_attention_backward(gp, gs, *qkv, op, lp, *rest, *(g.data_ptr() for g in grads), wp, size, st)
@@ -136,8 +136,8 @@ def spec_prompt_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: t
     return tuple(grads)
 
 
-def spec_prompt_attention_backward_workspace_bytes(N: int, q_heads: int) -> int:
-    """Bytes of workspace of spec_prompt_attention_backward; 0 for arguments outside its limits."""
-    if not all(0 <= x < _I32 for x in (N, q_heads)):
+def spec_prompt_attention_backward_workspace_bytes(B: int, N: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace of spec_prompt_attention_backward on the current device; 0 for arguments outside its limits."""
+    if not all(0 <= x < _I32 for x in (B, N, q_heads, kv_heads, head_dim)):
         return 0
-    return int(load().spec_prompt_attention_backward_workspace_bytes(N, q_heads))
+    return int(load().spec_prompt_attention_backward_workspace_bytes(B, N, q_heads, kv_heads, head_dim))

@@ -13,8 +13,13 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda"
 
 
-def build(groups, heads, kv_heads, dim, page, seed=0, spread=1.0):
-    """groups: a list of (shared tokens, [(own cached tokens or None for an empty place, new tokens), ...])."""
+# Two passes are made where the page table has room for this many bytes of keys and values that are read again
+TWO_PASSES = 320 << 20
+
+
+def build(groups, heads, kv_heads, dim, page, seed=0, spread=1.0, two=True):
+    """groups: a list of (shared tokens, [(own cached tokens or None for an empty place, new tokens), ...]).
+    two: the page table's rows are so long (unmapped at their ends) that the shared tokens are a pass of their own."""
     lens, new, of = [], [], []
     for i, (shared, members) in enumerate(groups):
         for own, t in members:
@@ -23,6 +28,11 @@ def build(groups, heads, kv_heads, dim, page, seed=0, spread=1.0):
             of.append(i)
     g, cache, sl, cu, table = make(lens, new, heads, kv_heads, dim, page, seed, spread=spread)
     cg = np.concatenate([[0], np.cumsum([len(m) for _, m in groups])])
+    again = (len(lens) - len(groups)) * kv_heads * 2 * dim * page
+    if two and again:
+        table = np.pad(table, ((0, 0), (0, max(0, TWO_PASSES // again + 1 - table.shape[1]))), constant_values=-1)
+    if not two:
+        assert again * table.shape[1] < TWO_PASSES
     shared = np.array([s for s, _ in groups], np.int32)
     for i, (s, _) in enumerate(groups):            # the members' rows name one member's pages for the whole pages shared
         live = [b for b in range(cg[i], cg[i + 1]) if lens[b] >= 0]
@@ -42,9 +52,9 @@ def build(groups, heads, kv_heads, dim, page, seed=0, spread=1.0):
 
 
 def check(groups, heads=8, kv_heads=2, dim=64, page=16, seed=0, told=None, scale=None, spread=1.0, edit=None, seqs=None, max_tokens=None,
-          q_edit=None):
+          q_edit=None, two=True):
     """told: what the call is told of shared_len, where that differs."""
-    g, cache, sl, cu, table, cg, shared = build(groups, heads, kv_heads, dim, page, seed, spread)
+    g, cache, sl, cu, table, cg, shared = build(groups, heads, kv_heads, dim, page, seed, spread, two)
     if edit:
         edit(cache, table)
     N = int(cu[-1])
@@ -68,6 +78,12 @@ def check(groups, heads=8, kv_heads=2, dim=64, page=16, seed=0, told=None, scale
 @pytest.mark.parametrize("heads,kv_heads,new", [(2, 2, 1), (8, 2, 3), (14, 2, 2), (32, 4, 5)])
 def test_one_prefix(heads, kv_heads, new, dim, page):
     check([(640, [(0, new), (1, new), (50, new), (300, new), (127, new)])], heads, kv_heads, dim, page, seed=dim + page + heads)
+
+
+def test_little_that_is_shared_is_one_pass():
+    g = [(640, [(0, 2), (50, 2), (300, 1)]), (100, [(None, 1), (4, 2)])]
+    a, b = (check(g, 4, 2, 64, 16, seed=20, two=two) for two in (False, True))
+    assert ((a[1] - b[1]).abs().nan_to_num(0) <= 1e-4).all()
 
 
 @pytest.mark.parametrize("dim", [64, 128])

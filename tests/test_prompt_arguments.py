@@ -18,7 +18,7 @@ def _forward(**kw):
 
 def _backward(**kw):
     a = dict(go=A, gs=1024, q=A, qs=1024, k=A, ks=256, v=A, vs=256, out=A, lse=A, cu=A, B=2, N=100, qh=8, kh=2, dim=128,
-             scale=0.1, window=0, gq=A, gk=A, gv=A, ws=A, wsb=sv.spec_prompt_attention_backward_workspace_bytes(100, 8))
+             scale=0.1, window=0, gq=A, gk=A, gv=A, ws=A, wsb=1 << 40)
     a.update(kw)
     return sv.load().spec_prompt_attention_backward(
         a["go"], a["gs"], a["q"], a["qs"], a["k"], a["ks"], a["v"], a["vs"], a["out"], a["lse"], a["cu"], a["B"], a["N"], a["qh"],
@@ -39,14 +39,15 @@ def test_forward_refuses(kw, status):
 @pytest.mark.parametrize("kw,status", [(dict([(x, None)]), 1) for x in ("go", "q", "k", "v", "out", "lse", "cu", "gq", "gk", "gv", "ws")] +
                          [(s, 2) for s in SHAPES + [dict(gs=1016)]] + [
     (dict(go=A + 8), 6), (dict(gs=1028), 6), (dict(out=A + 8), 6), (dict(gq=A + 4), 6), (dict(gk=A + 2), 6), (dict(gv=A + 8), 6),
-    (dict(lse=A + 2), 6), (dict(ws=A + 8), 4), (dict(wsb=100), 4)])
+    (dict(lse=A + 2), 6), (dict(ws=A + 8), 4), (dict(ws=A + 2), 4)])
 def test_backward_refuses(kw, status):
     assert _backward(**kw) == status
 
 
 def test_workspace_sizes():
     f = sv.spec_prompt_attention_backward_workspace_bytes
-    assert f(100, 8) >= 100 * 8 * 4 and f(0, 8) == 0 and f((1 << 24) + 1, 8) == 0 and f(1 << 40, 8) == 0 and f(-1, 8) == 0
+    assert f(2, 0, 8, 2, 64) == 0 and f(2, (1 << 24) + 1, 8, 2, 64) == 0 and f(2, 1 << 40, 8, 2, 64) == 0 and f(2, -1, 8, 2, 64) == 0
+    assert f(2, 100, 8, 3, 64) == 0 and f(2, 100, 8, 2, 96) == 0 and f(0, 100, 8, 2, 64) == 0
     g = sv.spec_kv_attention_shared_workspace_bytes
     assert g(2, 3, 4, 1, 8, 2, 128) == 0 and g(2, 0, 4, 1, 8, 2, 128) == 0 and g(2, 1, 4, 1, 8, 2, 96) == 0
     assert g(1 << 40, 1, 4, 1, 8, 2, 128) == 0
