@@ -6,8 +6,7 @@
 // 8-column side. The contraction may take its index in any order, so a lane keeps the 16
 // neighbouring codes that one 8-byte load of a row brings (64 elements of a row for the
 // four lanes that share it) and the hidden states are laid out to match, once, in shared memory. A
-// code becomes bf16 by way of 128 + code, whose low bits are the code; less 136 that is exact. The
-// products of a group are summed by themselves, then scaled:
+// code becomes bf16, exactly, by a mask and a multiply-add for two of them. The products of a group are summed by themselves, then scaled:
 //   logit += scale * sum (code - 8) h + (bias + 8 scale) * sum h.
 // Each warp streams its rows with the codes of the next 256 elements on their way in registers. Where a
 // device's warps would not get whole numbers of tiles, warps share a tile along d.
@@ -50,13 +49,15 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(b[0]), "r"(a[1]), "r"(b[1]), "r"(b0), "r"(b1));
 }
-// Eight codes less 8 as bf16, in the order 0 4, 1 5, 2 6, 3 7.
+// Eight codes as (code - 8) / 64 in bf16, in the order 0 4, 1 5, 2 6, 3 7. A code's bits at the foot of a
+// bf16 are a subnormal number, code 2^-133; from bit 4 on that or one of the smallest normal ones, code 2^-129.
+// Times 2^127 or 2^123, less 2^-3, both are that, exactly.
 __device__ __forceinline__ void widen(uint32_t w, uint32_t (&x)[4]) {
+  const uint32_t v = w >> 8;
+  const uint32_t c[4] = {w & 0x000F000Fu, w & 0x00F000F0u, v & 0x000F000Fu, v & 0x00F000F0u};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t t = ((w >> (4 * k)) & 0x000F000Fu) | 0x43004300u;   // 128 + code
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(x[k]) : "r"(t), "r"(0x43084308u));
-  }
+  for (int k = 0; k < 4; ++k)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(x[k]) : "r"(c[k]), "r"(k & 1 ? 0x7D007D00u : 0x7F007F00u), "r"(0xBE00BE00u));
 }
 __device__ __forceinline__ float widen1(unsigned short x) { return __uint_as_float((uint32_t)x << 16); }
 
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) q4_kernel(const Args A) {
 #pragma unroll
           for (int o = 0; o < OWN; ++o) {
             fs[j][o] = widen1(sc[j][o]);
-            ft[j][o] = fmaf(8.f, fs[j][o], widen1(bi[j][o]));
+            ft[j][o] = fmaf(8.f, fs[j][o], widen1(bi[j][o])) * 0.015625f;   // sums are kept in 64ths, as the products are
           }
         // the next super begins to come while this one is worked on
         ++ls;
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) q4_kernel(const Args A) {
           const int v = (tile * R + t) * 16 + g + 8 * (e >> 1), m = m0 + 8 * n + 2 * q + (e & 1);
           float x = out[t][n][e];
           for (int p = 1; p < A.split; ++p) x += red[(size_t)(warp + p * slots) * (R * NT * 4 * 32) + ((t * NT + n) * 4 + e) * 32 + lane];
-          if (v < A.N && m < A.M) A.logits[(size_t)m * A.N + v] = x;
+          if (v < A.N && m < A.M) A.logits[(size_t)m * A.N + v] = 64.f * x;
         }
   }
 }
