@@ -72,35 +72,51 @@ __device__ __forceinline__ int element(int step, int word, int q) {
 template <int G, int NT>
 __device__ __forceinline__ void lay_out(const Args& A, int m0, int c0, int c1, uint4* sh, float* sx) {
   const int s0 = c0 * SUPER, steps = (c1 - c0) * SUPER;
-  for (int x = threadIdx.x; x < NT * steps * 64; x += blockDim.x) {
-    const int lane = x & 31, word = x >> 5 & 1, st = x / 64 % steps, nt = x / 64 / steps;
-    const int m = m0 + 8 * nt + (lane >> 2), k = element<G>(s0 + st, word, lane & 3);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (m < A.M && k < A.d) v = *reinterpret_cast<const uint4*>(A.hidden + (size_t)m * A.d + k);
-    // pairs 01, 23, 45, 67 to 04, 15, 26, 37
-    sh[x] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                       __byte_perm(v.y, v.w, 0x7632));
-  }
-  const int g0 = s0 * STEP / G, groups = steps * STEP / G;
-  for (int x = threadIdx.x; x < 8 * NT * groups; x += blockDim.x) {
+  constexpr int AT_ONCE = 8;   // loads on their way
+  for (int nt = 0; nt < NT; ++nt)
+    for (int x0 = threadIdx.x; x0 < steps * 64; x0 += AT_ONCE * blockDim.x) {
+      uint4 v[AT_ONCE];
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) {
+        const int x = x0 + i * blockDim.x, m = m0 + 8 * nt + (x >> 2 & 7), k = element<G>(s0 + (x >> 6), x >> 5 & 1, x & 3);
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (x < steps * 64 && m < A.M && k < A.d) v[i] = *reinterpret_cast<const uint4*>(A.hidden + (size_t)m * A.d + k);
+      }
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) {
+        const int x = x0 + i * blockDim.x;
+        // pairs 01, 23, 45, 67 to 04, 15, 26, 37
+        if (x < steps * 64)
+          sh[nt * steps * 64 + x] = make_uint4(__byte_perm(v[i].x, v[i].z, 0x5410), __byte_perm(v[i].x, v[i].z, 0x7632),
+                                               __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632));
+      }
+    }
+  // sums: four lanes to a group
+  const int g0 = s0 * STEP / G, groups = steps * STEP / G, q = threadIdx.x & 3;
+  const unsigned four = 0xFu << (threadIdx.x & 28);
+#pragma unroll 2
+  for (int x = threadIdx.x >> 2; x < 8 * NT * groups; x += blockDim.x >> 2) {
     const int m = m0 + x % (8 * NT), g = g0 + x / (8 * NT);
     float sum = 0.f;
     if (m < A.M && g * G < A.d) {
-      const uint4* p = reinterpret_cast<const uint4*>(A.hidden + (size_t)m * A.d + g * G);
+      const uint4* p = reinterpret_cast<const uint4*>(A.hidden + (size_t)m * A.d + g * G) + q;
 #pragma unroll
-      for (int i = 0; i < G / 8; ++i) {
-        const uint4 v = p[i];
+      for (int i = 0; i < G / 32; ++i) {
+        const uint4 v = p[4 * i];
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xFFFF0000u);
       }
     }
-    sx[x] = sum;
+    sum += __shfl_xor_sync(four, sum, 1);
+    sum += __shfl_xor_sync(four, sum, 2);
+    if (q == 0) sx[x] = sum;
   }
 }
 
-// G: group; NT: column tiles of 8 rows; R: tiles of 16 vocabulary rows of a warp
-template <int G, int NT, int R>
+// G: group; NT: column tiles of 8 rows; R: tiles of 16 vocabulary rows of a warp; PARTS: the hidden states
+// do not fit shared memory and are laid out part by part, all over again for each turn
+template <int G, int NT, int R, bool PARTS>
 __global__ void __launch_bounds__(32 * WARPS, 1) q4_kernel(const Args A) {
   constexpr int PER = SUPER * STEP / G;            // groups of a super: 8, 4 or 2
   constexpr int OWN = PER > 4 ? 2 : 1;             // of which a lane looks up so many
@@ -112,7 +128,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) q4_kernel(const Args A) {
   const int m0 = blockIdx.y * 8 * NT, half = A.d / 2, per = A.d / G, steps = A.d / STEP;
   const int slots = (blockDim.x >> 5) / A.split, slot = warp % slots, part = warp / slots;
   const int tiles = (A.N + 16 * R - 1) / (16 * R), turns = (tiles + (int)gridDim.x * slots - 1) / ((int)gridDim.x * slots);
-  const int chunks = (A.supers + A.chunk - 1) / A.chunk;
+  const int chunks = PARTS ? (A.supers + A.chunk - 1) / A.chunk : 1;
   // the supers of chunk c that are this warp's
   const auto from = [&](int c) { return c * A.chunk + (min(A.chunk, A.supers - c * A.chunk) * part) / A.split; };
   const auto to = [&](int c) { return c * A.chunk + (min(A.chunk, A.supers - c * A.chunk) * (part + 1)) / A.split; };
@@ -163,13 +179,17 @@ __global__ void __launch_bounds__(32 * WARPS, 1) q4_kernel(const Args A) {
   };
   settle();
   place();
+  if (!PARTS) {
+    // the first codes come to the L2 meanwhile
+    if (left > 0)
 #pragma unroll
-  for (int i = 0; i < SUPER; ++i) load_codes(i);
-  load_scales();
-  if (chunks == 1) {
+      for (int j = 0; j < 2 * R; ++j) asm volatile("prefetch.global.L2 [%0];" ::"l"(at[j]));
     lay_out<G, NT>(A, m0, 0, A.supers, sh, sx);
     __syncthreads();
   }
+#pragma unroll
+  for (int i = 0; i < SUPER; ++i) load_codes(i);
+  load_scales();
 
   for (int turn = 0; turn < turns; ++turn) {
     const int tile = tile_of(turn);
@@ -179,7 +199,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) q4_kernel(const Args A) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) out[t][n][0] = out[t][n][1] = out[t][n][2] = out[t][n][3] = 0.f;
     for (int c = 0; c < chunks; ++c) {
-      if (chunks > 1) {
+      if (PARTS) {
         __syncthreads();
         lay_out<G, NT>(A, m0, c * A.chunk, min((c + 1) * A.chunk, A.supers), sh, sx);
         __syncthreads();
@@ -308,11 +328,17 @@ static bool raise_smem(const void* fn) try {
   return false;
 }
 
+// Bytes of a super's hidden states and sums in shared memory.
 template <int G, int NT>
+constexpr size_t super_bytes() {
+  return (size_t)NT * SUPER * 64 * sizeof(uint4) + (size_t)8 * NT * (SUPER * STEP / G) * sizeof(float);
+}
+
+template <int G, int NT, bool PARTS>
 static sv_status launch(Args A, cudaStream_t st) {
   constexpr int R = NT <= 2 ? 2 : 1;
   const int sms = sm_count();
-  if (sms < 1 || !raise_smem(reinterpret_cast<const void*>(q4_kernel<G, NT, R>))) return SV_ERR_CUDA;
+  if (sms < 1 || !raise_smem(reinterpret_cast<const void*>(q4_kernel<G, NT, R, PARTS>))) return SV_ERR_CUDA;
   // Few tiles: as many warps to a tile as leave each SM with 16. Else as many warps in a block as make
   // the turns come out: an SM's time goes by turns x warps.
   const long long tiles = (A.N + 16 * R - 1) / (16 * R);
@@ -325,26 +351,35 @@ static sv_status launch(Args A, cudaStream_t st) {
       if (best == 1ll << 60) best = cost(WARPS);
       if (cost(w) < best) best = cost(w), warps = (int)w;
     }
-  A.supers = (A.d + SUPER * STEP - 1) / (SUPER * STEP);
-  const size_t each = (size_t)NT * SUPER * 64 * sizeof(uint4) + (size_t)8 * NT * (SUPER * STEP / G) * sizeof(float);
-  const size_t fixed = A.split > 1 ? (size_t)WARPS * R * NT * 4 * 32 * sizeof(float) : 0;
+  const size_t fixed = A.split > 1 ? (size_t)WARPS * R * NT * 4 * 32 * sizeof(float) : 0, each = super_bytes<G, NT>();
   const size_t fit = (SMEM_MAX - fixed) / each;
-  A.chunk = (size_t)A.supers <= fit ? A.supers : (int)fit;
+  A.chunk = PARTS && (size_t)A.supers > fit ? (int)fit : A.supers;
   const long long blocks = (tiles * A.split + warps - 1) / warps;
   const dim3 grid((unsigned)(blocks < sms ? blocks : sms), (unsigned)((A.M + 8 * NT - 1) / (8 * NT)));
-  q4_kernel<G, NT, R><<<grid, 32 * warps, A.chunk * each + fixed, st>>>(A);
+  q4_kernel<G, NT, R, PARTS><<<grid, 32 * warps, A.chunk * each + fixed, st>>>(A);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
+// Shared memory that is always left for the sums of warps that share a tile.
+template <int G, int NT>
+static bool fits(const Args& A) {
+  return A.supers * super_bytes<G, NT>() + (size_t)WARPS * (NT <= 2 ? 2 : 1) * NT * 4 * 32 * sizeof(float) <= SMEM_MAX;
+}
+template <int G, int NT>
+static sv_status whole_or(const Args& A, cudaStream_t st) {
+  constexpr int UP = NT == 1 ? 1 : NT <= 4 ? 4 : 8;   // of the kernels that lay out parts there are three
+  return fits<G, NT>(A) ? launch<G, NT, false>(A, st) : launch<G, UP, true>(A, st);
+}
 template <int G>
-static sv_status pick(const Args& A, cudaStream_t st) {
+static sv_status pick(Args A, cudaStream_t st) {
+  A.supers = (A.d + SUPER * STEP - 1) / (SUPER * STEP);
   switch (A.M >= 64 ? 8 : (A.M + 7) / 8) {
-    case 1: return launch<G, 1>(A, st);
-    case 2: return launch<G, 2>(A, st);
-    case 3: return launch<G, 3>(A, st);
-    case 4: return launch<G, 4>(A, st);
-    case 5: return launch<G, 5>(A, st);
-    case 6: return launch<G, 6>(A, st);
-    default: return launch<G, 8>(A, st);
+    case 1: return whole_or<G, 1>(A, st);
+    case 2: return whole_or<G, 2>(A, st);
+    case 3: return whole_or<G, 3>(A, st);
+    case 4: return whole_or<G, 4>(A, st);
+    case 5: return whole_or<G, 5>(A, st);
+    case 6: return whole_or<G, 6>(A, st);
+    default: return whole_or<G, 8>(A, st);
   }
 }
 
