@@ -155,28 +155,41 @@ __global__ void __launch_bounds__(32 * WARPS, 1) q4_kernel(const Args A) {
       sat[j] = row * per + ls * PER + q * OWN;
     }
   };
+  // Loads where there is something, without branches, so that steps overlap
   const auto load_codes = [&](int i) {
-    if (i >= left) return;
 #pragma unroll
     for (int j = 0; j < 2 * R; ++j) {
       const uint8_t* p = at[j] + i * (STEP / 2);
       if (G == 32)
-        code[i][j] = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(p)), __ldg(reinterpret_cast<const uint32_t*>(p + 16)));
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %3, %4;\n\t@p ld.global.nc.u32 %0, [%2];\n\t@p ld.global.nc.u32 %1, [%2 + 16];\n\t}"
+            : "+r"(code[i][j].x), "+r"(code[i][j].y)
+            : "l"(p), "r"(i), "r"(left));
       else
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(code[i][j].x), "=r"(code[i][j].y) : "l"(p));
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %3, %4;\n\t@p ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
+            : "+r"(code[i][j].x), "+r"(code[i][j].y)
+            : "l"(p), "r"(i), "r"(left));
     }
   };
+  // Groups behind a row's end have scale and bias 0, and their hidden states are 0.
   const auto load_scales = [&]() {
     const int there = left * STEP / G - q * OWN;   // groups from the lane's first one on
 #pragma unroll
     for (int o = 0; o < OWN; ++o)
-      if (o < there && (PER >= 4 || q < PER))
 #pragma unroll
-        for (int j = 0; j < 2 * R; ++j) {
-          sc[j][o] = __ldg(A.scale + sat[j] + o);
-          bi[j][o] = __ldg(A.bias + sat[j] + o);
-        }
+      for (int j = 0; j < 2 * R; ++j) {
+        sc[j][o] = bi[j][o] = 0;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %4, %5;\n\t@p ld.global.nc.u16 %0, [%2];\n\t@p ld.global.nc.u16 %1, [%3];\n\t}"
+            : "+h"(sc[j][o]), "+h"(bi[j][o])
+            : "l"(A.scale + sat[j] + o), "l"(A.bias + sat[j] + o), "r"(o), "r"(PER >= 4 || q < PER ? there : 0));
+      }
   };
+#pragma unroll
+  for (int i = 0; i < SUPER; ++i)
+#pragma unroll
+    for (int j = 0; j < 2 * R; ++j) code[i][j] = make_uint2(0u, 0u);
   settle();
   place();
   if (!PARTS) {
@@ -231,7 +244,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) q4_kernel(const Args A) {
 #pragma unroll
         for (int i = 0; i < SUPER; ++i) {
           const int st = s * SUPER + i;
-          if (st < steps) {
+          {
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               uint32_t x[2 * R][4];
