@@ -138,6 +138,12 @@ __device__ __forceinline__ bool wait(Bar* b, uint32_t parity, volatile int* err,
 __device__ __forceinline__ bool wait_warp(Bar* b, uint32_t parity, volatile int* err) {
   return __all_sync(0xffffffffu, wait(b, parity, err));
 }
+// One lane of a warp that has come together, always the same: it issues products and commits them.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void commit(Bar* b) {

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   __syncthreads();
   after_sync();
-  const uint32_t tmem = C.taddr;   // S (and P) of tile t at columns 128 t, O at 256 + 128 t
+  const uint32_t tmem = __shfl_sync(0xffffffffu, C.taddr, 0);   // S (and P) of tile t at columns 128 t, O at 256 + 128 t
 
   if (warp < 4) {
   // registers: 128 x 72 and 256 x 216 are the 384 x 168 of the launch
@@ -204,54 +204,69 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // --- products, issued by one thread
-    if (lane == 0) {
-      int u = 0, uses[2] = {0, 0}, pu[2] = {0, 0};   // units; items and units of each tile
-      bool ok = true;
-      for (int it = 0; ok; ++it) {
-        if (!wait(&C.ready[it % NI], (uint32_t)(it / NI) & 1, err)) break;
-        const Item I = C.item[it % NI];
-        if (I.end) break;
-        arrive(&C.taken[it % NI]);
-        const int n = units_end(I);
-        const auto qk = [&](int t, int j, int at) {
+    // --- products. The warp stays together, so that addresses and descriptors are the same in all of it;
+    // one lane issues.
+    int u = 0, uses[2] = {0, 0}, pu[2] = {0, 0};   // units; items and units of each tile
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      ok = wait_warp(&C.ready[it % NI], (uint32_t)(it / NI) & 1, err);
+      if (!ok) break;
+      const int end = __shfl_sync(0xffffffffu, C.item[it % NI].end, 0), j0 = __shfl_sync(0xffffffffu, C.item[it % NI].j0, 0);
+      const int n0 = __shfl_sync(0xffffffffu, C.item[it % NI].n[0], 0), n1 = __shfl_sync(0xffffffffu, C.item[it % NI].n[1], 0);
+      if (end) break;
+      if (lane == 0) arrive(&C.taken[it % NI]);
+      const int n = max(n0, n1);
+      const auto qk = [&](int t, int j, int at) {
+        if (elect()) {
           mma_dims<D>(tmem + 128 * t, sq + t * TILE, sk + (at % NK) * TILE);
           commit(&C.sfull[t]);
-          if (j == I.n[t] - 1) commit(&C.qempty[t]);
-        };
-        ok = wait(&C.kfull[u % NK], (uint32_t)(u / NK) & 1, err);
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (I.n[t] == I.j0) continue;
-          ok = wait(&C.qfull[t], (uint32_t)uses[t] & 1, err);
-          if (!ok) break;
-          ++uses[t];
+          if (j == (t ? n1 : n0) - 1) commit(&C.qempty[t]);
+        }
+        __syncwarp();
+      };
+      ok = wait_warp(&C.kfull[u % NK], (uint32_t)(u / NK) & 1, err);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || (t ? n1 : n0) == j0) continue;
+        ok = wait_warp(&C.qfull[t], (uint32_t)uses[t] & 1, err);
+        if (!ok) continue;
+        ++uses[t];
+        after_sync();
+        qk(t, j0, u);
+      }
+      if (!ok) break;
+      if (elect()) commit(&C.kempty[u % NK]);
+      __syncwarp();
+      for (int j = j0; j < n; ++j, ++u) {
+        const bool more = j + 1 < n;
+        if (more) ok = wait_warp(&C.kfull[(u + 1) % NK], (uint32_t)((u + 1) / NK) & 1, err);
+        if (ok) ok = wait_warp(&C.vseen[u % NV], (uint32_t)(u / NV) & 1, err);
+        if (!ok) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int nt = t ? n1 : n0;
+          if (!ok || j >= nt) continue;
+          ok = wait_warp(&C.pfull[t], (uint32_t)pu[t] & 1, err);
+          if (!ok) continue;
+          ++pu[t];
           after_sync();
-          qk(t, I.j0, u);
+          if (elect()) {
+            mma_rows<D>(tmem + 256 + 128 * t, tmem + 128 * t, sv + (u % NV) * TILE, j != j0);
+            if (j == nt - 1) commit(&C.ofull[t]);
+          }
+          __syncwarp();
+          if (j + 1 < nt) qk(t, j + 1, u + 1);
         }
         if (!ok) break;
-        commit(&C.kempty[u % NK]);
-        for (int j = I.j0; j < n; ++j, ++u) {
-          const bool more = j + 1 < n;
-          if (more) ok = wait(&C.kfull[(u + 1) % NK], (uint32_t)((u + 1) / NK) & 1, err);
-          if (ok) ok = wait(&C.vseen[u % NV], (uint32_t)(u / NV) & 1, err);
-          if (!ok) break;
-          for (int t = 0; t < 2; ++t) {
-            if (j < I.n[t]) {
-              ok = wait(&C.pfull[t], (uint32_t)pu[t] & 1, err);
-              if (!ok) break;
-              ++pu[t];
-              after_sync();
-              mma_rows<D>(tmem + 256 + 128 * t, tmem + 128 * t, sv + (u % NV) * TILE, j != I.j0);
-              if (j == I.n[t] - 1) commit(&C.ofull[t]);
-              if (j + 1 < I.n[t]) qk(t, j + 1, u + 1);
-            }
-          }
-          if (!ok) break;
+        if (elect()) {
           commit(&C.vempty[u % NV]);
           if (more) commit(&C.kempty[(u + 1) % NK]);
         }
+        __syncwarp();
       }
-      // nothing is in flight when the block ends
+    }
+    // nothing is in flight when the block ends
+    if (elect()) {
       commit(&C.done);
       int never = 0;
       wait(&C.done, 0, &never, LAND_NS);
