@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   __syncthreads();
   after_sync();
-  const uint32_t tmem = C.taddr, ts = tmem, tp = tmem + 128, tv = tmem + 256, tk = tmem + 384;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, C.taddr, 0), ts = tmem, tp = tmem + 128, tv = tmem + 256, tk = tmem + 384;
 
   if (warp < 4) {
     // registers: 128 x 72 and 256 x 216 are the 384 x 168 of the launch
@@ -234,54 +234,67 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      // --- products, issued by one thread. While dS of a unit is formed, the tensor cores add its
-      // P^T dO and form the next S; while the next P is formed, they add dS^T Q and form the next dP.
-      if (lane == 0) {
-        int u = 0;
-        bool ok = true;
-        const auto scores = [&](int x) {
-          ok = wait(&C.qseen[x % NQ], (uint32_t)(x / NQ) & 1, err);
-          if (!ok) return;
-          after_sync();
+      // --- products. While dS of a unit is formed, the tensor cores add its P^T dO and form the next S;
+      // while the next P is formed, they add dS^T Q and form the next dP. The warp stays together, so
+      // that addresses and descriptors are the same in all of it; one lane issues.
+      int u = 0;
+      bool ok = true;
+      const auto scores = [&](int x) {
+        ok = wait_warp(&C.qseen[x % NQ], (uint32_t)(x / NQ) & 1, err);
+        if (!ok) return;
+        after_sync();
+        if (elect()) {
           mma_dims<D>(ts, sk, sq + (x % NQ) * TILE);
           commit(&C.sfull);
-        };
-        const auto products = [&](int x) {
-          ok = wait(&C.gseen[x % NO], (uint32_t)(x / NO) & 1, err);
-          if (!ok) return;
-          after_sync();
+        }
+        __syncwarp();
+      };
+      const auto products = [&](int x, bool last) {
+        ok = wait_warp(&C.gseen[x % NO], (uint32_t)(x / NO) & 1, err);
+        if (!ok) return;
+        after_sync();
+        if (elect()) {
           mma_dims<D>(tp, sv, sg + (x % NO) * TILE);
           commit(&C.dpfull);
-        };
-        for (int it = 0; ok; ++it) {
-          if (!wait(&C.ready[it % NI], (uint32_t)(it / NI) & 1, err)) break;
-          const Item& I = C.item[it % NI];
-          if (I.end) break;
-          const int n = (I.h1 - I.h0) * (I.hi - I.lo);
-          arrive(&C.taken[it % NI]);
-          ok = wait(&C.kvfull, (uint32_t)it & 1, err);
-          if (ok) scores(u);
-          if (ok) products(u);
-          if (ok && n == 1) commit(&C.kvempty);
-          for (int x = 0; x < n && ok; ++x, ++u) {
-            const bool more = x + 1 < n;
-            ok = wait(&C.pfull, (uint32_t)u & 1, err);
-            if (!ok) break;
-            after_sync();
+          if (last) commit(&C.kvempty);
+        }
+        __syncwarp();
+      };
+      for (int it = 0; ok; ++it) {
+        ok = wait_warp(&C.ready[it % NI], (uint32_t)(it / NI) & 1, err);
+        if (!ok) break;
+        const Item& I = C.item[it % NI];
+        const int end = __shfl_sync(0xffffffffu, I.end, 0), n = __shfl_sync(0xffffffffu, (I.h1 - I.h0) * (I.hi - I.lo), 0);
+        if (end) break;
+        if (lane == 0) arrive(&C.taken[it % NI]);
+        ok = wait_warp(&C.kvfull, (uint32_t)it & 1, err);
+        if (ok) scores(u);
+        if (ok) products(u, n == 1);
+        for (int x = 0; x < n && ok; ++x, ++u) {
+          const bool more = x + 1 < n;
+          ok = wait_warp(&C.pfull, (uint32_t)u & 1, err);
+          if (!ok) break;
+          after_sync();
+          if (elect()) {
             mma_rows<D>(tv, ts, sg + (u % NO) * TILE, x != 0, 32);
             commit(&C.gempty[u % NO]);
-            if (more) scores(u + 1);
-            if (ok) ok = wait(&C.dsfull, (uint32_t)u & 1, err);
-            if (!ok) break;
-            after_sync();
+          }
+          __syncwarp();
+          if (more) scores(u + 1);
+          if (ok) ok = wait_warp(&C.dsfull, (uint32_t)u & 1, err);
+          if (!ok) break;
+          after_sync();
+          if (elect()) {
             mma_rows<D>(tk, tp, sq + (u % NQ) * TILE, x != 0, 32);
             commit(&C.qempty[u % NQ]);
-            if (more) products(u + 1);
-            if (x + 2 == n) commit(&C.kvempty);
+            if (!more) commit(&C.ofull);
           }
-          if (ok) commit(&C.ofull);
+          __syncwarp();
+          if (more) products(u + 1, x + 2 == n);
         }
-        // nothing is in flight when the block ends
+      }
+      // nothing is in flight when the block ends
+      if (elect()) {
         commit(&C.done);
         int never = 0;
         wait(&C.done, 0, &never, LAND_NS);
@@ -533,7 +546,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   __syncthreads();
   after_sync();
-  const uint32_t tmem = C.taddr, tp = tmem + 256, to = tmem + 384;   // S of unit u at 128 (u % 2), dS over it
+  const uint32_t tmem = __shfl_sync(0xffffffffu, C.taddr, 0), tp = tmem + 256, to = tmem + 384;   // S of unit u at 128 (u % 2), dS over it
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -589,50 +602,66 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      // --- products, issued by one thread: S two units ahead, dP one
-      if (lane == 0) {
-        int u = 0;
-        bool ok = true;
-        const auto scores = [&](int x) {
-          ok = wait(&C.kseen[x % NK], (uint32_t)(x / NK) & 1, err);
-          if (!ok) return;
-          after_sync();
+      // --- products: S two units ahead, dP one
+      int u = 0;
+      bool ok = true;
+      const auto scores = [&](int x) {
+        ok = wait_warp(&C.kseen[x % NK], (uint32_t)(x / NK) & 1, err);
+        if (!ok) return;
+        after_sync();
+        if (elect()) {
           mma_dims<D>(tmem + 128 * (x & 1), sq, sk + (x % NK) * TILE);
           commit(&C.sfull[x & 1]);
-        };
-        const auto products = [&](int x) {
-          ok = wait(&C.vseen[x % NV], (uint32_t)(x / NV) & 1, err);
-          if (!ok) return;
-          after_sync();
+        }
+        __syncwarp();
+      };
+      const auto products = [&](int x) {
+        ok = wait_warp(&C.vseen[x % NV], (uint32_t)(x / NV) & 1, err);
+        if (!ok) return;
+        after_sync();
+        if (elect()) {
           mma_dims<D>(tp, sg, sv + (x % NV) * TILE);
           commit(&C.dpfull);
           commit(&C.vempty[x % NV]);
-        };
-        for (int it = 0; ok; ++it) {
-          if (!wait(&C.ready[it % NI], (uint32_t)(it / NI) & 1, err)) break;
-          const Item& I = C.item[it % NI];
-          if (I.end) break;
-          const int n = I.hi - I.lo;
-          arrive(&C.taken[it % NI]);
-          ok = wait(&C.qfull, (uint32_t)it & 1, err);
-          if (ok) scores(u);
-          if (ok) products(u);
-          if (ok && n > 1) scores(u + 1);
-          if (ok && n == 1) commit(&C.qempty);
-          for (int x = 0; x < n && ok; ++x, ++u) {
-            ok = wait(&C.dsfull, (uint32_t)u & 1, err);
-            if (!ok) break;
-            after_sync();
-            if (x + 1 < n) products(u + 1);
-            if (!ok) break;
+        }
+        __syncwarp();
+      };
+      for (int it = 0; ok; ++it) {
+        ok = wait_warp(&C.ready[it % NI], (uint32_t)(it / NI) & 1, err);
+        if (!ok) break;
+        const Item& I = C.item[it % NI];
+        const int end = __shfl_sync(0xffffffffu, I.end, 0), n = __shfl_sync(0xffffffffu, I.hi - I.lo, 0);
+        if (end) break;
+        if (lane == 0) arrive(&C.taken[it % NI]);
+        ok = wait_warp(&C.qfull, (uint32_t)it & 1, err);
+        if (ok) scores(u);
+        if (ok) products(u);
+        if (ok && n > 1) scores(u + 1);
+        if (ok && n == 1) {
+          if (elect()) commit(&C.qempty);
+          __syncwarp();
+        }
+        for (int x = 0; x < n && ok; ++x, ++u) {
+          ok = wait_warp(&C.dsfull, (uint32_t)u & 1, err);
+          if (!ok) break;
+          after_sync();
+          if (x + 1 < n) products(u + 1);
+          if (!ok) break;
+          if (elect()) {
             mma_rows<D>(to, tmem + 128 * (u & 1), sk + (u % NK) * TILE, x != 0, 32);
             commit(&C.kempty[u % NK]);
-            if (x + 2 < n) scores(u + 2);
-            if (x + 2 == n) commit(&C.qempty);
+            if (x + 1 == n) commit(&C.ofull);
           }
-          if (ok) commit(&C.ofull);
+          __syncwarp();
+          if (x + 2 < n) scores(u + 2);
+          if (x + 2 == n) {
+            if (elect()) commit(&C.qempty);
+            __syncwarp();
+          }
         }
-        // nothing is in flight when the block ends
+      }
+      // nothing is in flight when the block ends
+      if (elect()) {
         commit(&C.done);
         int never = 0;
         wait(&C.done, 0, &never, LAND_NS);
