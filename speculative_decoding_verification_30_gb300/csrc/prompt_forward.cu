@@ -51,6 +51,7 @@ struct Shape {
 template <int D>
 struct __align__(16) Ctl {
   static constexpr int NK = Shape<D>::NK, NV = Shape<D>::NV;
+  uint4 turn[8][32 * 4];       // of each warp of rows: 32 columns on their way out
   uint4 odd[NV][BLK];          // values that are not finite: a bit for each element of a token
   Item item[NI];
   Bar kfull[NK], kempty[NK], vfull[NV], vempty[NV], vseen[NV];
@@ -426,6 +427,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       after_sync();
       const bool there = i < I.len;
       const size_t at = (size_t)(I.first + i) * P.q_heads + I.head[t];
+      const size_t row_at = (size_t)(I.first + i - lane) * P.q_heads + I.head[t];   // of the warp's first row
+      uint4* turn = C.turn[warp - 4];
       const float f = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -433,7 +436,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_ld32(y, to + 32 * c);
         tmem_wait_ld();
         pin<32>(y);
-        if (!there) continue;
         const uint32_t b = c == 0 ? bad[0] : c == 1 ? bad[1] : c == 2 ? bad[2] : bad[3];
         uint32_t z[16];
 #pragma unroll
@@ -443,9 +445,19 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (b >> (2 * k + 1) & 1) y1 = NAN;
           z[k] = pack_bf2(y0, y1);
         }
-        uint4* o = reinterpret_cast<uint4*>(A.out + at * D + 32 * c);
+        // through shared memory, so that four lanes write 64 bytes of a row: a lane to a row takes the
+        // store unit four times as long, and the barriers' instructions wait behind it
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
+        for (int k = 0; k < 4; ++k)
+          turn[lane * 4 + (k ^ (lane >> 1 & 3))] = make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int x = 8 * k + (lane >> 2), e = lane & 3;
+          if (i - lane + x < I.len)
+            reinterpret_cast<uint4*>(A.out + (row_at + (size_t)x * P.q_heads) * D + 32 * c)[e] = turn[x * 4 + (e ^ (x >> 1 & 3))];
+        }
+        __syncwarp();
       }
       if (there && A.lse) A.lse[at] = LN2F * (m + log2f(l));
       before_sync();
