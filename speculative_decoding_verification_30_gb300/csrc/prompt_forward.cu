@@ -217,13 +217,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (end) break;
       if (lane == 0) arrive(&C.taken[it % NI]);
       const int n = max(n0, n1);
+      // S of tile t and unit j, by the lane that issues; the last of the tiles gives the keys' stage back
       const auto qk = [&](int t, int j, int at) {
-        if (elect()) {
-          mma_dims<D>(tmem + 128 * t, sq + t * TILE, sk + (at % NK) * TILE);
-          commit(&C.sfull[t]);
-          if (j == (t ? n1 : n0) - 1) commit(&C.qempty[t]);
-        }
-        __syncwarp();
+        mma_dims<D>(tmem + 128 * t, sq + t * TILE, sk + (at % NK) * TILE);
+        commit(&C.sfull[t]);
+        if (j == (t ? n1 : n0) - 1) commit(&C.qempty[t]);
+        if (t == (j < n1 ? 1 : 0)) commit(&C.kempty[at % NK]);
       };
       ok = wait_warp(&C.kfull[u % NK], (uint32_t)(u / NK) & 1, err);
 #pragma unroll
@@ -233,16 +232,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) continue;
         ++uses[t];
         after_sync();
-        qk(t, j0, u);
+        if (elect()) qk(t, j0, u);
+        __syncwarp();
       }
-      if (!ok) break;
-      if (elect()) commit(&C.kempty[u % NK]);
-      __syncwarp();
-      for (int j = j0; j < n; ++j, ++u) {
-        const bool more = j + 1 < n;
-        if (more) ok = wait_warp(&C.kfull[(u + 1) % NK], (uint32_t)((u + 1) / NK) & 1, err);
-        if (ok) ok = wait_warp(&C.vseen[u % NV], (uint32_t)(u / NV) & 1, err);
-        if (!ok) break;
+      for (int j = j0; j < n && ok; ++j, ++u) {
+        ok = wait_warp(&C.vseen[u % NV], (uint32_t)(u / NV) & 1, err);   // and the next unit's keys
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int nt = t ? n1 : n0;
@@ -254,16 +248,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (elect()) {
             mma_rows<D>(tmem + 256 + 128 * t, tmem + 128 * t, sv + (u % NV) * TILE, j != j0);
             if (j == nt - 1) commit(&C.ofull[t]);
+            if (t == (j < n1 ? 1 : 0)) commit(&C.vempty[u % NV]);
+            if (j + 1 < nt) qk(t, j + 1, u + 1);
           }
           __syncwarp();
-          if (j + 1 < nt) qk(t, j + 1, u + 1);
         }
-        if (!ok) break;
-        if (elect()) {
-          commit(&C.vempty[u % NV]);
-          if (more) commit(&C.kempty[(u + 1) % NK]);
-        }
-        __syncwarp();
       }
     }
     // nothing is in flight when the block ends
@@ -322,6 +311,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
         }
+        // a wait less for the warp that issues products: the next unit's keys are there too
+        if (j + 1 < n) ok = wait_warp(&C.kfull[(u + 1) % NK], (uint32_t)((u + 1) / NK) & 1, err);
+        if (!ok) break;
         __syncwarp();
         if (lane == 0) arrive(&C.vseen[vs]);
       }
