@@ -118,7 +118,7 @@ struct Item {
 template <int D>
 struct KvShape {
   static constexpr int TILE = D / 64 * COL;
-  static constexpr int NQ = 2, NO = 2, NS = 2;
+  static constexpr int NQ = 3, NO = 2, NS = 2;
 };
 template <int D>
 struct __align__(16) KvCtl {
@@ -133,7 +133,7 @@ struct __align__(16) KvCtl {
 };
 template <int D>
 constexpr int kv_smem() {
-  return 1024 + (2 + KvShape<D>::NQ + KvShape<D>::NO) * KvShape<D>::TILE + (int)sizeof(KvCtl<D>);
+  return (2 + KvShape<D>::NQ + KvShape<D>::NO) * KvShape<D>::TILE + (int)sizeof(KvCtl<D>);
 }
 static_assert(kv_smem<128>() <= 227 * 1024, "one block on an SM");
 
@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                           const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_g) {
   using S = KvShape<D>;
   constexpr int TILE = S::TILE, NQ = S::NQ, NO = S::NO, NS = S::NS;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) unsigned char smem_aligned[];   // no room to round up
+  unsigned char* smem = smem_aligned;
   unsigned char *sk = smem, *sv = sk + TILE, *sq = sv + TILE, *sg = sq + NQ * TILE;
   KvCtl<D>& C = *reinterpret_cast<KvCtl<D>*>(sg + NO * TILE);
   volatile int* err = &C.err;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bar_init(&C.pfull, 8), bar_init(&C.dsfull, 8), bar_init(&C.ofull, 1), bar_init(&C.done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    C.err = 0;
+    C.err = (smem_u32(smem) & 1023) != 0;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&C.taddr)) : "memory");
@@ -615,16 +615,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
       };
-      const auto products = [&](int x) {
-        ok = wait_warp(&C.vseen[x % NV], (uint32_t)(x / NV) & 1, err);
-        if (!ok) return;
-        after_sync();
-        if (elect()) {
-          mma_dims<D>(tp, sg, sv + (x % NV) * TILE);
-          commit(&C.dpfull);
-          commit(&C.vempty[x % NV]);
-        }
-        __syncwarp();
+      const auto products = [&](int x) {   // by the lane that issues
+        mma_dims<D>(tp, sg, sv + (x % NV) * TILE);
+        commit(&C.dpfull);
+        commit(&C.vempty[x % NV]);
       };
       for (int it = 0; ok; ++it) {
         ok = wait_warp(&C.ready[it % NI], (uint32_t)(it / NI) & 1, err);
@@ -635,19 +629,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) arrive(&C.taken[it % NI]);
         ok = wait_warp(&C.qfull, (uint32_t)it & 1, err);
         if (ok) scores(u);
-        if (ok) products(u);
-        if (ok && n > 1) scores(u + 1);
-        if (ok && n == 1) {
-          if (elect()) commit(&C.qempty);
-          __syncwarp();
+        if (ok) ok = wait_warp(&C.vseen[u % NV], (uint32_t)(u / NV) & 1, err);
+        if (!ok) break;
+        after_sync();
+        if (elect()) {
+          products(u);
+          if (n == 1) commit(&C.qempty);
         }
+        __syncwarp();
+        if (n > 1) scores(u + 1);
         for (int x = 0; x < n && ok; ++x, ++u) {
-          ok = wait_warp(&C.dsfull, (uint32_t)u & 1, err);
+          const bool more = x + 1 < n;
+          if (more) ok = wait_warp(&C.vseen[(u + 1) % NV], (uint32_t)((u + 1) / NV) & 1, err);
+          if (ok) ok = wait_warp(&C.dsfull, (uint32_t)u & 1, err);
           if (!ok) break;
           after_sync();
-          if (x + 1 < n) products(u + 1);
-          if (!ok) break;
           if (elect()) {
+            if (more) products(u + 1);
             mma_rows<D>(to, tmem + 128 * (u & 1), sk + (u % NK) * TILE, x != 0, 32);
             commit(&C.kempty[u % NK]);
             if (x + 1 == n) commit(&C.ofull);
