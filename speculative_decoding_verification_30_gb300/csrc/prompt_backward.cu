@@ -851,7 +851,7 @@ sv_status spec_prompt_attention_backward(const void* grad_out, long long go_stri
       workspace_bytes < spec_prompt_attention_backward_workspace_bytes(B, N, q_heads, kv_heads, head_dim))
     return SV_ERR_WORKSPACE;
   BwdArgs A = {};
-  A.p = Prompts{cu_tokens, B, N, q_heads, kv_heads, q_heads / kv_heads, window};
+  A.p = Prompts{cu_tokens, B, N, q_heads, kv_heads, q_heads / kv_heads, window < N ? window : 0};
   A.scale = scale;
   A.scale2 = fmaxf(scale * LOG2EF, 1.4e-45f);   // not 0: -inf of what is not seen stays -inf
   A.go = static_cast<const __nv_bfloat16*>(grad_out), A.out = static_cast<const __nv_bfloat16*>(out);

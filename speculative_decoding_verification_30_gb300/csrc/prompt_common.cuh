@@ -135,8 +135,8 @@ __device__ __forceinline__ bool wait(Bar* b, uint32_t parity, volatile int* err,
   }
   return true;
 }
-__device__ __forceinline__ bool wait_warp(Bar* b, uint32_t parity, volatile int* err) {
-  return __all_sync(0xffffffffu, wait(b, parity, err));
+__device__ __forceinline__ bool wait_warp(Bar* b, uint32_t parity, volatile int* err, uint64_t limit = SPEC_PROMPT_WAIT_NS) {
+  return __all_sync(0xffffffffu, wait(b, parity, err, limit));
 }
 // One lane of a warp that has come together, always the same: it issues products and commits them.
 __device__ __forceinline__ bool elect() {

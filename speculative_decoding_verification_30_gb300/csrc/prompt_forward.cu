@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     int u = 0, su = 0, uses = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
-      ok = wait_warp(&C.ready[it % NI], (uint32_t)(it / NI) & 1, err);
+      // a tile without rows waits for as long as the other one works
+      ok = wait_warp(&C.ready[it % NI], (uint32_t)(it / NI) & 1, err, 16 * SPEC_PROMPT_WAIT_NS);
       if (!ok) break;
       const Item& I = C.item[it % NI];
       if (I.end) break;
@@ -511,7 +512,7 @@ sv_status spec_prompt_attention(const void* q, long long q_stride, const void* k
       !aligned(lse, 4) || !aligned(cu_tokens, 4))
     return SV_ERR_ALIGN;
   FwdArgs A = {};
-  A.p = Prompts{cu_tokens, B, N, q_heads, kv_heads, q_heads / kv_heads, window};
+  A.p = Prompts{cu_tokens, B, N, q_heads, kv_heads, q_heads / kv_heads, window < N ? window : 0};
   A.scale = fmaxf(scale * LOG2EF, 1.4e-45f);   // not 0: -inf of what is not seen stays -inf
   A.out = static_cast<__nv_bfloat16*>(out);
   A.lse = lse;

@@ -142,6 +142,17 @@ def test_rows_outside_every_sequence(before, behind):
     check([40, 0], 2, 2, 128, before=before, behind=behind, seed=8)
 
 
+@pytest.mark.parametrize("window", [1 << 20, (1 << 31) - 2, (1 << 31) - 1])
+def test_windows_longer_than_every_prompt(window):
+    qkv, cu = make([130, 300], 2, 1, 64, seed=30)
+    q, k, v = qkv.to(DEV).split([2, 1, 1], 1)
+    cud = _i32(cu.tolist())
+    a, b = (sv.spec_prompt_attention(q, k, v, cud, window=w) for w in (0, window))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ga, gb = (sv.spec_prompt_attention_backward(a[0], q, k, v, *a, cud, window=w) for w in (0, window))
+    assert all(torch.equal(x, y) for x, y in zip(ga, gb))
+
+
 def test_no_rows_at_all():
     qkv, _ = make([], 4, 2, 64, behind=10)
     q, k, v = qkv.to(DEV).split([4, 2, 2], 1)
