@@ -131,7 +131,8 @@ size_t spec_kv_attention_shared_workspace_bytes(int B, int groups, int N, int ma
  *              its entries for them.
  * Whole units of 128 positions below shared_len[g] and below seq_len of every sequence of the
  * group that has new tokens are read through the first such sequence's row of the table, the rest
- * through each sequence's own. A negative seq_len marks an empty place, as in spec_kv_attention; it
+ * through each sequence's own. Where the page table has no room for 320 MB of keys and values that
+ * would be read again, every sequence reads its own row: that is faster. A negative seq_len marks an empty place, as in spec_kv_attention; it
  * limits nothing.
  * Limits: 1 <= groups <= B; other arguments, limits, outputs and statuses as in spec_kv_attention. */
 sv_status spec_kv_attention_shared(const void* q, long long q_stride, const void* k_codes, const float* k_scale,

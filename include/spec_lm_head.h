@@ -119,7 +119,7 @@ sv_status spec_verify_greedy_from_hidden(const void* hidden_target, const void* 
  * d a positive multiple of 64 and at most 65,536, group 32, 64 or 128 and a divisor of d.
  * Codes minus 8 and their products with hidden are exact; sums are fp32: with X the sum of
  * hidden over a group, a group adds scale * sum (code - 8) hidden + (bias + 8 scale) X.
- * Repeated calls give the same bits. Non-finite hidden states, scales and biases give
+ * Repeated calls give the same bits. Scales lie below 2^120. Non-finite hidden states, scales and biases give
  * non-finite logits in their rows and columns.
  * Returns SV_ERR_NULL, SV_ERR_SHAPE or SV_ERR_ALIGN before launching; SV_ERR_CUDA when the
  * launch fails. */

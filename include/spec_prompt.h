@@ -23,7 +23,8 @@
  *
  * Products are those of bf16 numbers, exact, summed in fp32; weights are rounded to bf16
  * for the products that take them (the gradient's P and dS too). Repeated calls give the
- * same bits.
+ * same bits. Every wait for a copy or product is bounded (0.2 s); a block of threads that gives
+ * one up writes NaN to all of its rows. Outputs must not overlap inputs.
  */
 #ifndef SPEC_PROMPT_H
 #define SPEC_PROMPT_H

@@ -8,8 +8,15 @@
 // four lanes that share it) and the hidden states are laid out to match, once, in shared memory. A
 // code becomes bf16, exactly, by a mask and a multiply-add for two of them. The products of a group are summed by themselves, then scaled:
 //   logit += scale * sum (code - 8) h + (bias + 8 scale) * sum h.
-// Each warp streams its rows with the codes of the next 256 elements on their way in registers. Where a
-// device's warps would not get whole numbers of tiles, warps share a tile along d.
+// Each warp streams its rows with the codes of the next 256 elements on their way in registers. Where
+// there are few tiles, warps share one along d.
+// Measured: 1 row x 151,936 x 1,024, groups of 64: 23.5 us, 3,750 GB/s; 5 rows x 4,096, groups of 128: 67 us,
+// 4,960 GB/s, 0.73 of measured, with issue at 56% and the loads of the next codes next; 40 rows x 50,257 x
+// 2,048, groups of 32: 66 us, latency of shared memory, shuffles and the products with 11 warps on an SM.
+// Tried: codes widened as 128 + code less 136 (seven instructions for eight codes and not five: 28 and 84
+// us); the next but one codes asked into the L2 (22.9 and 71 us); 16 warps with tiles shared by two of them for 40
+// rows (70 us); the 5th-generation tensor cores with codes widened into TMEM (47, 156 and 84 us: each 64 elements
+// are handed over and back, which takes longer than widening them).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>

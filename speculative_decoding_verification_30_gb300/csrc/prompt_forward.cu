@@ -7,7 +7,19 @@
 //   softmax      a thread to a row: S in registers, weights to TMEM as bf16 over S;
 //   O += P V     weights from TMEM, values with their rows contracted.
 // O stays in TMEM and is scaled there when a row's frame moves, which it does only when a
-// weight would pass 2^8. Warps: 0 walks the work and copies (TMA), 1 issues the products, 2-3
+// weight would pass 2^8. Rows of a tile are one head's tokens, so that any number of heads to a kv
+// head will do.
+// Measured: 2 prompts of 8,192 tokens, 32 heads on 8 of 128: 771 us, 1,430 TFLOP/s; 24 of up to 1,500
+// tokens 203 us; 8 of up to 4,001 in a window of 1,000, 12 heads of 64: 112 us. Clocks of a unit of
+// both tiles in long prompts: 3,150 while three waits and two commits lay between the weights and
+// their product (2,700 follow from the figures below). A tile's turn is 1,250 in the softmax (350 the
+// maximum, 690 exponentials and packing, 160 the store) and 1,100 in its two products, which the
+// other tile's turn covers; the tensor cores wait for the rest of the softmax. Head_dim 64 halves the
+// products and not the softmax. Short prompts: an item's start and end, 6,000 clocks, against 2,700
+// for a unit. Products issued from a branch of one lane, with descriptors in its registers, took 85
+// clocks each and not 64 (936 us): the warp stays together. A lane writing its row's 256 bytes by
+// itself kept the store unit, and the barriers behind it, busy for 4,000 clocks an item.
+// Warps: 0 walks the work and copies (TMA), 1 issues the products, 2-3
 // look for values that are not finite in units that not every row sees, 4-7 and 8-11 are the
 // rows. Every wait is bounded; one that runs out stops the block, which then writes NaN to
 // all of its rows.
