@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const size_t row_at = (size_t)(I.first + i - lane) * P.q_heads + I.head[t];   // of the warp's first row
       uint4* turn = C.turn[warp - 4];
       const float f = l == 0.f ? 0.f : 1.f / l;
+      const uint64_t f2 = pair(f, f);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t y[32];
@@ -442,12 +443,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_wait_ld();
         pin<32>(y);
         const uint32_t b = c == 0 ? bad[0] : c == 1 ? bad[1] : c == 2 ? bad[2] : bad[3];
+        if (b)
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (b >> k & 1) y[k] = 0x7FC00000u;
         uint32_t z[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          float y0 = __uint_as_float(y[2 * k]) * f, y1 = __uint_as_float(y[2 * k + 1]) * f;
-          if (b >> (2 * k) & 1) y0 = NAN;
-          if (b >> (2 * k + 1) & 1) y1 = NAN;
+          float y0, y1;
+          unpair(mul2(pair(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), f2), y0, y1);
           z[k] = pack_bf2(y0, y1);
         }
         // through shared memory, so that four lanes write 64 bytes of a row: a lane to a row takes the
