@@ -365,21 +365,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         after_sync();
         uint32_t x[128];
+        float best[4];   // the load finds the maxima
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(x + 32 * c, ts + 32 * c);
+        for (int c = 0; c < 4; ++c) tmem_max32(x + 32 * c, best[c], ts + 32 * c);
         tmem_wait_ld();
         pin<128>(x);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) asm volatile("" : "+f"(best[c]));
         const int hi = i - BLK * j, lo = P.window ? hi - P.window : -1;
         if (masked(P, I, t, j)) {
 #pragma unroll
           for (int k = 0; k < 128; ++k)
             if (k > hi || k <= lo) x[k] = 0xFF800000u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) best[k] = __uint_as_float(x[k]);
+#pragma unroll
+          for (int k = 4; k < 128; ++k) best[k & 3] = fmaxf(best[k & 3], __uint_as_float(x[k]));
         }
-        float best[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) best[k] = __uint_as_float(x[k]);
-#pragma unroll
-        for (int k = 4; k < 128; ++k) best[k & 3] = fmaxf(best[k & 3], __uint_as_float(x[k]));
         const float top = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * A.scale;
         const bool move = top > m + TOP;
         if (__any_sync(0xffffffffu, move)) {
