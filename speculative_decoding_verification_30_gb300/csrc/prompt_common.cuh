@@ -125,10 +125,14 @@ __device__ __forceinline__ bool wait(Bar* b, uint32_t parity, volatile int* err,
     return false;
   }
   if (arrived(at, parity)) return true;
-  const uint64_t t0 = now_ns();
-  while (!arrived(at, parity)) {
+  // the clock is looked at now and then: reading it takes longer than asking again
+  uint64_t t0 = 0;
+  for (uint32_t asked = 1; !arrived(at, parity); ++asked) {
+    if (asked % 32) continue;
     if (*err) return false;
-    if (now_ns() - t0 > limit) {
+    const uint64_t t = now_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > limit) {
       *err = 1;
       return false;
     }

@@ -48,11 +48,8 @@ struct Item {
 };
 __device__ __forceinline__ int units_end(const Item& I) { return max(I.n[0], I.n[1]); }
 // Whether some row of tile t does not see all keys of unit j.
-__device__ __forceinline__ bool masked(const Prompts& p, const Item& I, int t, int j) {
-  return BLK * j + BLK - 1 > I.q0[t] || (p.window && BLK * j <= I.q0[t] + BLK - 1 - p.window);
-}
-__device__ __forceinline__ bool masked_any(const Prompts& p, const Item& I, int j) {
-  return masked(p, I, 0, j) || masked(p, I, 1, j);
+__device__ __forceinline__ bool masked(const Prompts& p, int q0, int j) {
+  return BLK * j + BLK - 1 > q0 || (p.window && BLK * j <= q0 + BLK - 1 - p.window);
 }
 
 template <int D>
@@ -291,7 +288,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int vs = u % NV;
         ok = wait_warp(&C.vfull[vs], (uint32_t)(u / NV) & 1, err);
         if (!ok) break;
-        if (masked_any(P, I, j)) {
+        if (masked(P, I.q0[0], j) || masked(P, I.q0[1], j)) {
           unsigned char* at = sv + vs * TILE + half * 64 * 128;
           uint32_t hit = 0;
 #pragma unroll 1
@@ -356,11 +353,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) break;
       const Item& I = C.item[it % NI];
       if (I.end) break;
-      const int n = I.n[t], i = I.q0[t] + r;
+      const int n = I.n[t], j0 = I.j0, all = units_end(I) - j0, q0 = I.q0[t], other = I.q0[t ^ 1], i = q0 + r;
       float m = NO_FRAME, l = 0.f;
       uint32_t bad[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 1
-      for (int j = I.j0; j < n; ++j, ++su) {
+      for (int j = j0; j < n; ++j, ++su) {
         ok = wait_warp(&C.sfull[t], (uint32_t)su & 1, err);
         if (!ok) break;
         after_sync();
@@ -373,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) asm volatile("" : "+f"(best[c]));
         const int hi = i - BLK * j, lo = P.window ? hi - P.window : -1;
-        if (masked(P, I, t, j)) {
+        if (masked(P, q0, j)) {
 #pragma unroll
           for (int k = 0; k < 128; ++k)
             if (k > hi || k <= lo) x[k] = 0xFF800000u;
@@ -387,7 +384,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (__any_sync(0xffffffffu, move)) {
           // some weight would leave its range: those rows' frames move to their maxima
           const float m2 = move ? top : m, f = move ? ex2f(m - m2) : 1.f;   // f: 0 the first time
-          if (j != I.j0) {
+          if (j != j0) {
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t y[32];
@@ -403,8 +400,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           m = m2;
         }
         l += weights(x, ts, A.scale, m);
-        const int at = u + j - I.j0;
-        if (masked_any(P, I, j)) {
+        const int at = u + j - j0;
+        if (masked(P, q0, j) || masked(P, other, j)) {
           // the stage holds the unit until both tiles' weights are there
           const int vs = at % NV;
           ok = wait_warp(&C.vseen[vs], (uint32_t)(at / NV) & 1, err);
@@ -422,8 +419,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) arrive(&C.pfull[t]);
       }
       if (!ok) break;
-      u += units_end(I) - I.j0;
-      if (n == I.j0) {
+      u += all;
+      if (n == j0) {
         __syncwarp();
         if (lane == 0) arrive(&C.taken[it % NI]);
         continue;
