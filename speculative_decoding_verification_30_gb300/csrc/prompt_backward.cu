@@ -10,7 +10,7 @@
 // grad_q += dS K. Seven products in the place of the five that one kernel would need, but no
 // atomics; and no fp32 sums in memory, except where there are fewer tiles of keys than SMs: there
 // pieces of a group's heads are summed through memory, in their order.
-// Measured: 12 documents of up to 2,500 tokens, 32 heads on 8 of 128: 781 us, 776 TFLOP/s of the five
+// Measured: 12 documents of up to 2,500 tokens, 32 heads on 8 of 128: 777 us, 781 TFLOP/s of the five
 // products; rows 46 us (5,700 GB/s), keys' side 376 us (tensor pipe 62% active), queries' side 330 us
 // (52%). Both are near what shared memory gives: a product of two tiles there reads 64 KB, all that it
 // can in the product's 512 clocks, and 64 KB of tiles come in for each unit. Queries have three stages on

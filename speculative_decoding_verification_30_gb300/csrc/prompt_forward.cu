@@ -9,16 +9,17 @@
 // O stays in TMEM and is scaled there when a row's frame moves, which it does only when a
 // weight would pass 2^8. Rows of a tile are one head's tokens, so that any number of heads to a kv
 // head will do.
-// Measured: 2 prompts of 8,192 tokens, 32 heads on 8 of 128: 771 us, 1,430 TFLOP/s; 24 of up to 1,500
-// tokens 203 us; 8 of up to 4,001 in a window of 1,000, 12 heads of 64: 112 us. Clocks of a unit of
-// both tiles in long prompts: 3,150 while three waits and two commits lay between the weights and
-// their product (2,700 follow from the figures below). A tile's turn is 1,250 in the softmax (350 the
-// maximum, 690 exponentials and packing, 160 the store) and 1,100 in its two products, which the
-// other tile's turn covers; the tensor cores wait for the rest of the softmax. Head_dim 64 halves the
-// products and not the softmax. Short prompts: an item's start and end, 6,000 clocks, against 2,700
-// for a unit. Products issued from a branch of one lane, with descriptors in its registers, took 85
-// clocks each and not 64 (936 us): the warp stays together. A lane writing its row's 256 bytes by
-// itself kept the store unit, and the barriers behind it, busy for 4,000 clocks an item.
+// Measured: 2 prompts of 8,192 tokens, 32 heads on 8 of 128: 742 us, 1,480 TFLOP/s; 24 of up to 1,500
+// tokens 199 us; 8 of up to 4,001 in a window of 1,000, 12 heads of 64: 112 us. Clocks of a unit of
+// both tiles in long prompts: 2,850, of which the products take 2,200 (16 of a tile 1,100, issued
+// without a pause). A tile's softmax is 1,250 (load 50, maximum and votes 290, exponentials and packing
+// 740, store 160) and its products' results 250 behind the last one, so that the tensor cores
+// wait some 300 clocks a tile. Head_dim 64 halves the products and not the softmax. Short prompts: an
+// item's end takes 4,500 clocks (the results' way out 3,500) beside 2,850 for a unit. The maximum
+// taken from registers, 765 us; products issued from a branch of one lane, with descriptors in its
+// registers, 85 clocks each and not 64, 936 us; waits and commits one after the other between
+// weights and product, 816 us; a lane writing its row's 256 bytes by itself, which keeps the store
+// unit, and the barriers behind it, busy, 842 us.
 // Warps: 0 walks the work and copies (TMA), 1 issues the products, 2-3
 // look for values that are not finite in units that not every row sees, 4-7 and 8-11 are the
 // rows. Every wait is bounded; one that runs out stops the block, which then writes NaN to
