@@ -401,3 +401,58 @@ def test_a_long_prompt_against_64_bits_on_the_device(dim, heads, kv_heads, windo
         d = 2 * (dim + 8) * U * A + 8 * U * (1.45 * (A + m.abs()[:, None]) + 8) + 2.0 ** -21
         assert ((out[at, h].double() - ref).abs() <= (2.0 ** -8 + 2 * d + 2 * T * U) * size + 2.0 ** -8 * ref.abs()).all()
         assert ((lse[at, h].double() - m).abs() <= d[:, 0] + (T + 80) * U + 4 * U * m.abs()).all()
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(64, 1, 64), (126, 2, 128), (256, 256, 64), (192, 64, 128)])
+def test_many_heads(heads, kv_heads, dim):
+    check([40, 1, 150], heads, kv_heads, dim, seed=31, window=0 if heads < 200 else 30)
+
+
+def test_offsets_past_32_bits():
+    # queries, results and gradients of 2.3e9 elements: rows at both ends against float64 on the device, with the
+    # tolerances of the header (a row sees 100 keys; the keys' last row is seen by one query of each of 64 heads)
+    T, H, kv, D, W = 70_000, 256, 4, 128, 100
+    g = torch.Generator(device=DEV).manual_seed(32)
+
+    def rnd(heads):
+        return torch.randn(T, heads, D, generator=g, device=DEV, dtype=BF)
+    q, k, v, go = rnd(H), rnd(kv), rnd(kv), rnd(H)
+    cu, c = _i32([0, T]), D ** -0.5
+    out, lse = sv.spec_prompt_attention(q, k, v, cu, window=W)
+    gq, gk, gv = sv.spec_prompt_attention_backward(go, q, k, v, out, lse, cu, window=W)
+
+    def d_of(A, m):
+        return 2 * (D + 8) * U * A + 8 * U * (1.45 * (A + abs(m)) + 8) + 2.0 ** -21
+
+    def ds_of(p, d, q, k, v, go, o):
+        """dS and how far it may be off, of pairs in rows."""
+        dp, ab = (go * v).sum(-1), (go * v).abs().sum(-1)
+        delta, size = (go * o).sum(-1), (go * o).abs().sum(-1)
+        ds = p * (dp - delta)
+        return ds, p * 2 * (D + 8) * U * (ab + size) + (d + 4 * U) * p * (dp.abs() + delta.abs()) + 2.0 ** -8 * ds.abs()
+    for r in (3, T // 2, T - 1):
+        for h in (0, H - 1):
+            a = max(0, r - W + 1)
+            n = r + 1 - a
+            kk, vv, x, y, o = (t.double() for t in (k[a:r + 1, h // 64], v[a:r + 1, h // 64], q[r, h], go[r, h], out[r, h]))
+            z = kk @ x * c
+            m = float(torch.logsumexp(z, 0))
+            d = d_of(float((kk.abs() @ x.abs()).max()) * c, m)
+            p = torch.softmax(z, 0)
+            ref = p @ vv
+            assert ((o - ref).abs() <= (2.0 ** -8 + 2 * d + 2 * n * U) * (p @ vv.abs()) + 2.0 ** -8 * ref.abs()).all()
+            assert abs(float(lse[r, h]) - m) <= d + (n + 80) * U + 4 * U * abs(m)
+            # the gradient starts from the call's own lse, which is off by as much again
+            ds, off = ds_of(p, 2 * d + (n + 80) * U, x, kk, vv, y, o)
+            ref = ds @ kk * c
+            tol = c * ((off + 2 * n * U * ds.abs()) @ kk.abs()) + 2.0 ** -8 * ref.abs()
+            assert ((gq[r, h].double() - ref).abs() <= tol).all()
+    r, y, hs = T - 1, kv - 1, slice(H - 64, H)
+    x, w, o, kk, vv = q[r, hs].double(), go[r, hs].double(), out[r, hs].double(), k[r, y].double(), v[r, y].double()
+    p = torch.exp(x @ kk * c - lse[r, hs].double())
+    d = d_of(float((x.abs() @ kk.abs()).max()) * c, float(lse[r, hs].abs().max()))
+    ref = p @ w
+    assert ((gv[r, y].double() - ref).abs() <= (2.0 ** -8 + d + 128 * U) * (p @ w.abs()) + 2.0 ** -8 * ref.abs()).all()
+    ds, off = ds_of(p, d, x, kk, vv, w, o)
+    ref = ds @ x * c
+    assert ((gk[r, y].double() - ref).abs() <= c * ((off + 128 * U * ds.abs()) @ x.abs()) + 2.0 ** -8 * ref.abs()).all()
