@@ -371,7 +371,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int lo = I.token + r - q0 - 64 * half, hi = P.window ? lo + P.window : 1 << 30;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
-            if (c < lo || c >= hi) p[c] = 0xFF800000u;
+            if (c < lo) p[c] = 0xFF800000u;
+          if (P.window)
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c >= hi) p[c] = 0xFF800000u;
         }
         const uint64_t a = pair(A.scale2, A.scale2);
         const float4* nl = reinterpret_cast<const float4*>(C.nlse[y] + 64 * half);
@@ -725,7 +729,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int hi = I.token + r - k0 - 64 * half, lo = P.window ? hi - P.window : -1;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
-            if (c > hi || c <= lo) p[c] = 0xFF800000u;
+            if (c > hi) p[c] = 0xFF800000u;
+          if (P.window)
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c <= lo) p[c] = 0xFF800000u;
         }
 #pragma unroll
         for (int c = 0; c < 64; c += 2) {

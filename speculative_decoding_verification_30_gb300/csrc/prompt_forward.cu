@@ -372,9 +372,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int c = 0; c < 4; ++c) asm volatile("" : "+f"(best[c]));
         const int hi = i - BLK * j, lo = P.window ? hi - P.window : -1;
         if (masked(P, q0, j)) {
+          // nearly always one of the two
+          if (BLK * j + BLK - 1 > q0)
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k > hi || k <= lo) x[k] = 0xFF800000u;
+            for (int k = 0; k < 128; ++k)
+              if (k > hi) x[k] = 0xFF800000u;
+          if (P.window && BLK * j <= q0 + BLK - 1 - P.window)
+#pragma unroll
+            for (int k = 0; k < 128; ++k)
+              if (k <= lo) x[k] = 0xFF800000u;
 #pragma unroll
           for (int k = 0; k < 4; ++k) best[k] = __uint_as_float(x[k]);
 #pragma unroll
