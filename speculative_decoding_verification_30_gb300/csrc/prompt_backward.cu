@@ -74,21 +74,41 @@ __device__ __forceinline__ void clear_tail(unsigned char* tile, int live, int la
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
 }
-// 32 columns of a row of TMEM, times f, as bf16.
-__device__ __forceinline__ void store32(__nv_bfloat16* to, uint32_t from, float f, bool there) {
-  uint32_t y[32];
+// 32 columns of a row of TMEM, times f, as bf16, to the lane's row `to` of rows `stride` elements apart, of
+// which `rows` are there from the warp's first one on. Four lanes hand one another their parts of 16
+// bytes, so that they write 64 bytes of a row together: a lane to a row takes the store unit four times as long.
+__device__ __forceinline__ void store32(__nv_bfloat16* to, size_t stride, uint32_t from, float f, int rows) {
+  uint32_t y[32], z[4][4];
   tmem_ld32(y, from);
   tmem_wait_ld();
   pin<32>(y);
-  if (!there) return;
+  const uint64_t f2 = pair(f, f);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t z[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      z[e] = pack_bf2(__uint_as_float(y[8 * k + 2 * e]) * f, __uint_as_float(y[8 * k + 2 * e + 1]) * f);
-    reinterpret_cast<uint4*>(to)[k] = make_uint4(z[0], z[1], z[2], z[3]);
+  for (int k = 0; k < 16; ++k) {
+    float y0, y1;
+    unpair(mul2(pair(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), f2), y0, y1);
+    z[k >> 2][k & 3] = pack_bf2(y0, y1);
   }
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int round = 1; round <= 2; ++round) {
+    const bool odd = lane & round;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c & round) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? z[c][e] : z[c | round][e], round);
+        if (odd) z[c][e] = got;
+        else z[c | round][e] = got;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)   // part `lane & 3` of row j of the four
+    if ((lane & ~3) + j < rows)
+      reinterpret_cast<uint4*>(to + ((long long)j - (lane & 3)) * (long long)stride)[lane & 3] =
+          make_uint4(z[j][0], z[j][1], z[j][2], z[j][3]);
 }
 // The same in fp32.
 __device__ __forceinline__ void keep32(float* to, uint32_t from, float f, bool there) {
@@ -448,7 +468,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       } else {
 #pragma unroll 1
         for (int c = 0; c < D; c += 32)
-          store32((half ? A.gk : A.gv) + at + c, (half ? tk : tv) + lanes + c, half ? A.scale : 1.f, there);
+          store32((half ? A.gk : A.gv) + at + c, (size_t)P.kv_heads * D, (half ? tk : tv) + lanes + c, half ? A.scale : 1.f,
+                  I.len - I.token - (r & ~31));
       }
       before_sync();
       __syncwarp();
@@ -773,7 +794,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       after_sync();
       const size_t at = ((size_t)(I.first + I.token + r) * P.q_heads + I.head) * D;
 #pragma unroll 1
-      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) store32(A.gq + at + c, to + lanes + c, A.scale, there);
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32)
+        store32(A.gq + at + c, (size_t)P.q_heads * D, to + lanes + c, A.scale, I.len - I.token - (r & ~31));
       before_sync();
       __syncwarp();
       if (lane == 0) arrive(&C.taken[it % NI]);
