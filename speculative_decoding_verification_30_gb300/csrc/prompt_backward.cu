@@ -10,14 +10,17 @@
 // grad_q += dS K. Seven products in the place of the five that one kernel would need, but no
 // atomics; and no fp32 sums in memory, except where there are fewer tiles of keys than SMs: there
 // pieces of a group's heads are summed through memory, in their order.
-// Measured: 12 documents of up to 2,500 tokens, 32 heads on 8 of 128: 777 us, 781 TFLOP/s of the five
-// products; rows 46 us (5,700 GB/s), keys' side 376 us (tensor pipe 62% active), queries' side 330 us
-// (52%). Both are near what shared memory gives: a product of two tiles there reads 64 KB, all that it
-// can in the product's 512 clocks, and 64 KB of tiles come in for each unit. Queries have three stages on
+// Measured: 12 documents of up to 2,500 tokens, 32 heads on 8 of 128: 750 us, 808 TFLOP/s of the five
+// products; rows 46 us (5,700 GB/s), keys' side 366 us (tensor pipe some 63% active), queries' side 302 us
+// (some 57%). The keys' side is near what shared memory gives: a product of two tiles there reads 64 KB, all that
+// it can in the product's 512 clocks, and 64 KB of tiles come in for each unit. Queries have three stages on
 // the keys' side: with two, S waits for its copy (788 us); waiting for them before P^T dO is issued,
-// 879 us. Blocks as in the forward kernel: warp 0 walks the work and copies, 1 issues the products, 2-3
-// see to what lies behind a sequence's end, 4-11 have the rows, each half of them 64 columns. Every wait is
-// bounded; a block that gives up writes NaN to all of its rows.
+// 879 us. A unit of the queries' side takes 2,290 clocks, its products 1,650: the warp that issues them
+// waits for copies in between. One wait for a unit's values and the next one's keys asks for a key
+// stage that is not free yet: its kernel 377 us. A lane writing 64 bytes of its own row on the way
+// out: 774 us. Blocks as in the forward kernel: warp 0 walks the work and copies, 1 issues the
+// products, 2-3 see to what lies behind a sequence's end, 4-11 have the rows, each half of them 64
+// columns. Every wait is bounded; a block that gives up writes NaN to all of its rows.
 #include "prompt_common.cuh"
 
 namespace svpr {

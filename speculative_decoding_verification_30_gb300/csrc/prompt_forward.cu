@@ -9,8 +9,8 @@
 // O stays in TMEM and is scaled there when a row's frame moves, which it does only when a
 // weight would pass 2^8. Rows of a tile are one head's tokens, so that any number of heads to a kv
 // head will do.
-// Measured: 2 prompts of 8,192 tokens, 32 heads on 8 of 128: 742 us, 1,480 TFLOP/s; 24 of up to 1,500
-// tokens 199 us; 8 of up to 4,001 in a window of 1,000, 12 heads of 64: 112 us. Clocks of a unit of
+// Measured: 2 prompts of 8,192 tokens, 32 heads on 8 of 128: 745 us, 1,475 TFLOP/s; 24 of up to 1,500
+// tokens 196 us; 8 of up to 4,001 in a window of 1,000, 12 heads of 64: 102 us. Clocks of a unit of
 // both tiles in long prompts: 2,850, of which the products take 2,200 (16 of a tile 1,100, issued
 // without a pause). A tile's softmax is 1,250 (load 50, maximum and votes 290, exponentials and packing
 // 740, store 160) and its products' results 250 behind the last one, so that the tensor cores
