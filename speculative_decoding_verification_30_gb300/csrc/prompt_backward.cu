@@ -535,7 +535,7 @@ struct __align__(16) QCtl {
   Item item[NI];
   Bar ready[NI], taken[NI], qfull, qempty;
   Bar kfull[S::NK], kseen[S::NK], kempty[S::NK], vfull[S::NV], vseen[S::NV], vempty[S::NV];
-  Bar sfull[2], dpfull, dsfull, ofull, done;
+  Bar sfull[2], sread[2], dpfull[2], dsfull[2], ofull, done;
   uint32_t taddr;
   int err;
 };
@@ -567,8 +567,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < NI; ++i) bar_init(&C.ready[i], 1), bar_init(&C.taken[i], THREADS / 32 - 1);
     for (int i = 0; i < NK; ++i) bar_init(&C.kfull[i], 1), bar_init(&C.kseen[i], 1), bar_init(&C.kempty[i], 1);
     for (int i = 0; i < NV; ++i) bar_init(&C.vfull[i], 1), bar_init(&C.vseen[i], 1), bar_init(&C.vempty[i], 1);
-    bar_init(&C.qfull, 1), bar_init(&C.qempty, 1), bar_init(&C.sfull[0], 1), bar_init(&C.sfull[1], 1);
-    bar_init(&C.dpfull, 1), bar_init(&C.dsfull, 8), bar_init(&C.ofull, 1), bar_init(&C.done, 1);
+    for (int i = 0; i < 2; ++i)
+      bar_init(&C.sfull[i], 1), bar_init(&C.sread[i], 8), bar_init(&C.dpfull[i], 1), bar_init(&C.dsfull[i], 8);
+    bar_init(&C.qfull, 1), bar_init(&C.qempty, 1), bar_init(&C.ofull, 1), bar_init(&C.done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     C.err = 0;
@@ -580,15 +581,36 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   __syncthreads();
   after_sync();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, C.taddr, 0), tp = tmem + 256, to = tmem + 384;   // S of unit u at 128 (u % 2), dS over it
+  const uint32_t tmem = __shfl_sync(0xffffffffu, C.taddr, 0), to = tmem + 384;
+  // Three places of 128 columns in turn: S of a unit; dP of the next one there as soon as S has been read;
+  // dS over that dP; and then S of the unit after it.
+  const auto s_at = [&](int u) { return tmem + 128 * (u % 3); };
+  const auto dp_at = [&](int u) { return tmem + 128 * ((u + 2) % 3); };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // --- the walk, and the copies
       Walk w = walk_start(P, BLK, P.q_heads, 0, lane);
-      int u = 0, items = 0, asked_v = 0;
+      int u = 0, asked_v = 0, items = 0;
       bool ok = true;
+      // of unit u: the values' place is free before the keys'
+      const auto copy_unit = [&](int kv, int row) {
+        if (u >= NV) ok = wait_warp(&C.vempty[u % NV], (uint32_t)(u / NV - 1) & 1, err);
+        if (!ok) return;
+        if (lane == 0) {
+          expect(&C.vfull[u % NV], TILE);
+          copy_tile<D>(sv + (u % NV) * TILE, &map_v, kv, row, &C.vfull[u % NV]);
+        }
+        asked_v = u + 1;
+        if (u >= NK) ok = wait_warp(&C.kempty[u % NK], (uint32_t)(u / NK - 1) & 1, err);
+        if (!ok) return;
+        if (lane == 0) {
+          expect(&C.kfull[u % NK], TILE);
+          copy_tile<D>(sk + (u % NK) * TILE, &map_k, kv, row, &C.kfull[u % NK]);
+        }
+        ++u;
+      };
       for (int it = 0; ok; ++it) {
         Seq s;
         int token, slot;
@@ -601,7 +623,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           arrive(&C.ready[it % NI]);
         }
         if (!on) break;
-        if (items) ok = wait_warp(&C.qempty, (uint32_t)(items - 1) & 1, err);
+        // the first unit's before the queries, which the item before needs longer
+        const int kv = I.head / P.group;
+        copy_unit(kv, I.first + BLK * I.lo);
+        if (ok && items) ok = wait_warp(&C.qempty, (uint32_t)(items - 1) & 1, err);
         if (!ok) break;
         if (lane == 0) {
           expect(&C.qfull, 2 * TILE);
@@ -609,23 +634,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           copy_tile<D>(sg, &map_g, I.head, I.first + I.token, &C.qfull);
         }
         ++items;
-        const int kv = I.head / P.group;
-        for (int j = I.lo; j < I.hi; ++j) {
-          if (u >= NK) ok = wait_warp(&C.kempty[u % NK], (uint32_t)(u / NK - 1) & 1, err);
-          if (!ok) break;
-          if (lane == 0) {
-            expect(&C.kfull[u % NK], TILE);
-            copy_tile<D>(sk + (u % NK) * TILE, &map_k, kv, I.first + BLK * j, &C.kfull[u % NK]);
-          }
-          ++u;
-          if (u > NV) ok = wait_warp(&C.vempty[(u - 1) % NV], (uint32_t)((u - 1) / NV - 1) & 1, err);
-          if (!ok) break;
-          if (lane == 0) {
-            expect(&C.vfull[(u - 1) % NV], TILE);
-            copy_tile<D>(sv + ((u - 1) % NV) * TILE, &map_v, kv, I.first + BLK * j, &C.vfull[(u - 1) % NV]);
-          }
-          asked_v = u;
-        }
+        for (int j = I.lo + 1; j < I.hi && ok; ++j) copy_unit(kv, I.first + BLK * j);
       }
       // what was asked for lands before the block ends, also when the others have stopped
       if (lane == 0) {
@@ -636,7 +645,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      // --- products: S two units ahead, dP one
+      // --- products: S two units ahead, dP one, as soon as S of the unit before it has been read
       int u = 0;
       bool ok = true;
       const auto scores = [&](int x) {
@@ -644,14 +653,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) return;
         after_sync();
         if (elect()) {
-          mma_dims<D>(tmem + 128 * (x & 1), sq, sk + (x % NK) * TILE);
+          mma_dims<D>(s_at(x), sq, sk + (x % NK) * TILE);
           commit(&C.sfull[x & 1]);
         }
         __syncwarp();
       };
       const auto products = [&](int x) {   // by the lane that issues
-        mma_dims<D>(tp, sg, sv + (x % NV) * TILE);
-        commit(&C.dpfull);
+        mma_dims<D>(dp_at(x), sg, sv + (x % NV) * TILE);
+        commit(&C.dpfull[x & 1]);
         commit(&C.vempty[x % NV]);
       };
       for (int it = 0; ok; ++it) {
@@ -673,23 +682,27 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (n > 1) scores(u + 1);
         for (int x = 0; x < n && ok; ++x, ++u) {
-          const bool more = x + 1 < n;
-          if (more) ok = wait_warp(&C.vseen[(u + 1) % NV], (uint32_t)((u + 1) / NV) & 1, err);
-          if (ok) ok = wait_warp(&C.dsfull, (uint32_t)u & 1, err);
+          if (x + 1 < n) {
+            ok = wait_warp(&C.vseen[(u + 1) % NV], (uint32_t)((u + 1) / NV) & 1, err);
+            if (ok) ok = wait_warp(&C.sread[u & 1], (uint32_t)(u >> 1) & 1, err);
+            if (!ok) break;
+            after_sync();
+            if (elect()) {
+              products(u + 1);
+              if (x + 2 == n) commit(&C.qempty);
+            }
+            __syncwarp();
+          }
+          ok = wait_warp(&C.dsfull[u & 1], (uint32_t)(u >> 1) & 1, err);
           if (!ok) break;
           after_sync();
           if (elect()) {
-            if (more) products(u + 1);
-            mma_rows<D>(to, tmem + 128 * (u & 1), sk + (u % NK) * TILE, x != 0, 32);
+            mma_rows<D>(to, dp_at(u), sk + (u % NK) * TILE, x != 0, 32);
             commit(&C.kempty[u % NK]);
             if (x + 1 == n) commit(&C.ofull);
           }
           __syncwarp();
           if (x + 2 < n) scores(u + 2);
-          if (x + 2 == n) {
-            if (elect()) commit(&C.qempty);
-            __syncwarp();
-          }
         }
       }
       // nothing is in flight when the block ends
@@ -741,12 +754,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = wait_warp(&C.sfull[u & 1], (uint32_t)(u >> 1) & 1, err);
         if (!ok) break;
         after_sync();
-        const uint32_t ts = tmem + 128 * (u & 1) + mine;
+        const uint32_t ts = s_at(u) + mine, tp = dp_at(u) + mine;
         uint32_t p[64];
         tmem_ld32(p, ts);
         tmem_ld32(p + 32, ts + 32);
         tmem_wait_ld();
         pin<64>(p);
+        before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(&C.sread[u & 1]);
         const int k0 = BLK * j;
         if (k0 + BLK - 1 > I.token || (P.window && k0 <= I.token + BLK - 1 - P.window)) {
           // the query sees key c of the half if c <= hi and, in a window, c > hi - window
@@ -765,12 +781,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           unpair(fma2(pair(__uint_as_float(p[c]), __uint_as_float(p[c + 1])), a, nl2), y0, y1);
           p[c] = __float_as_uint(ex2f(y0)), p[c + 1] = __float_as_uint(ex2f(y1));
         }
-        ok = wait_warp(&C.dpfull, (uint32_t)u & 1, err);
+        ok = wait_warp(&C.dpfull[u & 1], (uint32_t)(u >> 1) & 1, err);
         if (!ok) break;
         after_sync();
         uint32_t d[64];
-        tmem_ld32(d, tp + mine);
-        tmem_ld32(d + 32, tp + mine + 32);
+        tmem_ld32(d, tp);
+        tmem_ld32(d + 32, tp + 32);
         tmem_wait_ld();
         pin<64>(d);
 #pragma unroll
@@ -784,12 +800,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         pair(__uint_as_float(p[e]), __uint_as_float(p[e + 1]))), y0, y1);
             z[k] = pack_bf2(y0, y1);
           }
-          tmem_st16(ts + 16 * c, z);
+          tmem_st16(tp + 16 * c, z);
         }
         tmem_wait_st();
         before_sync();
         __syncwarp();
-        if (lane == 0) arrive(&C.dsfull);
+        if (lane == 0) arrive(&C.dsfull[u & 1]);
       }
       if (!ok) break;
       ok = wait_warp(&C.ofull, (uint32_t)it & 1, err);
