@@ -187,6 +187,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int* err = &C.err;
   const Prompts& P = A.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the queries' side needs only what the rows' kernel left
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (tid == 0) {
     for (int i = 0; i < NI; ++i) bar_init(&C.ready[i], 1), bar_init(&C.taken[i], THREADS / 32 - 1);
@@ -836,6 +838,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int x = token + warp; x < min(token + BLK, s.len); x += THREADS / 32)
         fill_rows(A.gq, (size_t)(s.first + x) * P.q_heads + slot, D, lane, 32, NAN);
   }
+  // this grid ends only after the one before it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 static long long most_tiles(int B, int N) { return N / BLK + (B < N ? B : N); }
@@ -865,11 +869,19 @@ static sv_status launch(const BwdArgs& A, const void* q, long long qs, const voi
   const long long tiles = most_tiles(P.B, P.N), nk = tiles * P.kv_heads * A.split, nq = tiles * P.q_heads;
   prompt_grad_kv_kernel<D><<<(unsigned)(nk < sms ? nk : sms), THREADS, kv_smem<D>(), st>>>(A, mq, mk, mv, mg);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  if (A.split > 1) {
-    prompt_sum_kernel<D><<<(unsigned)(((long long)P.N * P.kv_heads * D / 4 + 255) / 256), 256, 0, st>>>(A);
-    if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  }
-  prompt_grad_q_kernel<D><<<(unsigned)(nq < sms ? nq : sms), THREADS, q_smem<D>(), st>>>(A, mq, mk, mv, mg);
+  // beside the keys' side: in SMs that it has left, or never took
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(nq < sms ? nq : sms));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = q_smem<D>();
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, prompt_grad_q_kernel<D>, A, mq, mk, mv, mg) != cudaSuccess) return SV_ERR_CUDA;
+  if (A.split > 1) prompt_sum_kernel<D><<<(unsigned)(((long long)P.N * P.kv_heads * D / 4 + 255) / 256), 256, 0, st>>>(A);
   return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
