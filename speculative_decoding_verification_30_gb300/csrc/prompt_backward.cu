@@ -10,17 +10,20 @@
 // grad_q += dS K. Seven products in the place of the five that one kernel would need, but no
 // atomics; and no fp32 sums in memory, except where there are fewer tiles of keys than SMs: there
 // pieces of a group's heads are summed through memory, in their order.
-// Measured: 12 documents of up to 2,500 tokens, 32 heads on 8 of 128: 750 us, 808 TFLOP/s of the five
-// products; rows 46 us (5,700 GB/s), keys' side 366 us (tensor pipe some 63% active), queries' side 302 us
-// (some 57%). The keys' side is near what shared memory gives: a product of two tiles there reads 64 KB, all that
-// it can in the product's 512 clocks, and 64 KB of tiles come in for each unit. Queries have three stages on
-// the keys' side: with two, S waits for its copy (788 us); waiting for them before P^T dO is issued,
-// 879 us. A unit of the queries' side takes 2,290 clocks, its products 1,650: the warp that issues them
-// waits for copies in between. One wait for a unit's values and the next one's keys asks for a key
-// stage that is not free yet: its kernel 377 us. A lane writing 64 bytes of its own row on the way
-// out: 774 us. Blocks as in the forward kernel: warp 0 walks the work and copies, 1 issues the
-// products, 2-3 see to what lies behind a sequence's end, 4-11 have the rows, each half of them 64
-// columns. Every wait is bounded; a block that gives up writes NaN to all of its rows.
+// Measured: 12 documents of up to 2,500 tokens, 32 heads on 8 of 128: 738 us, 821 TFLOP/s of the five
+// products; rows 46 us (5,700 GB/s), keys' side 367 us (tensor pipe some 63% active), queries' side 295 us
+// (some 58%), which begins where the keys' side ends (752 us one after the other; the keys' side
+// beginning beside the rows in the same way, 751 us). The keys' side is near what shared memory gives:
+// a product of two tiles there reads 64 KB, all that it can in the product's 512 clocks, and 64 KB of
+// tiles come in for each unit. Queries have three stages on the keys' side: with two, S waits for its
+// copy (788 us when all took 777); waiting for them before P^T dO is issued, 879 us. A unit of the
+// queries' side takes some 2,200 clocks, its products 1,650 and its rows, from S to dS, 1,450. dP asked for only
+// when dS of the unit before it is there: its kernel 302 us; one wait for a unit's values and the next
+// one's keys, which asks for a key stage that is not free yet, 377 us. A lane writing 64 bytes of its
+// own row on the way out: 774 us when all took 746.
+// Blocks as in the forward kernel: warp 0 walks the work and copies, 1 issues the products, 2-3 see to
+// what lies behind a sequence's end, 4-11 have the rows, each half of them 64 columns. Every wait is
+// bounded; a block that gives up writes NaN to all of its rows.
 #include "prompt_common.cuh"
 
 namespace svpr {
